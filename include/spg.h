@@ -113,6 +113,8 @@ typedef enum { SPG_F16 = 0, SPG_BF16 = 1, SPG_I8 = 2 } spg_dtype;
 #define SPG_DEVERR_SEQ_LEN 2 /* seq_lens[b] < 0 or > max_pages_per_seq * page_size */
 #define SPG_DEVERR_SEL 4     /* sel entry outside [0, P_b) or sel_cnt outside [0, n_sel] */
 #define SPG_DEVERR_TIMEOUT 8 /* a bounded wait for an asynchronous copy ran out */
+#define SPG_DEVERR_Q_START 16 /* q_start not ascending within [0, total_q], or a sequence
+                                 with more new tokens than seq_lens[b] */
 
 typedef struct spg_params {
   int32_t batch;             /* B >= 1 */
@@ -165,7 +167,8 @@ const char* spg_status_str(int32_t status);
 spg_status spg_validate(const spg_params* p);
 
 /* Bytes of device workspace every entry point needs for these parameters
- * (the same figure for all of them).  Host only. */
+ * (the same figure for all of them, but for paged_chunk_attention, see
+ * spg_chunk_workspace_size).  Host only. */
 spg_status spg_workspace_size(const spg_params* p, size_t* bytes);
 
 /* Metadata maintenance (Quest 关键性估计算法, insert-time update; SALS low-rank
@@ -274,6 +277,135 @@ spg_status dense_decode_attention(const spg_params* p, const void* q, const void
                                   const void* v_pool, const void* k_scale, const void* v_scale,
                                   const int32_t* page_table, const int32_t* seq_lens, float* out,
                                   float* lse, void* ws, size_t ws_bytes, spg_stream_t stream);
+
+/* ---- chunks of new tokens over the paged cache -------------------------------
+ * What a serving loop does around the decode steps: put the tokens of a
+ * prompt (or a few drafted tokens, or one token per sequence) into the cache,
+ * attend them, keep account of the attention weight each cached token
+ * received, and evict the light ones.
+ *
+ * Chunks are ragged: sequence b's new tokens are rows q_start[b] ..
+ * q_start[b+1] of the row-per-token tensors, and seq_lens[b] counts them, so
+ * that with n_b = q_start[b+1] - q_start[b] row q_start[b] + i stands at
+ * cache position seq_lens[b] - n_b + i.  n_b may be 0.  Rows past q_start[B]
+ * are neither read nor written.
+ *   q_start      [B+1] int32           ascending, within [0, total_q]
+ *   q            [total_q][Hq][d]      q_dtype
+ * A sequence whose q_start or seq_lens entry is bad (SPG_DEVERR_Q_START,
+ * SPG_DEVERR_SEQ_LEN) is skipped, a bad page is skipped
+ * (SPG_DEVERR_PAGE_ID): its tokens take no part and are not written.
+ * The selector fields of spg_params play no part here.  Cached values of
+ * tokens below seq_lens must be finite; slots past it may hold anything. */
+
+/* Workspace bytes that are enough for every entry point of this header with
+ * these parameters and chunks of up to total_q rows (at least
+ * spg_workspace_size).  Host only. */
+spg_status spg_chunk_workspace_size(const spg_params* p, int32_t total_q, size_t* bytes);
+
+typedef enum { SPG_ROPE_HALF = 0, SPG_ROPE_INTERLEAVED = 1 } spg_rope_layout;
+typedef enum {
+  SPG_ROPE_PLAIN = 0,  /* angle of pair i at position t: t * base^(-2i / rot_dim) */
+  SPG_ROPE_LINEAR = 1, /* positions divided by factor */
+  SPG_ROPE_NTK = 2,    /* base * factor^(rot_dim / (rot_dim - 2)) in place of base */
+  SPG_ROPE_YARN = 3    /* by parts: pairs that turn more than 32 times over orig_len
+                          positions as plain, fewer than once as linear, a linear ramp
+                          over the pair index between; q and k also times
+                          0.1 ln(factor) + 1 */
+} spg_rope_scaling;
+
+typedef struct spg_rope {
+  int32_t rot_dim;  /* leading channels that turn: a multiple of 16 up to head_dim; 0 => head_dim */
+  int32_t layout;   /* spg_rope_layout: pairs (i, i + rot_dim/2), or (2i, 2i+1) */
+  int32_t scaling;  /* spg_rope_scaling */
+  int32_t orig_len; /* positions the frequencies were made for (YARN only, >= 1) */
+  double base;      /* > 1, finite */
+  double factor;    /* >= 1, finite; ignored by PLAIN */
+} spg_rope;
+
+/* The angle per position of every pair (rot_dim / 2 doubles) and the factor
+ * on the rotated channels (1 unless YARN).  Host only. */
+spg_status spg_rope_freqs(const spg_rope* rope, int32_t head_dim, double* inv_freq, double* mscale);
+
+/* Rotary positions of a chunk, and its keys and values into the cache.  Per
+ * row: q_out = rotated q; the rotated k and v go to the row's cache slot,
+ * converted to kv_dtype (int8: codes rint(x / s) in [-127, 127] with the fp16
+ * scale s = absmax / 127 of the token and head, 1 for an all-zero row).
+ *   q, k, v      q_dtype, [total_q] rows of [Hq | Hkv | Hkv][d], the rows
+ *                q_stride, k_stride, v_stride elements apart (multiples of
+ *                8, so that the three may be slices of one projection's
+ *                output)
+ *   q_out        [total_q][Hq][d], may be q itself when q_stride is Hq * d;
+ *                q and q_out may both be NULL
+ *   positions    [total_q] int32 rotation angles' positions, or NULL for the
+ *                cache positions (an evicted cache is shorter than the text
+ *                it stands for)
+ *   rope         NULL leaves q and k as they are
+ * The angles are exact to 2^-32 of a turn at any position.  Page metadata is
+ * not touched: call sparse_page_meta_update (rebuild == 0 after one token per
+ * sequence, else rebuild != 0) before the next selection, or let
+ * sparse_decode_step append its one token. */
+spg_status paged_rope_append(const spg_params* p, const spg_rope* rope, int32_t total_q,
+                             const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const int32_t* q_start,
+                             const int32_t* positions, const int32_t* page_table,
+                             const int32_t* seq_lens, void* k_pool, void* v_pool, void* k_scale,
+                             void* v_scale, void* q_out, void* ws, size_t ws_bytes,
+                             spg_stream_t stream);
+
+/* Causal attention of a chunk over the cache its keys and values are already
+ * in: row i of sequence b attends the tokens t <= seq_lens[b] - n_b + i.
+ *   out          [total_q][Hq][d] q_dtype
+ *   lse          [total_q][Hq] fp32 natural-log log-sum-exp (may be NULL)
+ * Logits, softmax statistics and sums in fp32; the probabilities enter the
+ * P V product rounded to the 16-bit type (int8 V scales, at most 255, folded
+ * in first).  Needs spg_chunk_workspace_size bytes. */
+spg_status paged_chunk_attention(const spg_params* p, int32_t total_q, const void* q,
+                                 const int32_t* q_start, const void* k_pool, const void* v_pool,
+                                 const void* k_scale, const void* v_scale,
+                                 const int32_t* page_table, const int32_t* seq_lens, void* out,
+                                 float* lse, void* ws, size_t ws_bytes, spg_stream_t stream);
+
+/* Attention weight received by every cached token (StreamingLLM/H2O heavy
+ * hitters): per (batch, kv-head), over the group's query heads and the
+ * chunk's rows,
+ *   mass_out[t] = decay * mass_in[t] (0 for the chunk's own tokens)
+ *                 + sum exp(scale q.k_t - lse),  t < seq_lens[b]
+ * with the lse paged_chunk_attention (or, for one token per sequence,
+ * dense_decode_attention) returned; rows with lse = -inf add nothing.
+ *   mass_in      [B][Hkv][MP * S] fp32, or NULL for zeros; not read when
+ *                decay is 0
+ *   mass_out     the same shape, may be mass_in; entries past seq_lens[b]
+ *                are left as they were
+ *   decay        in [0, 1] */
+spg_status paged_attention_mass(const spg_params* p, int32_t total_q, const void* q,
+                                const int32_t* q_start, const void* k_pool, const void* k_scale,
+                                const int32_t* page_table, const int32_t* seq_lens,
+                                const float* lse, const float* mass_in, float* mass_out,
+                                float decay, void* ws, size_t ws_bytes, spg_stream_t stream);
+
+/* Evicts the light tokens of every (batch, kv-head): of sequence b keeps its
+ * first n_sink tokens, its last n_recent, and the heaviest others (lower
+ * position first among equals, NaN lightest) up to keep tokens in all, and
+ * moves the kept ones to the front in their order: keys, values, scales and
+ * mass.  Sequences of at most keep tokens keep everything.
+ *   mass         [B][Hkv][MP * S] fp32
+ *   dst_page_table [B][MP] int32: pages the kept tokens are moved to, none of
+ *                them in use by any sequence of page_table, or NULL to
+ *                compact within page_table (pages past ceil(new_lens / S)
+ *                are then free); no two sequences may share a page that is
+ *                written
+ *   kept         [B][Hkv][keep] int32 positions kept, ascending, then -1
+ *   new_lens     [B] int32, min(seq_lens[b], keep); not seq_lens itself
+ *   mass_out     [B][Hkv][MP * S] fp32: the kept tokens' masses in their new
+ *                order, entries past new_lens left as they were; may be mass
+ * n_sink, n_recent >= 0, keep >= 1, n_sink + n_recent <= keep.  Page
+ * metadata has to be rebuilt afterwards (sparse_page_meta_update). */
+spg_status paged_cache_evict(const spg_params* p, const float* mass, int32_t keep, int32_t n_sink,
+                             int32_t n_recent, void* k_pool, void* v_pool, void* k_scale,
+                             void* v_scale, const int32_t* page_table,
+                             const int32_t* dst_page_table, const int32_t* seq_lens, int32_t* kept,
+                             int32_t* new_lens, float* mass_out, void* ws, size_t ws_bytes,
+                             spg_stream_t stream);
 
 /* Bytes of the library-owned scratch array behind
  * sparse_decode_attention_noalloc (16 MiB).  A call needs

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspg.so")
@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libspg.so")
 SPG_OK, SPG_EINVAL, SPG_EUNSUPPORTED, SPG_ECUDA, SPG_EWORKSPACE = 0, 1, 2, 3, 4
 SEL_QUEST, SEL_SKETCH_INT4, SEL_ALL, SEL_PROBE = 0, 1, 2, 3
 F16, BF16, I8 = 0, 1, 2
-DEVERR_PAGE_ID, DEVERR_SEQ_LEN, DEVERR_SEL, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_PAGE_ID, DEVERR_SEQ_LEN, DEVERR_SEL, DEVERR_TIMEOUT, DEVERR_Q_START = 1, 2, 4, 8, 16
 
 _DTYPES = {"f16": F16, "bf16": BF16, "i8": I8}
 _SELECTORS = {"quest": SEL_QUEST, "sketch": SEL_SKETCH_INT4, "all": SEL_ALL, "probe": SEL_PROBE}
@@ -71,6 +71,28 @@ def make_params(batch, num_q_heads, num_kv_heads, head_dim, page_size, num_phys_
                       sketch_dim, softmax_scale, top_p, min_pages, n_probe)
 
 
+class spg_rope(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", c_int32),
+        ("layout", c_int32),
+        ("scaling", c_int32),
+        ("orig_len", c_int32),
+        ("base", c_double),
+        ("factor", c_double),
+    ]
+
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def make_rope(rot_dim=0, layout="half", base=10000.0, scaling="none", factor=1.0,
+              orig_len=1) -> spg_rope:
+    lay = _ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+    sc = _ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    return spg_rope(int(rot_dim), lay, sc, int(orig_len), float(base), float(factor))
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -94,6 +116,17 @@ def _load():
         "sparse_decode_step": (
             [P, v, v, v, v, v, v, v, v, v, v, v, v, v, v, v, v, c_size_t, v], c_int32),
         "sparse_page_sketch_dots": ([P, v, v, v, v, v, v, v, v, c_size_t, v], c_int32),
+        "spg_chunk_workspace_size": ([P, c_int32, POINTER(c_size_t)], c_int32),
+        "spg_rope_freqs": ([POINTER(spg_rope), c_int32, POINTER(c_double), POINTER(c_double)], c_int32),
+        "paged_rope_append": (
+            [P, POINTER(spg_rope), c_int32, v, c_int64, v, c_int64, v, c_int64, v, v, v, v, v, v, v, v, v, v,
+             c_size_t, v], c_int32),
+        "paged_chunk_attention": (
+            [P, c_int32, v, v, v, v, v, v, v, v, v, v, v, c_size_t, v], c_int32),
+        "paged_attention_mass": (
+            [P, c_int32, v, v, v, v, v, v, v, v, v, c_float, v, c_size_t, v], c_int32),
+        "paged_cache_evict": (
+            [P, v, c_int32, c_int32, c_int32, v, v, v, v, v, v, v, v, v, v, v, c_size_t, v], c_int32),
         "spg_step_kernel": ([P], c_char_p),
         "spg_prefer_dense": ([P, c_int32, c_float], c_int32),
         "spg_step_launches": ([P], c_int32),
@@ -260,6 +293,139 @@ def dense_decode_attention(p, q, k_pool, v_pool, k_scale, v_scale, page_table, s
         ctypes.byref(p), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
         _ptr(page_table), _ptr(seq_lens), _ptr(out), _ptr(lse), wp, wn, _stream(stream)),
         "dense_decode_attention")
+
+
+# ---- chunks of new tokens ----------------------------------------------------------
+_ELEM = {F16: "float16", BF16: "bfloat16", I8: "int8"}
+
+
+def _take(name, t, shape, dtype):
+    """Device pointer of a tensor that has to be contiguous, of this shape and type."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if str(t.dtype) != f"torch.{dtype}":
+        raise ValueError(f"{name}: {t.dtype}, expected torch.{dtype}")
+    return _ptr(t)
+
+
+def _take_rows(name, t, shape, dtype):
+    """Pointer and row stride of a tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if str(t.dtype) != f"torch.{dtype}":
+        raise ValueError(f"{name}: {t.dtype}, expected torch.{dtype}")
+    if not t.is_cuda:
+        raise ValueError("libspg takes device tensors")
+    if t.numel() and not t[0].is_contiguous():
+        raise ValueError(f"{name}: the heads of one token have to be contiguous")
+    n = shape[1] * shape[2]
+    return c_void_p(t.data_ptr()), int(t.stride(0)) if shape[0] > 1 else n
+
+
+def _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, q_start=None):
+    pool = (p.num_phys_pages, p.num_kv_heads, p.page_size, p.head_dim)
+    r = [_take("k_pool", k_pool, pool, _ELEM[p.kv_dtype]), _take("v_pool", v_pool, pool, _ELEM[p.kv_dtype]),
+         _take("k_scale", k_scale, pool[:3], "float16"), _take("v_scale", v_scale, pool[:3], "float16"),
+         _take("page_table", page_table, (p.batch, p.max_pages_per_seq), "int32"),
+         _take("seq_lens", seq_lens, (p.batch,), "int32"), _take("q_start", q_start, (p.batch + 1,), "int32")]
+    return r
+
+
+class _on:
+    """The device the workspace lives on made current, and the stream to launch on there."""
+
+    def __init__(self, ws, stream):
+        import torch
+
+        if ws is None:
+            raise ValueError("a workspace is needed")
+        self.guard = torch.cuda.device(ws.device) if ws.is_cuda else None
+        self.stream, self.ws = stream, ws
+
+    def __enter__(self):
+        if self.guard is None:
+            raise ValueError("libspg takes device tensors")
+        self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def spg_chunk_workspace_size(p: spg_params, total_q: int) -> int:
+    n = c_size_t(0)
+    _check(LIB.spg_chunk_workspace_size(ctypes.byref(p), int(total_q), ctypes.byref(n)),
+           "spg_chunk_workspace_size")
+    return n.value
+
+
+def spg_rope_freqs(rope: spg_rope, head_dim: int):
+    """(angle per position of every pair, factor on the rotated channels)."""
+    f, m = (c_double * max(head_dim, 2))(), c_double(0)
+    _check(LIB.spg_rope_freqs(ctypes.byref(rope), int(head_dim), f, ctypes.byref(m)), "spg_rope_freqs")
+    return list(f)[: (rope.rot_dim or head_dim) // 2], m.value
+
+
+def paged_rope_append(p, rope, q, k, v, q_start, page_table, seq_lens, k_pool, v_pool, k_scale=None,
+                      v_scale=None, q_out=None, positions=None, ws=None, stream=None):
+    T, d = k.shape[0], p.head_dim
+    qd = _ELEM[p.q_dtype]
+    qp, qs = _take_rows("q", q, (T, p.num_q_heads, d), qd)
+    kp, ks = _take_rows("k", k, (T, p.num_kv_heads, d), qd)
+    vp, vs = _take_rows("v", v, (T, p.num_kv_heads, d), qd)
+    kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table,
+                                                     seq_lens, q_start)
+    out = _take("q_out", q_out, (T, p.num_q_heads, d), qd)
+    pos = _take("positions", positions, (T,), "int32")
+    with _on(ws, stream) as s:
+        wp, wn = _ws(ws)
+        _check(LIB.paged_rope_append(
+            ctypes.byref(p), None if rope is None else ctypes.byref(rope), T, qp, qs, kp, ks, vp, vs, st, pos,
+            pt, sl, kpool, vpool, ksc, vsc, out, wp, wn, s), "paged_rope_append")
+
+
+def paged_chunk_attention(p, q, q_start, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, out,
+                          lse=None, ws=None, stream=None):
+    T, rows = q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim)
+    qp, op = _take("q", q, rows, _ELEM[p.q_dtype]), _take("out", out, rows, _ELEM[p.q_dtype])
+    lp = _take("lse", lse, rows[:2], "float32")
+    kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table,
+                                                     seq_lens, q_start)
+    with _on(ws, stream) as s:
+        wp, wn = _ws(ws)
+        _check(LIB.paged_chunk_attention(ctypes.byref(p), T, qp, st, kpool, vpool, ksc, vsc, pt, sl, op, lp, wp,
+                                         wn, s), "paged_chunk_attention")
+
+
+def paged_attention_mass(p, q, q_start, k_pool, k_scale, page_table, seq_lens, lse, mass_in, mass_out,
+                         decay=1.0, ws=None, stream=None):
+    T, rows = q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim)
+    m = (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size)
+    qp, lp = _take("q", q, rows, _ELEM[p.q_dtype]), _take("lse", lse, rows[:2], "float32")
+    mi, mo = _take("mass_in", mass_in, m, "float32"), _take("mass_out", mass_out, m, "float32")
+    kpool, _, ksc, _, pt, sl, st = _take_cache(p, k_pool, None, k_scale, None, page_table, seq_lens, q_start)
+    with _on(ws, stream) as s:
+        wp, wn = _ws(ws)
+        _check(LIB.paged_attention_mass(ctypes.byref(p), T, qp, st, kpool, ksc, pt, sl, lp, mi, mo, float(decay),
+                                        wp, wn, s), "paged_attention_mass")
+
+
+def paged_cache_evict(p, mass, keep, n_sink, n_recent, k_pool, v_pool, k_scale, v_scale, page_table,
+                      dst_page_table, seq_lens, kept, new_lens, mass_out, ws=None, stream=None):
+    kpool, vpool, ksc, vsc, pt, sl, _ = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens)
+    m = (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size)
+    mi, mo = _take("mass", mass, m, "float32"), _take("mass_out", mass_out, m, "float32")
+    dst = _take("dst_page_table", dst_page_table, (p.batch, p.max_pages_per_seq), "int32")
+    kp = _take("kept", kept, (p.batch, p.num_kv_heads, int(keep)), "int32")
+    nl = _take("new_lens", new_lens, (p.batch,), "int32")
+    with _on(ws, stream) as s:
+        wp, wn = _ws(ws)
+        _check(LIB.paged_cache_evict(ctypes.byref(p), mi, int(keep), int(n_sink), int(n_recent), kpool, vpool, ksc,
+                                     vsc, pt, dst, sl, kp, nl, mo, wp, wn, s), "paged_cache_evict")
 
 
 def spg_read_device_error(ws, stream=None) -> int:

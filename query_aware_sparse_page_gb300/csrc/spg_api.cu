@@ -396,6 +396,125 @@ spg_status sparse_page_sketch_dots(const spg_params* p, const void* q, const int
                                              reinterpret_cast<cudaStream_t>(stream)));
 }
 
+spg_status spg_chunk_workspace_size(const spg_params* p, int32_t total_q, size_t* bytes) {
+  const spg_status s = spg_validate(p);
+  if (s != SPG_OK) return s;
+  if (!bytes || total_q < 0) return SPG_EINVAL;
+  *bytes = spg::workspace_bytes(*p);
+  return SPG_OK;
+}
+
+spg_status spg_rope_freqs(const spg_rope* rope, int32_t head_dim, double* inv_freq, double* mscale) {
+  if (!rope || !inv_freq || !mscale || head_dim < 2) return SPG_EINVAL;
+  return spg::rope_freqs(*rope, head_dim, inv_freq, mscale) ? SPG_OK : SPG_EINVAL;
+}
+
+spg_status paged_rope_append(const spg_params* p, const spg_rope* rope, int32_t total_q,
+                             const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const int32_t* q_start,
+                             const int32_t* positions, const int32_t* page_table,
+                             const int32_t* seq_lens, void* k_pool, void* v_pool, void* k_scale,
+                             void* v_scale, void* q_out, void* ws, size_t ws_bytes,
+                             spg_stream_t stream) {
+  spg_status s = spg_validate(p);
+  if (s != SPG_OK) return s;
+  if (rope) {
+    double inv[64], m;  // head_dim / 2 <= 64 pairs
+    if (!spg::rope_freqs(*rope, p->head_dim, inv, &m)) return SPG_EINVAL;
+    if (rope->rot_dim % 16) return SPG_EUNSUPPORTED;  // whole 16-byte pieces of both halves
+  }
+  if (total_q < 0) return SPG_EINVAL;
+  if ((s = check_ws(p, ws, ws_bytes)) != SPG_OK) return s;
+  if (total_q == 0) return SPG_OK;
+  if (!ok_ptr(k) || !ok_ptr(v) || !ok_ptr(q_start) || !ok_ptr(page_table) || !ok_ptr(seq_lens) ||
+      !aligned16(positions) || !aligned16(q) || !aligned16(q_out) || (q == nullptr) != (q_out == nullptr))
+    return SPG_EINVAL;
+  const int64_t d = p->head_dim;
+  if (k_stride < p->num_kv_heads * d || v_stride < p->num_kv_heads * d || k_stride % 8 || v_stride % 8)
+    return SPG_EINVAL;
+  if (q && (q_stride < p->num_q_heads * d || q_stride % 8)) return SPG_EINVAL;
+  if (q && q == q_out && q_stride != p->num_q_heads * d) return SPG_EINVAL;
+  if ((s = check_kv(p, k_pool, v_pool, k_scale, v_scale)) != SPG_OK) return s;
+  const Workspace w = spg::carve_workspace(*p, ws);
+  spg::RopeRows r{};
+  r.q = q;
+  r.q_start = q_start;
+  r.page_table = page_table;
+  r.seq_lens = seq_lens;
+  r.total_q = total_q;
+  r.k = k;
+  r.v = v;
+  r.q_stride = q_stride;
+  r.k_stride = k_stride;
+  r.v_stride = v_stride;
+  r.positions = positions;
+  r.q_out = q_out;
+  return cuda_status(spg::launch_rope_append(*p, rope, r, k_pool, v_pool, k_scale, v_scale, w.err,
+                                             reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spg_status paged_chunk_attention(const spg_params* p, int32_t total_q, const void* q,
+                                 const int32_t* q_start, const void* k_pool, const void* v_pool,
+                                 const void* k_scale, const void* v_scale,
+                                 const int32_t* page_table, const int32_t* seq_lens, void* out,
+                                 float* lse, void* ws, size_t ws_bytes, spg_stream_t stream) {
+  size_t need = 0;
+  spg_status s = spg_chunk_workspace_size(p, total_q, &need);
+  if (s != SPG_OK) return s;
+  if (!ok_ptr(ws)) return SPG_EINVAL;
+  if (ws_bytes < need) return SPG_EWORKSPACE;
+  if (total_q == 0) return SPG_OK;
+  if (!ok_ptr(q) || !ok_ptr(q_start) || !ok_ptr(page_table) || !ok_ptr(seq_lens) || !ok_ptr(out) ||
+      !aligned16(lse))
+    return SPG_EINVAL;
+  if ((s = check_kv(p, k_pool, v_pool, k_scale, v_scale)) != SPG_OK) return s;
+  const Workspace w = spg::carve_workspace(*p, ws);
+  const spg::ChunkRows r{q, q_start, page_table, seq_lens, total_q};
+  return cuda_status(spg::launch_chunk(*p, r, k_pool, v_pool, k_scale, v_scale, out, lse, w,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spg_status paged_attention_mass(const spg_params* p, int32_t total_q, const void* q,
+                                const int32_t* q_start, const void* k_pool, const void* k_scale,
+                                const int32_t* page_table, const int32_t* seq_lens,
+                                const float* lse, const float* mass_in, float* mass_out,
+                                float decay, void* ws, size_t ws_bytes, spg_stream_t stream) {
+  spg_status s = spg_validate(p);
+  if (s != SPG_OK) return s;
+  if (total_q < 0 || !(decay >= 0.f && decay <= 1.f)) return SPG_EINVAL;
+  if ((s = check_ws(p, ws, ws_bytes)) != SPG_OK) return s;
+  if (!ok_ptr(q_start) || !ok_ptr(page_table) || !ok_ptr(seq_lens) || !ok_ptr(k_pool) ||
+      !ok_ptr(mass_out) || !aligned16(mass_in) || (total_q > 0 && (!ok_ptr(q) || !ok_ptr(lse))))
+    return SPG_EINVAL;
+  if (p->kv_dtype == SPG_I8 && !ok_ptr(k_scale)) return SPG_EINVAL;
+  const Workspace w = spg::carve_workspace(*p, ws);
+  const spg::ChunkRows r{q, q_start, page_table, seq_lens, total_q};
+  return cuda_status(spg::launch_mass(*p, r, k_pool, k_scale, lse, mass_in, mass_out, decay, w,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spg_status paged_cache_evict(const spg_params* p, const float* mass, int32_t keep, int32_t n_sink,
+                             int32_t n_recent, void* k_pool, void* v_pool, void* k_scale,
+                             void* v_scale, const int32_t* page_table,
+                             const int32_t* dst_page_table, const int32_t* seq_lens, int32_t* kept,
+                             int32_t* new_lens, float* mass_out, void* ws, size_t ws_bytes,
+                             spg_stream_t stream) {
+  spg_status s = spg_validate(p);
+  if (s != SPG_OK) return s;
+  if (keep < 1 || n_sink < 0 || n_recent < 0 || static_cast<int64_t>(n_sink) + n_recent > keep)
+    return SPG_EINVAL;
+  if ((s = check_ws(p, ws, ws_bytes)) != SPG_OK) return s;
+  if (!ok_ptr(mass) || !ok_ptr(mass_out) || !ok_ptr(page_table) || !aligned16(dst_page_table) ||
+      !ok_ptr(seq_lens) || !ok_ptr(kept) || !ok_ptr(new_lens) || new_lens == seq_lens)
+    return SPG_EINVAL;
+  if ((s = check_kv(p, k_pool, v_pool, k_scale, v_scale)) != SPG_OK) return s;
+  const Workspace w = spg::carve_workspace(*p, ws);
+  return cuda_status(spg::launch_evict(*p, mass, keep, n_sink, n_recent, k_pool, v_pool, k_scale,
+                                       v_scale, page_table, dst_page_table, seq_lens, kept,
+                                       new_lens, mass_out, w.err,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int32_t spg_prefer_dense(const spg_params* p, int32_t max_seq_len, float ratio) {
   if (spg_validate(p) != SPG_OK || p->selector == SPG_SEL_ALL || max_seq_len < 0) return 0;
   if (!(ratio > 0.f)) ratio = SPG_DENSE_BYPASS_RATIO;

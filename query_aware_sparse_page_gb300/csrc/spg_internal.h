@@ -94,4 +94,39 @@ cudaError_t launch_fused(const spg_params& p, const void* q, const void* k_pool,
                          int32_t* sel, int32_t* sel_cnt, float* out, float* lse, int append,
                          const Workspace& ws, cudaStream_t stream);
 
+// ---- chunks of new tokens (spg_rope.cu, spg_chunk.cu, spg_evict.cu) ------------
+
+// A ragged chunk: rows of q and where they stand.
+struct ChunkRows {
+  const void* q;
+  const int32_t *q_start, *page_table, *seq_lens;
+  int total_q;
+};
+struct RopeRows : ChunkRows {
+  const void *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  const int32_t* positions;
+  void* q_out;
+};
+
+// Angle per position of every pair and the factor on the rotated channels;
+// false when the parameters are out of range.
+bool rope_freqs(const spg_rope& rope, int head_dim, double* inv_freq, double* mscale);
+
+cudaError_t launch_rope_append(const spg_params& p, const spg_rope* rope, const RopeRows& r,
+                               void* k_pool, void* v_pool, void* k_scale, void* v_scale,
+                               int32_t* err, cudaStream_t stream);
+cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_pool,
+                         const void* v_pool, const void* k_scale, const void* v_scale, void* out,
+                         float* lse, const Workspace& ws, cudaStream_t stream);
+cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_pool,
+                        const void* k_scale, const float* lse, const float* mass_in,
+                        float* mass_out, float decay, const Workspace& ws, cudaStream_t stream);
+// dst_table NULL (or page_table itself): compact within the sequences' pages
+cudaError_t launch_evict(const spg_params& p, const float* mass, int keep, int n_sink, int n_recent,
+                         void* k_pool, void* v_pool, void* k_scale, void* v_scale,
+                         const int32_t* page_table, const int32_t* dst_table,
+                         const int32_t* seq_lens, int32_t* kept, int32_t* new_lens,
+                         float* mass_out, int32_t* err, cudaStream_t stream);
+
 }  // namespace spg
