@@ -400,7 +400,7 @@ spg_status spg_chunk_workspace_size(const spg_params* p, int32_t total_q, size_t
   const spg_status s = spg_validate(p);
   if (s != SPG_OK) return s;
   if (!bytes || total_q < 0) return SPG_EINVAL;
-  *bytes = spg::workspace_bytes(*p);
+  *bytes = spg::chunk_workspace_bytes(*p, total_q);
   return SPG_OK;
 }
 
@@ -468,9 +468,8 @@ spg_status paged_chunk_attention(const spg_params* p, int32_t total_q, const voi
       !aligned16(lse))
     return SPG_EINVAL;
   if ((s = check_kv(p, k_pool, v_pool, k_scale, v_scale)) != SPG_OK) return s;
-  const Workspace w = spg::carve_workspace(*p, ws);
   const spg::ChunkRows r{q, q_start, page_table, seq_lens, total_q};
-  return cuda_status(spg::launch_chunk(*p, r, k_pool, v_pool, k_scale, v_scale, out, lse, w,
+  return cuda_status(spg::launch_chunk(*p, r, k_pool, v_pool, k_scale, v_scale, out, lse, ws,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 

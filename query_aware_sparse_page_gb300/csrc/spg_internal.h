@@ -94,7 +94,7 @@ cudaError_t launch_fused(const spg_params& p, const void* q, const void* k_pool,
                          int32_t* sel, int32_t* sel_cnt, float* out, float* lse, int append,
                          const Workspace& ws, cudaStream_t stream);
 
-// ---- chunks of new tokens (spg_rope.cu, spg_chunk.cu, spg_evict.cu) ------------
+// ---- chunks of new tokens (spg_rope.cu, spg_chunk.cu, spg_mass.cu, spg_evict.cu) ------------
 
 // A ragged chunk: rows of q and where they stand.
 struct ChunkRows {
@@ -118,7 +118,9 @@ cudaError_t launch_rope_append(const spg_params& p, const spg_rope* rope, const 
                                int32_t* err, cudaStream_t stream);
 cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_pool,
                          const void* v_pool, const void* k_scale, const void* v_scale, void* out,
-                         float* lse, const Workspace& ws, cudaStream_t stream);
+                         float* lse, void* ws, cudaStream_t stream);
+// the whole workspace of a chunk of total_q rows: the common one, then launch_chunk's
+size_t chunk_workspace_bytes(const spg_params& p, int total_q);
 cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_pool,
                         const void* k_scale, const float* lse, const float* mass_in,
                         float* mass_out, float decay, const Workspace& ws, cudaStream_t stream);
