@@ -63,7 +63,7 @@ struct ChunkArgs {
   void* out;
   float* lse;
   int32_t *err, *counters;
-  float* part;  // [2 * CTAs][part_rows][D + 2]
+  float* part;  // [2 * CTAs][D + 2][part_rows]: O by channel, then m and l, so that a warp's rows are neighbours
   int B, Hkv, G, S, MP, n_phys, total_q, part_rows;
   float scale_log2;
 };
@@ -240,39 +240,59 @@ struct Kernel {
   using Lay = Layout<D, I8>;
   static constexpr int KST = Lay::KST, VST = Lay::VST, NH = Lay::NH;
   using M = Misc<KST, VST, I8>;
-  static constexpr int kWarps = I8 ? 13 : 11, kThreads = kWarps * 32;
-  static constexpr int kMmaWarp = 8, kFillWarp = 9;  // 16-bit: K warp, V warp; int8: four converting warps
+  // warpgroups 0, 1: softmax; then, 16-bit: the issuing warp, the K and the V
+  // warp and an idle one; int8: four converting warps, then the issuing warp
+  // and three idle ones
+  static constexpr int kWarps = I8 ? 16 : 12, kThreads = kWarps * 32;
+  static constexpr int kMmaWarp = I8 ? 12 : 8, kFillWarp = I8 ? 8 : 9;
+  // registers per thread: at launch (65536 / kThreads, a multiple of 8), then
+  // each warpgroup's share of the same total; a softmax thread holds a whole
+  // row of 128 logits
+  static constexpr int kRegs = I8 ? 128 : 168, kRegsSoftmax = I8 ? 184 : 208, kRegsFill = I8 ? 88 : 88, kRegsMma = I8 ? 56 : 88;
+  static_assert(2 * kRegsSoftmax + kRegsFill + (I8 ? kRegsMma : 0) <= (I8 ? 4 : 3) * kRegs, "the block's registers");
   static constexpr int kFillThreads = 128;
   // fp16 holds p * 16 * (value scale) for scales up to 255
   static constexpr float kSlack = I8 ? 4.f : 8.f;
   static constexpr float kVScale = I8 ? 16.f : 1.f;
 
-  // ---- the issuing thread -----------------------------------------------------------------
+  // ---- the issuing warp: all of it waits, one elected lane issues --------------------------
   static __device__ bool issue(const ChunkArgs& a, M& m, uint32_t smem, uint32_t tmem) {
-    const Waiter wait{a.err};
+    const auto wait = [&](uint64_t* bar, uint32_t phase) {  // the whole warp goes on, or none of it
+      return __all_sync(0xffffffffu, Waiter{a.err}(bar, phase)) != 0;
+    };
     constexpr uint32_t idS = instr_desc<TQ>(kTile, kTile, false), idO = instr_desc<TQ>(kTile, D, true);
-    const uint32_t page_bytes = static_cast<uint32_t>(a.S) * D * 2;
+    constexpr uint32_t kStep = Lay::kTileBytes >> 4;  // descriptors count 16 bytes
+    const uint64_t dq = desc_k_major(smem + Lay::q_off), dk = desc_k_major(smem + Lay::k_off);
     // V blocks of 64 columns: within a page (TMA), or over the whole tile (converted)
-    const uint32_t v_block = I8 ? Lay::kHalf : static_cast<uint32_t>(a.S) * 128u;
-    uint32_t kc = 0, vc = 0, sc[2] = {0, 0}, qc = 0;
-    const auto S = [&](int t, int qt, uint32_t stage) {
-      const uint64_t dq = desc_k_major(smem + Lay::q_off + qt * Lay::kTileBytes);
-      const uint64_t dk = desc_k_major(smem + Lay::k_off + stage * Lay::kTileBytes);
+    const uint64_t dv = desc_mn_major(smem + Lay::v_off, I8 ? Lay::kHalf : static_cast<uint32_t>(a.S) * 128u);
+    uint32_t v_at[kTile / 16];  // the tile's tokens 16 ks
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks) {
+      const uint32_t tok = 16 * ks, S = a.S;
+      v_at[ks] = (I8 ? tok * 128u : (tok / S) * (S * D * 2) + (tok % S) * 128u) >> 4;
+    }
+    uint32_t sc[2] = {0, 0}, qc = 0;          // rounds of the barriers
+    uint32_t ki = 0, vi = 0, kr = 0, vr = 0;          // stage and round of the rings
+    const auto next_k = [&] {
+      if (++ki == KST) ki = 0, ++kr;
+    };
+    const auto next_v = [&] {
+      if (++vi == VST) vi = 0, ++vr;
+    };
+    const auto S = [&](int t, int qt) {
+      const uint64_t q = dq + qt * kStep, k = dk + ki * kStep;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * Lay::kHalf + (ks & 3) * 32u) >> 4;
-        mma_ss(tmem + t * 128, dq + off, dk + off, idS, ks > 0);
+        mma_ss(tmem + t * 128, q + off, k + off, idS, ks > 0);
       }
       mma_commit(&m.s_full[t]);
     };
-    const auto PV = [&](int t, uint32_t stage, bool acc) {
-      const uint32_t base = smem + Lay::v_off + stage * Lay::kTileBytes;
+    const auto PV = [&](int t, bool acc) {
+      const uint64_t v = dv + vi * kStep;
 #pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks) {
-        const uint32_t tok = 16 * ks;
-        const uint32_t at = I8 ? tok * 128u : (tok / a.S) * page_bytes + (tok % a.S) * 128u;
-        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * ks, desc_mn_major(base + at, v_block), idO, acc || ks > 0);
-      }
+      for (int ks = 0; ks < kTile / 16; ++ks)
+        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * ks, v + v_at[ks], idO, acc || ks > 0);
     };
     SegIter it(a, m.plan);
     Seg s;
@@ -280,60 +300,75 @@ struct Kernel {
       const int n = s.k1 - s.k0;
       if (!wait(&m.q_full, qc++)) return false;
       if (s.n_rows > kTile) {  // two tiles of rows over the same keys
-        if (!wait(&m.k_full[kc % KST], kc / KST)) return false;
+        if (!wait(&m.k_full[ki], kr)) return false;
         tc_fence_after();
-        S(0, 0, kc % KST);
-        S(1, 1, kc % KST);
-        mma_commit(&m.k_empty[kc % KST]);
-        ++kc;
+        if (elect_one()) {
+          S(0, 0);
+          S(1, 1);
+          mma_commit(&m.k_empty[ki]);
+        }
+        __syncwarp();
+        next_k();
         for (int j = 0; j < n; ++j) {
-          if (!wait(&m.v_full[vc % VST], vc / VST)) return false;
+          if (!wait(&m.v_full[vi], vr)) return false;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
+            if (t == 0 && j + 1 < n && !wait(&m.k_full[ki], kr)) return false;
             if (!wait(&m.p_full[t], sc[t]++)) return false;
             tc_fence_after();
-            PV(t, vc % VST, j > 0);
-            if (j + 1 < n) {
-              if (t == 0 && !wait(&m.k_full[kc % KST], kc / KST)) return false;
-              tc_fence_after();
-              S(t, t, kc % KST);
+            if (elect_one()) {
+              PV(t, j > 0);
+              if (j + 1 < n) S(t, t);
+              if (t == 1) {
+                mma_commit(&m.v_empty[vi]);
+                if (j + 1 < n) mma_commit(&m.k_empty[ki]);
+              }
             }
+            __syncwarp();
           }
-          mma_commit(&m.v_empty[vc % VST]);
-          ++vc;
-          if (j + 1 < n) {
-            mma_commit(&m.k_empty[kc % KST]);
-            ++kc;
-          }
+          next_v();
+          if (j + 1 < n) next_k();
         }
-      } else {  // one tile of rows, streams take alternate steps
+      } else {  // one tile of rows, the streams take alternate steps
         for (int j = 0; j < min(n, 2); ++j) {
-          if (!wait(&m.k_full[kc % KST], kc / KST)) return false;
+          if (!wait(&m.k_full[ki], kr)) return false;
           tc_fence_after();
-          S(j, 0, kc % KST);
-          mma_commit(&m.k_empty[kc % KST]);
-          ++kc;
+          if (elect_one()) {
+            S(j, 0);
+            mma_commit(&m.k_empty[ki]);
+          }
+          __syncwarp();
+          next_k();
         }
         for (int j = 0; j < n; ++j) {
           const int t = j & 1;
-          if (!wait(&m.v_full[vc % VST], vc / VST)) return false;
+          if (!wait(&m.v_full[vi], vr)) return false;
           if (!wait(&m.p_full[t], sc[t]++)) return false;
           tc_fence_after();
-          PV(t, vc % VST, j > 1);
-          mma_commit(&m.v_empty[vc % VST]);
-          ++vc;
+          if (elect_one()) {
+            PV(t, j > 1);
+            mma_commit(&m.v_empty[vi]);
+          }
+          __syncwarp();
+          next_v();
           if (j + 2 < n) {
-            if (!wait(&m.k_full[kc % KST], kc / KST)) return false;
+            if (!wait(&m.k_full[ki], kr)) return false;
             tc_fence_after();
-            S(t, 0, kc % KST);
-            mma_commit(&m.k_empty[kc % KST]);
-            ++kc;
+            if (elect_one()) {
+              S(t, 0);
+              mma_commit(&m.k_empty[ki]);
+            }
+            __syncwarp();
+            next_k();
           }
         }
       }
-      mma_commit(&m.q_empty);
-      mma_commit(&m.o_full[0]);
-      mma_commit(&m.o_full[1]);
+      if (elect_one()) {
+        mma_commit(&m.q_empty);
+        mma_commit(&m.o_full[0]);
+        mma_commit(&m.o_full[1]);
+      }
+      __syncwarp();
     }
     return true;
   }
@@ -534,8 +569,9 @@ struct Kernel {
     float m, l;
   };
 
+  // channel 0 of a row in a slot; the next channel is part_rows further
   static __device__ __forceinline__ float* part_at(const ChunkArgs& a, int slot, int row) {
-    return a.part + (static_cast<size_t>(slot) * a.part_rows + row) * (D + 2);
+    return a.part + static_cast<size_t>(slot) * (D + 2) * a.part_rows + row;
   }
 
   // out and lse of a row from its unnormalised O (element i by o(i)), m and l
@@ -732,21 +768,23 @@ struct Kernel {
                                                              pack2<TQ>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
           } else if (live) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              __stcg(reinterpret_cast<uint2*>(part + c + i), make_uint2(o[i], o[i + 1]));
+            for (int i = 0; i < 32; ++i) __stcg(part + (c + i) * a.part_rows, __uint_as_float(o[i]));
           }
         }
         if (live && whole && a.lse) a.lse[orow] = row.l > 0.f ? (row.m + log2f(row.l)) * kLn2 : -INFINITY;
-        if (live && !whole) __stcg(reinterpret_cast<float2*>(part + D), make_float2(row.m, row.l));
+        if (live && !whole) {
+          __stcg(part + D * a.part_rows, row.m);
+          __stcg(part + (D + 1) * a.part_rows, row.l);
+        }
       }
       tc_fence_before();  // the loads of O come before the next segment's first product
       if (!two) bar_sync(2, 256);
-      if (!whole) join(a, m, s, tid, warp, lane);
+      if (!whole) join(a, m, s, tid);
     }
   }
 
   // Counts a part of an item in; the last to arrive joins them all.
-  static __device__ void join(const ChunkArgs& a, M& m, const Seg& s, int tid, int warp, int lane) {
+  static __device__ void join(const ChunkArgs& a, M& m, const Seg& s, int tid) {
     const long long n = m.plan.ctas, total = m.plan.total;
     const int c0 = static_cast<int>(((s.item_first + 1) * n - 1) / total);
     const int c1 = static_cast<int>(((s.item_first + s.nk) * n - 1) / total);
@@ -756,34 +794,39 @@ struct Kernel {
     bar_sync(2, 256);
     if (!m.last) return;
     __threadfence();
-    constexpr int CPL = D / 32;  // channels of a lane
-    for (int r = warp; r < s.n_rows; r += 8) {
-      const auto slot = [&](int c) { return c == c0 ? 2 * c + 1 : 2 * c; };
-      float mm = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, __ldcg(part_at(a, slot(c), r) + D));
-      mm = warp_max(mm);
-      float l = 0.f, o[CPL];
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) o[i] = 0.f;
-      if (mm != -INFINITY)
-        for (int c = c0; c <= c1; ++c) {
-          const float* p = part_at(a, slot(c), r);
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
-          const float f = ex2(ml.x - mm);
-          l = fmaf(ml.y, f, l);
-#pragma unroll
-          for (int i = 0; i < CPL; i += 2) {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(p + CPL * lane + i));
-            o[i] = fmaf(v.x, f, o[i]);
-            o[i + 1] = fmaf(v.y, f, o[i + 1]);
-          }
-        }
+    // a thread per row, or two with half the channels each
+    const bool two = s.n_rows > kTile;
+    const int r = two ? tid : tid % kTile, d0 = two ? 0 : tid / kTile * (D / 2), d1 = two ? D : d0 + D / 2;
+    if (r < s.n_rows) {
+      const auto at = [&](int c) { return part_at(a, c == c0 ? 2 * c + 1 : 2 * c, r); };
+      float mm = -INFINITY, l = 0.f;
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(at(c) + D * a.part_rows));
+      if (mm == -INFINITY) mm = 0.f;  // every part's weight is 0
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c)
+        l = fmaf(__ldcg(at(c) + (D + 1) * a.part_rows), ex2(__ldcg(at(c) + D * a.part_rows) - mm), l);
       const float inv = l > 0.f ? (1.f / kVScale) / l : 0.f;
       const size_t orow = out_row(a, s, r);
-      TQ* dst = static_cast<TQ*>(a.out) + orow * D + CPL * lane;
+      TQ* dst = static_cast<TQ*>(a.out) + orow * D;
+      for (int d = d0; d < d1; d += 32) {
+        float o[32];
 #pragma unroll
-      for (int i = 0; i < CPL; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack2<TQ>(o[i] * inv, o[i + 1] * inv);
-      if (lane == 0 && a.lse) a.lse[orow] = l > 0.f ? (mm + log2f(l)) * kLn2 : -INFINITY;
+        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        for (int c = c0; c <= c1; ++c) {
+          const float* p = at(c);
+          const float f = ex2(__ldcg(p + D * a.part_rows) - mm);
+          p += d * a.part_rows;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(__ldcg(p + i * a.part_rows), f, o[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          *reinterpret_cast<uint4*>(dst + d + i) =
+              make_uint4(pack2<TQ>(o[i] * inv, o[i + 1] * inv), pack2<TQ>(o[i + 2] * inv, o[i + 3] * inv),
+                         pack2<TQ>(o[i + 4] * inv, o[i + 5] * inv), pack2<TQ>(o[i + 6] * inv, o[i + 7] * inv));
+      }
+      if (d0 == 0 && a.lse) a.lse[orow] = l > 0.f ? (mm + log2f(l)) * kLn2 : -INFINITY;
     }
     if (tid == 0) a.counters[c0] = 0;  // ready for the next call
   }
@@ -826,20 +869,24 @@ __global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const
   tc_fence_after();
   const uint32_t tmem = m.tmem;
 
-  if (warp < K::kMmaWarp) {
+  if (warp < 8) {
+    regs_up<K::kRegsSoftmax>();
     K::softmax(a, m, tmem, warp, lane);
-  } else if (warp == K::kMmaWarp) {
-    if (lane == 0 && !K::issue(a, m, smem_u32(smem), tmem)) {
-      // products in flight end before TMEM goes back
-      mma_commit(&m.drain);
-      mbar_wait_bounded(&m.drain, 0);
-    }
-    __syncwarp();
   } else {
-    if constexpr (K::I8)
-      K::convert(a, m, smem, threadIdx.x - K::kFillWarp * 32);
-    else
+    if (K::I8 && warp >= 12) regs_down<K::kRegsMma>(); else regs_down<K::kRegsFill>();  // whole warpgroups
+    if (warp == K::kMmaWarp) {
+      const bool ok = K::issue(a, m, smem_u32(smem), tmem);
+      if (!ok) {
+        // products in flight end before TMEM goes back
+        if (elect_one()) mma_commit(&m.drain);
+        __syncwarp();
+        mbar_wait_bounded(&m.drain, 0);
+      }
+    } else if constexpr (K::I8) {
+      if (warp < 12) K::convert(a, m, smem, threadIdx.x - K::kFillWarp * 32);
+    } else if (warp <= K::kFillWarp + 1) {
       K::fill(a, m, smem, warp == K::kFillWarp + 1, lane);
+    }
   }
   pdl_trigger();
   tc_fence_before();
