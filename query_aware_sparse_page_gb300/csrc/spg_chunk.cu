@@ -216,7 +216,7 @@ struct Layout {
 };
 template <int KST, int VST, bool I8>
 struct Misc {
-  uint64_t q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[2], p_full[2][2], o_full[2], drain;
   Plan plan;
   uint32_t tmem;
   int last;
@@ -224,11 +224,20 @@ struct Misc {
   alignas(16) float scales[I8 ? VST : 1][2][I8 ? kTile : 1];  // int8: scale * key scale, 16 * value scale of a step's tokens
 };
 
-// A wait that ran out: recorded, and the caller leaves its loop.
+// A wait: false, and recorded, when it ran out (as mbar_wait_bounded, in few
+// instructions: the issuing warp's path has five of them per step).
 struct Waiter {
   int32_t* err;
-  __device__ bool operator()(uint64_t* bar, uint32_t phase) const {
-    if (mbar_wait_bounded(bar, phase & 1)) return true;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t phase) const {
+    if (mbar_try_wait(bar, phase & 1)) return true;
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+#pragma unroll 1
+    for (int i = 0; i < (1 << 22); ++i) {
+      if (mbar_try_wait(bar, phase & 1)) return true;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (t - t0 > 100ull * 1000 * 1000) break;
+    }
     record_error(err, SPG_DEVERR_TIMEOUT);
     return false;
   }
@@ -262,9 +271,12 @@ struct Kernel {
     };
     constexpr uint32_t idS = instr_desc<TQ>(kTile, kTile, false), idO = instr_desc<TQ>(kTile, D, true);
     constexpr uint32_t kStep = Lay::kTileBytes >> 4;  // descriptors count 16 bytes
-    const uint64_t dq = desc_k_major(smem + Lay::q_off), dk = desc_k_major(smem + Lay::k_off);
+    // what the whole warp agrees on, taken from one lane so that it can be kept once per warp
+    const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    tmem = uniform(tmem);
+    const uint32_t dq = desc_k_major(smem + Lay::q_off), dk = desc_k_major(smem + Lay::k_off);
     // V blocks of 64 columns: within a page (TMA), or over the whole tile (converted)
-    const uint64_t dv = desc_mn_major(smem + Lay::v_off, I8 ? Lay::kHalf : static_cast<uint32_t>(a.S) * 128u);
+    const uint32_t dv = desc_mn_major(smem + Lay::v_off, I8 ? Lay::kHalf : static_cast<uint32_t>(a.S) * 128u);
     uint32_t v_at[kTile / 16];  // the tile's tokens 16 ks
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks) {
@@ -280,7 +292,7 @@ struct Kernel {
       if (++vi == VST) vi = 0, ++vr;
     };
     const auto S = [&](int t, int qt) {
-      const uint64_t q = dq + qt * kStep, k = dk + ki * kStep;
+      const uint32_t q = dq + qt * kStep, k = dk + ki * kStep;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * Lay::kHalf + (ks & 3) * 32u) >> 4;
@@ -288,18 +300,21 @@ struct Kernel {
       }
       mma_commit(&m.s_full[t]);
     };
-    const auto PV = [&](int t, bool acc) {
-      const uint64_t v = dv + vi * kStep;
+    // half the step's tokens: the first half starts while the second is in its softmax
+    const auto PV = [&](int t, int half, bool acc) {
+      const uint32_t v = dv + vi * kStep;
 #pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks)
+      for (int i = 0; i < kTile / 32; ++i) {
+        const int ks = half * (kTile / 32) + i;
         mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * ks, v + v_at[ks], idO, acc || ks > 0);
+      }
     };
     SegIter it(a, m.plan);
     Seg s;
-    while (it.next(a, s)) {
-      const int n = s.k1 - s.k0;
+    while (uniform(it.next(a, s))) {
+      const int n = uniform(s.k1 - s.k0);
       if (!wait(&m.q_full, qc++)) return false;
-      if (s.n_rows > kTile) {  // two tiles of rows over the same keys
+      if (uniform(s.n_rows) > kTile) {  // two tiles of rows over the same keys
         if (!wait(&m.k_full[ki], kr)) return false;
         tc_fence_after();
         if (elect_one()) {
@@ -314,10 +329,14 @@ struct Kernel {
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t == 0 && j + 1 < n && !wait(&m.k_full[ki], kr)) return false;
-            if (!wait(&m.p_full[t], sc[t]++)) return false;
+            if (!wait(&m.p_full[t][0], sc[t])) return false;
+            tc_fence_after();
+            if (elect_one()) PV(t, 0, j > 0);
+            __syncwarp();
+            if (!wait(&m.p_full[t][1], sc[t]++)) return false;
             tc_fence_after();
             if (elect_one()) {
-              PV(t, j > 0);
+              PV(t, 1, true);
               if (j + 1 < n) S(t, t);
               if (t == 1) {
                 mma_commit(&m.v_empty[vi]);
@@ -343,10 +362,14 @@ struct Kernel {
         for (int j = 0; j < n; ++j) {
           const int t = j & 1;
           if (!wait(&m.v_full[vi], vr)) return false;
-          if (!wait(&m.p_full[t], sc[t]++)) return false;
+          if (!wait(&m.p_full[t][0], sc[t])) return false;
+          tc_fence_after();
+          if (elect_one()) PV(t, 0, j > 1);
+          __syncwarp();
+          if (!wait(&m.p_full[t][1], sc[t]++)) return false;
           tc_fence_after();
           if (elect_one()) {
-            PV(t, j > 1);
+            PV(t, 1, true);
             mma_commit(&m.v_empty[vi]);
           }
           __syncwarp();
@@ -656,13 +679,18 @@ struct Kernel {
           for (int c = 0; c < kTile; ++c)
             if (c > lim || ((bad16 >> (c / 16)) & 1u)) x[c] = 0xff800000u;  // -inf
         }
-        float mx = fmaxf(f(0), f(1));
+        float mx[4];  // chains that do not wait for one another
 #pragma unroll
-        for (int c = 2; c < kTile; c += 2) mx = fmaxf(mx, fmaxf(f(c), f(c + 1)));
-        if constexpr (!I8) mx *= a.scale_log2;
-        const bool raise = mx > row.m + kSlack;  // -inf + kSlack = -inf: the first finite logit
+        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(f(c), f(c + 4));
+#pragma unroll
+        for (int c = 8; c < kTile; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], f(c + i)), f(c + 4 + i));
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if constexpr (!I8) top *= a.scale_log2;
+        const bool raise = top > row.m + kSlack;  // -inf + kSlack = -inf: the first finite logit
         if (__any_sync(0xffffffffu, raise)) {
-          const float mn = raise ? mx : row.m;
+          const float mn = raise ? top : row.m;
           const float factor = row.m == -INFINITY ? (raise ? 0.f : 1.f) : ex2(row.m - mn);
           row.m = mn;
           row.l *= factor;
@@ -699,10 +727,12 @@ struct Kernel {
             w[i] = pack2<TQ>(p.x, p.y);
           }
           tmem_st16(tS + c0 / 2, w);
+          if (c0 % (kTile / 2)) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&m.p_full[t][c0 / (kTile / 2)]);
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&m.p_full[t]);
         const float2 s0 = unpack_f32x2(l0), s1 = unpack_f32x2(l1);
         row.l += (s0.x + s0.y) + (s1.x + s1.y);
       }
@@ -855,7 +885,8 @@ __global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.s_full[i], 1);
-      mbar_init(&m.p_full[i], 128);
+      mbar_init(&m.p_full[i][0], 128);
+      mbar_init(&m.p_full[i][1], 128);
       mbar_init(&m.o_full[i], 1);
     }
     mbar_init(&m.drain, 1);

@@ -4,10 +4,10 @@
 // Shared-memory operands are tiles of 128-byte rows with the 128-byte swizzle
 // (16-byte piece c of row r at c ^ (r % 8), tiles 1024-byte aligned), as the
 // TMA copies leave them:
-//   K-major (the contraction runs along the 128 bytes): 8-row groups are
-//     `group` bytes apart, a k-step of 16 values starts 32 bytes further;
-//   MN-major (the contraction runs over the rows): 8-row groups are 1024
-//     bytes apart, blocks of 64 columns `block` bytes apart.
+//   K-major (the contraction runs along the 128 bytes): a k-step of 16
+//     values starts 32 bytes further;
+//   MN-major (the contraction runs over the rows): blocks of 64 columns are
+//     `block` bytes apart.
 #pragma once
 
 #include "spg_common.cuh"
@@ -15,14 +15,12 @@
 namespace spg {
 
 // ---- descriptors ------------------------------------------------------------------
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading, uint32_t stride) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>((leading >> 4) & 0x3fffu) << 16) |
-         (static_cast<uint64_t>((stride >> 4) & 0x3fffu) << 32) | (1ull << 46) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr, uint32_t group = 1024) {
-  return smem_desc(addr, 16, group);
-}
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t block) { return smem_desc(addr, block, 1024); }
+// The upper word is the same for every operand here (8-row groups 1024 bytes
+// apart, 128-byte swizzle); the lower one is address and block distance,
+// both in units of 16 bytes, so that moving along an operand adds to it.
+constexpr uint32_t kDescUpper = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t addr) { return (addr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t addr, uint32_t block) { return (addr >> 4) | ((block >> 4) << 16); }
 
 // kind::f16 with fp32 accumulation, A and B of the 16-bit type T; b_mn: B is MN-major
 template <typename T>
@@ -41,19 +39,19 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // ---- matrix products (one thread issues) ---------------------------------------------
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "n"(kDescUpper)
       : "memory");
 }
 // A in TMEM: two 16-bit values per column
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "n"(kDescUpper)
       : "memory");
 }
 // arrives on `bar` when every product issued so far by this thread is done
