@@ -28,11 +28,13 @@
 // the part that arrives last joins them in a fixed order.  No CTA waits for
 // another.
 //
-// Keys and values of 16-bit pools come by TMA, one copy per page and 64
-// channels (K: the pages' rows of a half follow one another, so that 128
-// tokens are one operand) or per page (V).  int8 pages are turned into exact
-// 16-bit codes by four warps; the key scales then multiply the logits and the
-// value scales (times 16, undone at the end) the probabilities.
+// Four warps fill the K and V rings, 16 bytes per thread and copy, straight
+// into the swizzled tiles: pages of 16 tokens are too small for TMA (24 tile
+// copies per step kept its unit busy for 3200 cycles, 1.5 times what the
+// products take), and tokens that are not there become zeros on the way.
+// int8 codes land in the upper half of their tile's own space and are widened
+// in place to exact 16-bit values; the key scales then multiply the logits
+// and the value scales (times 16, undone at the end) the probabilities.
 //
 // Roundings: P to the 16-bit type (as the products take it) and the result;
 // everything else is fp32.
@@ -55,8 +57,7 @@ constexpr int kMaxParts = 32;        // most parts an average item is split into
 constexpr uint32_t kTmemCols = 512;  // S0 S1 O0 O1, 128 columns each
 
 struct ChunkArgs {
-  CUtensorMap tmq, tmk, tmv;
-  int v_whole;  // tmv takes a whole page per copy
+  CUtensorMap tmq;
   const void *k_pool, *v_pool;
   const __half *k_scale, *v_scale;
   const int32_t *q_start, *page_table, *seq_lens;
@@ -216,11 +217,12 @@ struct Layout {
 };
 template <int KST, int VST, bool I8>
 struct Misc {
-  uint64_t q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[2], p_full[2][2], o_full[2], drain;
+  uint64_t q_full, q_empty, k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], s_full[2], p_full[2][2], o_full[2], turn[2], drain[2];
   Plan plan;
   uint32_t tmem;
   int last;
   float ml[kTile][2];                            // stream 1's m and l, joined by stream 0
+  alignas(16) float ones[I8 ? kTile : 1];
   alignas(16) float scales[I8 ? VST : 1][2][I8 ? kTile : 1];  // int8: scale * key scale, 16 * value scale of a step's tokens
 };
 
@@ -249,23 +251,24 @@ struct Kernel {
   using Lay = Layout<D, I8>;
   static constexpr int KST = Lay::KST, VST = Lay::VST, NH = Lay::NH;
   using M = Misc<KST, VST, I8>;
-  // warpgroups 0, 1: softmax; then, 16-bit: the issuing warp, the K and the V
-  // warp and an idle one; int8: four converting warps, then the issuing warp
-  // and three idle ones
-  static constexpr int kWarps = I8 ? 16 : 12, kThreads = kWarps * 32;
-  static constexpr int kMmaWarp = I8 ? 12 : 8, kFillWarp = I8 ? 8 : 9;
-  // registers per thread: at launch (65536 / kThreads, a multiple of 8), then
-  // each warpgroup's share of the same total; a softmax thread holds a whole
-  // row of 128 logits
-  static constexpr int kRegs = I8 ? 128 : 168, kRegsSoftmax = I8 ? 184 : 208, kRegsFill = I8 ? 88 : 88, kRegsMma = I8 ? 56 : 88;
-  static_assert(2 * kRegsSoftmax + kRegsFill + (I8 ? kRegsMma : 0) <= (I8 ? 4 : 3) * kRegs, "the block's registers");
-  static constexpr int kFillThreads = 128;
+  // warpgroups 0, 1: softmax; 2: loads; 3: the two issuing warps, the warp
+  // that loads Q, an idle one
+  static constexpr int kThreads = 512, kLoadWarp = 8, kMmaWarp = 12, kQWarp = 14;
+  // registers per thread: 128 at launch, then each warpgroup's share of the
+  // same total; a softmax thread holds half a row of 128 logits
+  static constexpr int kRegsSoftmax = 168, kRegsLoad = 112, kRegsIssue = 64;
+  static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 4 * 128, "the block's registers");
+  static constexpr int kLoadThreads = 128;
   // fp16 holds p * 16 * (value scale) for scales up to 255
   static constexpr float kSlack = I8 ? 4.f : 8.f;
   static constexpr float kVScale = I8 ? 16.f : 1.f;
 
-  // ---- the issuing warp: all of it waits, one elected lane issues --------------------------
-  static __device__ bool issue(const ChunkArgs& a, M& m, uint32_t smem, uint32_t tmem) {
+  // ---- the issuing warps, one per stream: all of a warp waits, one elected lane issues -----
+  // One warp's waits and issues for both streams took longer than their
+  // products.  The streams' batches (P V of a step, S of the next) go to the
+  // tensor cores strictly in turn: left to themselves the two fall into step,
+  // both in their softmax while the tensor cores idle, then both in line.
+  static __device__ bool issue(const ChunkArgs& a, M& m, uint32_t smem, uint32_t tmem, int t) {
     const auto wait = [&](uint64_t* bar, uint32_t phase) {  // the whole warp goes on, or none of it
       return __all_sync(0xffffffffu, Waiter{a.err}(bar, phase)) != 0;
     };
@@ -274,220 +277,157 @@ struct Kernel {
     // what the whole warp agrees on, taken from one lane so that it can be kept once per warp
     const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     tmem = uniform(tmem);
+    t = uniform(t);
+    const uint32_t tS = tmem + t * 128, tO = tmem + 256 + t * 128;
     const uint32_t dq = desc_k_major(smem + Lay::q_off), dk = desc_k_major(smem + Lay::k_off);
-    // V blocks of 64 columns: within a page (TMA), or over the whole tile (converted)
-    const uint32_t dv = desc_mn_major(smem + Lay::v_off, I8 ? Lay::kHalf : static_cast<uint32_t>(a.S) * 128u);
-    uint32_t v_at[kTile / 16];  // the tile's tokens 16 ks
-#pragma unroll
-    for (int ks = 0; ks < kTile / 16; ++ks) {
-      const uint32_t tok = 16 * ks, S = a.S;
-      v_at[ks] = (I8 ? tok * 128u : (tok / S) * (S * D * 2) + (tok % S) * 128u) >> 4;
-    }
-    uint32_t sc[2] = {0, 0}, qc = 0;          // rounds of the barriers
-    uint32_t ki = 0, vi = 0, kr = 0, vr = 0;          // stage and round of the rings
+    const uint32_t dv = desc_mn_major(smem + Lay::v_off, Lay::kHalf);
+    uint32_t sc = 0, qc = 0, tc = 0;          // rounds of the barriers
+    uint32_t ki = 0, vi = 0, kr = 0, vr = 0;  // stage and round of the rings
     const auto next_k = [&] {
       if (++ki == KST) ki = 0, ++kr;
     };
     const auto next_v = [&] {
       if (++vi == VST) vi = 0, ++vr;
     };
-    const auto S = [&](int t, int qt) {
+    // S of the next key tile; its stage is free (for this stream) once that is done
+    const auto S = [&](int qt) {
       const uint32_t q = dq + qt * kStep, k = dk + ki * kStep;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * Lay::kHalf + (ks & 3) * 32u) >> 4;
-        mma_ss(tmem + t * 128, q + off, k + off, idS, ks > 0);
+        mma_ss(tS, q + off, k + off, idS, ks > 0);
       }
       mma_commit(&m.s_full[t]);
+      mma_commit(&m.k_empty[ki]);
     };
     // half the step's tokens: the first half starts while the second is in its softmax
-    const auto PV = [&](int t, int half, bool acc) {
+    const auto PV = [&](int half, bool acc) {
       const uint32_t v = dv + vi * kStep;
 #pragma unroll
       for (int i = 0; i < kTile / 32; ++i) {
         const int ks = half * (kTile / 32) + i;
-        mma_ts(tmem + 256 + t * 128, tmem + t * 128 + 8 * ks, v + v_at[ks], idO, acc || ks > 0);
+        mma_ts(tO, tS + 8 * ks, v + ks * (16 * 128 >> 4), idO, acc || ks > 0);
       }
     };
     SegIter it(a, m.plan);
     Seg s;
     while (uniform(it.next(a, s))) {
       const int n = uniform(s.k1 - s.k0);
+      // two tiles of rows: both streams take every step; one: alternate ones
+      const int step = uniform(s.n_rows) > kTile ? 1 : 2, qt = step == 1 ? t : 0;
       if (!wait(&m.q_full, qc++)) return false;
-      if (uniform(s.n_rows) > kTile) {  // two tiles of rows over the same keys
-        if (!wait(&m.k_full[ki], kr)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          S(0, 0);
-          S(1, 1);
-          mma_commit(&m.k_empty[ki]);
-        }
+      int j = step == 1 ? 0 : t, jk = 0;  // next step of P V, next key tile
+      // stream 0's first S, stream 1's, stream 0's first P V and next S, ...
+      // (with one tile of rows the streams' batches differ in number, and the
+      // keys' bytes bound them anyway)
+      const auto take_turn = [&] {
+        if (step == 2) return true;
+        const uint32_t round = tc++;
+        return t == 1 ? wait(&m.turn[1], round) : round == 0 || wait(&m.turn[0], round - 1);
+      };
+      const auto pass_turn = [&] {
+        if (step == 1 && elect_one()) mbar_arrive(&m.turn[t ^ 1]);
         __syncwarp();
-        next_k();
-        for (int j = 0; j < n; ++j) {
-          if (!wait(&m.v_full[vi], vr)) return false;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t == 0 && j + 1 < n && !wait(&m.k_full[ki], kr)) return false;
-            if (!wait(&m.p_full[t][0], sc[t])) return false;
-            tc_fence_after();
-            if (elect_one()) PV(t, 0, j > 0);
-            __syncwarp();
-            if (!wait(&m.p_full[t][1], sc[t]++)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-              PV(t, 1, true);
-              if (j + 1 < n) S(t, t);
-              if (t == 1) {
-                mma_commit(&m.v_empty[vi]);
-                if (j + 1 < n) mma_commit(&m.k_empty[ki]);
-              }
-            }
-            __syncwarp();
-          }
-          next_v();
-          if (j + 1 < n) next_k();
-        }
-      } else {  // one tile of rows, the streams take alternate steps
-        for (int j = 0; j < min(n, 2); ++j) {
+      };
+      // the key tile of this stream's step j, past those that are the other stream's alone
+      const auto next_s = [&](int j) {
+        for (; jk <= j && jk < n; ++jk) {
           if (!wait(&m.k_full[ki], kr)) return false;
+          fence_proxy_async();  // the tile was written with plain copies
           tc_fence_after();
           if (elect_one()) {
-            S(j, 0);
-            mma_commit(&m.k_empty[ki]);
+            if (jk == j) S(qt); else mbar_arrive(&m.k_empty[ki]);
           }
           __syncwarp();
           next_k();
         }
-        for (int j = 0; j < n; ++j) {
-          const int t = j & 1;
-          if (!wait(&m.v_full[vi], vr)) return false;
-          if (!wait(&m.p_full[t][0], sc[t])) return false;
+        return true;
+      };
+      if (!take_turn() || !next_s(j)) return false;
+      pass_turn();
+      for (int jv = 0; jv < n; ++jv) {
+        if (!wait(&m.v_full[vi], vr)) return false;
+        fence_proxy_async();
+        if (jv == j) {
+          if (!wait(&m.p_full[t][0], sc) || !take_turn()) return false;
           tc_fence_after();
-          if (elect_one()) PV(t, 0, j > 1);
+          if (elect_one()) PV(0, j >= step);
           __syncwarp();
-          if (!wait(&m.p_full[t][1], sc[t]++)) return false;
+          if (!wait(&m.p_full[t][1], sc++)) return false;
           tc_fence_after();
           if (elect_one()) {
-            PV(t, 1, true);
+            PV(1, true);
             mma_commit(&m.v_empty[vi]);
           }
           __syncwarp();
-          next_v();
-          if (j + 2 < n) {
-            if (!wait(&m.k_full[ki], kr)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-              S(t, 0);
-              mma_commit(&m.k_empty[ki]);
-            }
-            __syncwarp();
-            next_k();
-          }
+          j += step;
+          if (!next_s(j)) return false;
+          pass_turn();
+        } else if (elect_one()) {
+          mbar_arrive(&m.v_empty[vi]);
         }
+        next_v();
       }
+      while (jk < n)  // key tiles behind this stream's last step
+        if (!next_s(n)) return false;
       if (elect_one()) {
         mma_commit(&m.q_empty);
-        mma_commit(&m.o_full[0]);
-        mma_commit(&m.o_full[1]);
+        mma_commit(&m.o_full[t]);
       }
       __syncwarp();
     }
     return true;
   }
 
-  // Q tiles of a segment (one thread)
-  static __device__ bool load_q(const ChunkArgs& a, M& m, uint8_t* smem, const Seg& s, uint32_t count) {
-    if (count > 0 && !Waiter{a.err}(&m.q_empty, count - 1)) return false;
-    const int tiles = s.n_rows > kTile ? 2 : 1;
-    mbar_arrive_expect_tx(&m.q_full, tiles * Lay::kTileBytes);
-    for (int t = 0; t < tiles; ++t)
-      for (int hf = 0; hf < NH; ++hf)
-        tma_tile_4d(smem + Lay::q_off + t * Lay::kTileBytes + hf * Lay::kHalf, &a.tmq, hf * 64, 0, s.h,
-                    s.sq.start + (s.row0 + t * kTile) / a.G, &m.q_full);
-    return true;
-  }
-
-  // ---- 16-bit pools: one warp fills the K ring, one the V ring -----------------------------
-  static __device__ bool fill(const ChunkArgs& a, M& m, uint8_t* smem, bool is_v, int lane) {
+  // ---- Q tiles (one thread), as soon as the products are done with the last ones ---------
+  static __device__ void load_q(const ChunkArgs& a, M& m, uint8_t* smem) {
     const Waiter wait{a.err};
-    const int S = a.S, ppt = kTile / S;
-    const uint32_t page_bytes = static_cast<uint32_t>(S) * D * 2;
-    uint32_t c = 0, qc = 0;
+    uint32_t c = 0;
     SegIter it(a, m.plan);
     Seg s;
-    while (it.next(a, s)) {
-      const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
-      bool ok = true;
-      if (!is_v) {
-        if (lane == 0) ok = load_q(a, m, smem, s, qc);
-        ++qc;
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return false;
-      }
-      const auto page_of = [&](int k) {  // the lane's page of step k; -1: none, or a bad one
-        const int lp = k * ppt + lane;
-        if (lane >= ppt || k >= s.k1 || lp * S > s.last) return -1;
-        const int page = pt[lp];
-        return page >= 0 && page < a.n_phys ? page : -1;
-      };
-      int page = page_of(s.k0);
-      for (int k = s.k0; k < s.k1; ++k) {
-        const int ahead = page_of(k + 1);
-        const uint32_t stage = is_v ? c % VST : c % KST;
-        uint64_t* full = is_v ? &m.v_full[stage] : &m.k_full[stage];
-        const uint32_t round = is_v ? c / VST : c / KST;
-        if (lane == 0 && round > 0) ok = wait(is_v ? &m.v_empty[stage] : &m.k_empty[stage], round - 1);
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) return false;
-        uint8_t* dst = smem + (is_v ? Lay::v_off : Lay::k_off) + stage * Lay::kTileBytes;
-        const int lp = k * ppt + lane;
-        // V rows that hold no token must be zeros (p = 0 there, and 0 times
-        // what the pool holds could be NaN); K rows may be anything, their
-        // logits are masked
-        const bool part = is_v && page >= 0 && (lp + 1) * S > s.sq.L;
-        const bool copy = page >= 0 && !part;
-        const unsigned by_hand = __ballot_sync(0xffffffffu, is_v && lane < ppt && !copy);
-        if (by_hand) {
-          for (unsigned left = by_hand; left; left &= left - 1) {
-            const int l = __ffs(left) - 1;
-            const int pg = __shfl_sync(0xffffffffu, page, l);
-            const int rows = pg >= 0 ? min(S, s.sq.L - (k * ppt + l) * S) : 0;
-            const uint8_t* src = static_cast<const uint8_t*>(a.v_pool) + (static_cast<size_t>(max(pg, 0)) * a.Hkv + s.h) * page_bytes;
-            for (int i = lane; i < S * D / 8; i += 32) {
-              const int r = i / (D / 8), x = i % (D / 8);
-              uint4 w = make_uint4(0u, 0u, 0u, 0u);
-              if (r < rows) w = *reinterpret_cast<const uint4*>(src + r * (D * 2) + x * 16);
-              *reinterpret_cast<uint4*>(dst + l * page_bytes + (x >> 3) * (S * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4)) = w;
-            }
-          }
-          fence_proxy_async();
-        }
-        const int copies = __popc(__ballot_sync(0xffffffffu, copy));
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(full, copies * page_bytes);
-        __syncwarp();
-        if (copy) {
-          const int row = (page * a.Hkv + s.h) * S;
-          if (is_v && a.v_whole) {
-            tma_tile_3d(dst + lane * page_bytes, &a.tmv, 0, row, 0, full);
-          } else {
-#pragma unroll
-            for (int hf = 0; hf < NH; ++hf) {
-              if (is_v)
-                tma_tile_2d(dst + lane * page_bytes + hf * S * 128, &a.tmv, hf * 64, row, full);
-              else
-                tma_tile_2d(dst + hf * Lay::kHalf + lane * S * 128, &a.tmk, hf * 64, row, full);
-            }
-          }
-        }
-        ++c;
-        page = ahead;
-      }
+    for (; it.next(a, s); ++c) {
+      if (c > 0 && !wait(&m.q_empty, c - 1)) return;
+      const int tiles = s.n_rows > kTile ? 2 : 1;
+      mbar_arrive_expect_tx(&m.q_full, tiles * Lay::kTileBytes);
+      for (int t = 0; t < tiles; ++t)
+        for (int hf = 0; hf < NH; ++hf)
+          tma_tile_4d(smem + Lay::q_off + t * Lay::kTileBytes + hf * Lay::kHalf, &a.tmq, hf * 64, 0, s.h,
+                      s.sq.start + (s.row0 + t * kTile) / a.G, &m.q_full);
     }
-    // copies still in flight land before the CTA leaves: their consumers wait for them
-    return true;
   }
 
-  // ---- int8 pools: four warps turn codes into 16-bit tiles -----------------------------------
+  // ---- loads ----------------------------------------------------------------------------------
+  // A thread's pieces of a tile are one 16-byte column of every kPieces-th row.
+  static constexpr int kCpr = D * static_cast<int>(sizeof(T)) / 16;  // pieces of a row
+  static constexpr int kRowsPer = kLoadThreads / kCpr;              // rows of the threads together
+  static constexpr int kPieces = kTile / kRowsPer;
+
+  // pages of step k, one per lane
+  static __device__ __forceinline__ int page_of(const ChunkArgs& a, const Seg& s, const int32_t* pt, int k, int lane) {
+    const int lp = k * (kTile / a.S) + lane;
+    if (lane >= kTile / a.S || k >= s.k1 || lp * a.S > s.last) return -1;
+    const int page = pt[lp];
+    return page >= 0 && page < a.n_phys ? page : -1;
+  }
+  static __device__ __forceinline__ void issue_copies(const ChunkArgs& a, const Seg& s, const void* pool, int k, int page, int s_log2,
+                                                      int tid, uint32_t dst) {
+    const int c = tid % kCpr, r0 = tid / kCpr;
+    const uint8_t* base = static_cast<const uint8_t*>(pool) + c * 16;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = r0 + i * kRowsPer;
+      const int pg = __shfl_sync(0xffffffffu, page, r >> s_log2);
+      const bool live = pg >= 0 && k * kTile + r < s.sq.L;
+      const size_t row = (((static_cast<size_t>(live ? pg : 0) * a.Hkv + s.h) << s_log2) + (r & (a.S - 1)));
+      uint32_t to;
+      if constexpr (I8)
+        to = r * D + c * 16;
+      else
+        to = (c >> 3) * Lay::kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+      copy16(dst + to, base + row * (D * sizeof(T)), live);
+    }
+  }
+
   // four bytes -> two pairs, exact
   static __device__ __forceinline__ void widen4(uint32_t r, uint32_t& lo, uint32_t& hi) {
     const uint32_t u = r ^ 0x80808080u;
@@ -510,80 +450,109 @@ struct Kernel {
       hi = pack2<TQ>(f[2], f[3]);
     }
   }
-
-  static constexpr int kCpt = D / 16;                          // 16-byte pieces of a row of codes
-  static constexpr int kPieces = kTile * kCpt / kFillThreads;  // of one tile, per thread
-
-  static __device__ __forceinline__ void fetch(const ChunkArgs& a, const Seg& s, const void* pool, int k, int tid, uint4 (&w)[kPieces]) {
-    const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
+  // int8: the codes in the tile's upper half become the tile
+  static __device__ __forceinline__ void widen(uint8_t* tile, int tid) {
+    uint4 w[kPieces];
+    const uint8_t* raw = tile + Lay::kTileBytes / 2;
+    const int x = tid % kCpr, r0 = tid / kCpr, c = 2 * x;  // two 16-byte pieces of 16-bit values
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + (r0 + i * kRowsPer) * D + x * 16);
+    bar_sync(3, kLoadThreads);  // every code is in a register
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int x = tid + kFillThreads * i, t = k * kTile + x / kCpt;
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (k < s.k1 && t <= s.last) {
-        const int page = pt[t / a.S];
-        if (page >= 0 && page < a.n_phys)
-          w[i] = *reinterpret_cast<const uint4*>(static_cast<const int8_t*>(pool) +
-                                                 ((static_cast<size_t>(page) * a.Hkv + s.h) * a.S + t % a.S) * D + 16 * (x % kCpt));
-      }
-    }
-  }
-  static __device__ __forceinline__ void widen(uint8_t* dst, int tid, const uint4 (&w)[kPieces]) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int x = tid + kFillThreads * i, r = x / kCpt, c = 2 * (x % kCpt);  // two 16-byte pieces of 16-bit values
+      const int r = r0 + i * kRowsPer;
       uint4 lo, hi;
       widen4(w[i].x, lo.x, lo.y);
       widen4(w[i].y, lo.z, lo.w);
       widen4(w[i].z, hi.x, hi.y);
       widen4(w[i].w, hi.z, hi.w);
-      uint8_t* row = dst + (c >> 3) * Lay::kHalf + r * 128;
+      uint8_t* row = tile + (c >> 3) * Lay::kHalf + r * 128;
       *reinterpret_cast<uint4*>(row + (((c & 7) ^ (r & 7)) << 4)) = lo;
       *reinterpret_cast<uint4*>(row + ((((c & 7) + 1) ^ (r & 7)) << 4)) = hi;
     }
   }
-  static __device__ bool convert(const ChunkArgs& a, M& m, uint8_t* smem, int tid) {
-    const Waiter wait{a.err};
-    uint32_t c = 0, qc = 0;
+
+  static __device__ void load(const ChunkArgs& a, M& m, uint8_t* smem, int tid, int lane) {
+    // as in softmax(): after a wait that ran out the others are skipped
+    bool dead = false;
+    const auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
+    };
+    const uint32_t sm = smem_u32(smem);
+    const int s_log2 = 31 - __clz(a.S);
+    uint32_t ki = 0, vi = 0, kr = 0, vr = 0;  // stage and round of the rings
+    // int8: tiles copied, not yet widened (at most two: a K and a V)
+    uint32_t kw = 0, vw = 0;
+    int open = 0;
+    const auto finish = [&](bool is_v) {
+      uint8_t* tile = smem + (is_v ? Lay::v_off + vw * Lay::kTileBytes : Lay::k_off + kw * Lay::kTileBytes);
+      widen(tile, tid);  // a thread widens what it copied
+      fence_proxy_async();
+      mbar_arrive(is_v ? &m.v_full[vw] : &m.k_full[kw]);
+      uint32_t& w = is_v ? vw : kw;
+      if (++w == static_cast<uint32_t>(is_v ? VST : KST)) w = 0;
+    };
     SegIter it(a, m.plan);
     Seg s;
-    uint4 wk[kPieces], wv[kPieces];
     while (it.next(a, s)) {
-      if (tid == 0 && !load_q(a, m, smem, s, qc)) return false;  // the others run out at the next empty stage
-      ++qc;
       const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
-      fetch(a, s, a.k_pool, s.k0, tid, wk);
-      fetch(a, s, a.v_pool, s.k0, tid, wv);
+      int page = page_of(a, s, pt, s.k0, lane);
       for (int k = s.k0; k < s.k1; ++k) {
-        const uint32_t ks = c % KST, vs = c % VST;
-        float sk = 0.f, sv = 0.f;  // of the step's token tid
-        {
-          const int t = k * kTile + tid;
-          if (t <= s.last) {
-            const int page = pt[t / a.S];
-            if (page >= 0 && page < a.n_phys) {
-              const size_t at = (static_cast<size_t>(page) * a.Hkv + s.h) * a.S + t % a.S;
-              sk = __half2float(a.k_scale[at]) * a.scale_log2;
-              sv = __half2float(a.v_scale[at]) * kVScale;
-            }
+        const int ahead = page_of(a, s, pt, k + 1, lane);
+        if (kr > 0) wait(&m.k_empty[ki], kr - 1);
+        const uint32_t kt = sm + Lay::k_off + ki * Lay::kTileBytes;
+        issue_copies(a, s, a.k_pool, k, page, s_log2, tid, kt + (I8 ? Lay::kTileBytes / 2 : 0));
+        if constexpr (I8) {
+          copy_commit();
+          if (open == 2) {  // the K of the step before
+            copy_wait<2>();
+            finish(false);
+            --open;
+          }
+          ++open;
+        } else {
+          copy_arrive(&m.k_full[ki]);
+        }
+        if (++ki == KST) ki = 0, ++kr;
+        float sk = 0.f, sv = 0.f;  // int8: scales of the step's token tid
+        if constexpr (I8) {
+          const int pg = __shfl_sync(0xffffffffu, page, tid >> s_log2);
+          if (pg >= 0 && k * kTile + tid < s.sq.L) {
+            const size_t at = ((static_cast<size_t>(pg) * a.Hkv + s.h) << s_log2) + (tid & (a.S - 1));
+            sk = __half2float(a.k_scale[at]) * a.scale_log2;
+            sv = __half2float(a.v_scale[at]) * kVScale;
           }
         }
-        if (c >= KST && !wait(&m.k_empty[ks], c / KST - 1)) return false;
-        widen(smem + Lay::k_off + ks * Lay::kTileBytes, tid, wk);
-        fence_proxy_async();
-        mbar_arrive(&m.k_full[ks]);
-        fetch(a, s, a.k_pool, k + 1, tid, wk);
-        if (c >= VST && !wait(&m.v_empty[vs], c / VST - 1)) return false;
-        m.scales[vs][0][tid] = sk;
-        m.scales[vs][1][tid] = sv;
-        widen(smem + Lay::v_off + vs * Lay::kTileBytes, tid, wv);
-        fence_proxy_async();
-        mbar_arrive(&m.v_full[vs]);
-        fetch(a, s, a.v_pool, k + 1, tid, wv);
-        ++c;
+        if (vr > 0) wait(&m.v_empty[vi], vr - 1);
+        const uint32_t vt = sm + Lay::v_off + vi * Lay::kTileBytes;
+        issue_copies(a, s, a.v_pool, k, page, s_log2, tid, vt + (I8 ? Lay::kTileBytes / 2 : 0));
+        if constexpr (I8) {
+          copy_commit();
+          m.scales[vi][0][tid] = sk;
+          m.scales[vi][1][tid] = sv;
+          if (open == 2) {
+            copy_wait<2>();
+            finish(true);
+            --open;
+          }
+          ++open;
+        } else {
+          copy_arrive(&m.v_full[vi]);
+        }
+        if (++vi == VST) vi = 0, ++vr;
+        page = ahead;
       }
     }
-    return true;
+    if constexpr (I8) {
+      if (open == 2) {
+        copy_wait<1>();
+        finish(false);
+        copy_wait<0>();
+        finish(true);
+      }
+    }
+    copy_commit();
+    copy_wait<0>();  // nothing is in flight when the CTA leaves
   }
 
   // ---- softmax ------------------------------------------------------------------------------------
@@ -646,47 +615,63 @@ struct Kernel {
         wait(&m.s_full[t], sc);
         ++sc;
         tc_fence_after();
-        uint32_t x[kTile];
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) tmem_ld32(x + c, tS + c);
-        tmem_wait_ld();
-        const auto f = [&](int c) { return __uint_as_float(x[c]); };
-        if constexpr (I8) {
-          const float* ks = m.scales[stage][0];
-#pragma unroll
-          for (int c = 0; c < kTile; c += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(ks + c);
-            const float2 u = unpack_f32x2(mul_f32x2(f32x2(f(c), f(c + 1)), f32x2(w.x, w.y)));
-            const float2 v = unpack_f32x2(mul_f32x2(f32x2(f(c + 2), f(c + 3)), f32x2(w.z, w.w)));
-            x[c] = __float_as_uint(u.x);
-            x[c + 1] = __float_as_uint(u.y);
-            x[c + 2] = __float_as_uint(v.x);
-            x[c + 3] = __float_as_uint(v.y);
-          }
-        }
+        // Half a row of logits in registers at a time: the maximum of the upper
+        // half, then of the lower, which stays; the upper is read again when
+        // its turn comes.  int8: logits times their key scales.
+        constexpr int kHalfTile = kTile / 2;
+        const float* ks = m.ones;
+        if constexpr (I8) ks = m.scales[stage][0];
         const int t0 = k * kTile;
-        if (t0 + kTile - 1 > pos_first || any_bad) {
-          // the step's last tokens are hidden from some row, or a page is bad (per 16 tokens)
-          unsigned bad16 = 0;
-          if (any_bad)
-            for (int c = 0; c < kTile; c += 16)
-              if (t0 + c <= s.last) {
-                const int page = pt[(t0 + c) / a.S];
-                if (page < 0 || page >= a.n_phys) bad16 |= 1u << (c / 16);
+        const bool masked = t0 + kTile - 1 > pos_first || any_bad;
+        uint32_t x[kHalfTile];
+        float top = -INFINITY;
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+          const uint32_t at = tS + half * kHalfTile;
+          tmem_ld32(x, at);
+          tmem_ld32(x + 32, at + 32);
+          tmem_wait_ld();
+          const auto f = [&](int c) { return __uint_as_float(x[c]); };
+          if (masked) {
+            // the step's last tokens are hidden from some row, or a page is bad (per 16 tokens)
+            unsigned bad16 = 0;
+            if (any_bad)
+              for (int c = 0; c < kHalfTile; c += 16) {
+                const int tok = t0 + half * kHalfTile + c;
+                if (tok <= s.last) {
+                  const int page = pt[tok / a.S];
+                  if (page < 0 || page >= a.n_phys) bad16 |= 1u << (c / 16);
+                }
               }
-          const int lim = pos - t0;
+            const int lim = pos - t0 - half * kHalfTile;
 #pragma unroll
-          for (int c = 0; c < kTile; ++c)
-            if (c > lim || ((bad16 >> (c / 16)) & 1u)) x[c] = 0xff800000u;  // -inf
+            for (int c = 0; c < kHalfTile; ++c) {
+              if constexpr (I8) x[c] = __float_as_uint(f(c) * ks[half * kHalfTile + c]);
+              if (c > lim || ((bad16 >> (c / 16)) & 1u)) x[c] = 0xff800000u;  // -inf
+            }
+            tmem_st32(at, x);
+            tmem_st32(at + 32, x + 32);
+          }
+          float mx[4] = {top, top, top, top};  // chains that do not wait for one another
+          if (I8 && !masked) {
+#pragma unroll
+            for (int c = 0; c < kHalfTile; c += 8) {
+              const float4 u = *reinterpret_cast<const float4*>(ks + half * kHalfTile + c);
+              const float4 w = *reinterpret_cast<const float4*>(ks + half * kHalfTile + c + 4);
+              mx[0] = fmaxf(fmaxf(mx[0], f(c) * u.x), f(c + 4) * w.x);
+              mx[1] = fmaxf(fmaxf(mx[1], f(c + 1) * u.y), f(c + 5) * w.y);
+              mx[2] = fmaxf(fmaxf(mx[2], f(c + 2) * u.z), f(c + 6) * w.z);
+              mx[3] = fmaxf(fmaxf(mx[3], f(c + 3) * u.w), f(c + 7) * w.w);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kHalfTile; c += 8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], f(c + i)), f(c + 4 + i));
+          }
+          top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         }
-        float mx[4];  // chains that do not wait for one another
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(f(c), f(c + 4));
-#pragma unroll
-        for (int c = 8; c < kTile; c += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], f(c + i)), f(c + 4 + i));
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (I8 && masked) ks = m.ones;  // the logits went back with their scales
         if constexpr (!I8) top *= a.scale_log2;
         const bool raise = top > row.m + kSlack;  // -inf + kSlack = -inf: the first finite logit
         if (__any_sync(0xffffffffu, raise)) {
@@ -695,7 +680,7 @@ struct Kernel {
           row.m = mn;
           row.l *= factor;
           if (k >= s.k0 + step) {  // O holds earlier steps (all done: S of this step was issued after them)
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
               tmem_ld32(o, tO + c);
@@ -709,29 +694,36 @@ struct Kernel {
         const float mm = row.m == -INFINITY ? 0.f : row.m;
         const uint64_t nm = f32x2(-mm, -mm), sc2 = f32x2(a.scale_log2, a.scale_log2);
         uint64_t l0 = f32x2(0.f, 0.f), l1 = l0;
+        if (masked) tmem_wait_st();
 #pragma unroll
-        for (int c0 = 0; c0 < kTile; c0 += 32) {
-          uint32_t w[16];
+        for (int half = 0; half < 2; ++half) {
+          if (half == 1) tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int c = c0 + 2 * i;
-            const uint64_t z = f32x2(f(c), f(c + 1));
-            const float2 e = unpack_f32x2(I8 ? add_f32x2(z, nm) : fma_f32x2(z, sc2, nm));
-            float2 p = make_float2(ex2(e.x), ex2(e.y));
-            if (i & 1) l1 = add_f32x2(l1, f32x2(p.x, p.y)); else l0 = add_f32x2(l0, f32x2(p.x, p.y));
-            if constexpr (I8) {
-              const float2 vs = *reinterpret_cast<const float2*>(&m.scales[stage][1][c]);
-              p.x *= vs.x;
-              p.y *= vs.y;
+          for (int q = 0; q < 2; ++q) {
+            const int c0 = half * kHalfTile + 32 * q;  // first token of these 32
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t z = f32x2(__uint_as_float(x[32 * q + 2 * i]), __uint_as_float(x[32 * q + 2 * i + 1]));
+              uint64_t mul = sc2;
+              if constexpr (I8) mul = *reinterpret_cast<const uint64_t*>(ks + c0 + 2 * i);
+              const float2 e = unpack_f32x2(fma_f32x2(z, mul, nm));
+              float2 p = make_float2(ex2(e.x), ex2(e.y));
+              if (i & 1) l1 = add_f32x2(l1, f32x2(p.x, p.y)); else l0 = add_f32x2(l0, f32x2(p.x, p.y));
+              if constexpr (I8) {
+                const float2 vs = *reinterpret_cast<const float2*>(&m.scales[stage][1][c0 + 2 * i]);
+                p.x *= vs.x;
+                p.y *= vs.y;
+              }
+              w[i] = pack2<TQ>(p.x, p.y);
             }
-            w[i] = pack2<TQ>(p.x, p.y);
+            // the lower half's logits are all in registers, the upper half's lie beyond P
+            tmem_st16(tS + c0 / 2, w);
+            if (half == 0) tmem_ld32(x + 32 * q, tS + kHalfTile + 32 * q);
           }
-          tmem_st16(tS + c0 / 2, w);
-          if (c0 % (kTile / 2)) {
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&m.p_full[t][c0 / (kTile / 2)]);
-          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&m.p_full[t][half]);
         }
         const float2 s0 = unpack_f32x2(l0), s1 = unpack_f32x2(l1);
         row.l += (s0.x + s0.y) + (s1.x + s1.y);
@@ -872,26 +864,27 @@ __global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const
   M& m = *reinterpret_cast<M*>(smem + Lay::misc);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    const uint32_t fill = K::I8 ? K::kFillThreads : 1;
     mbar_init(&m.q_full, 1);
-    mbar_init(&m.q_empty, 1);
+    mbar_init(&m.q_empty, 2);
     for (int i = 0; i < K::KST; ++i) {
-      mbar_init(&m.k_full[i], fill);
-      mbar_init(&m.k_empty[i], 1);
+      mbar_init(&m.k_full[i], K::kLoadThreads);
+      mbar_init(&m.k_empty[i], 2);
     }
     for (int i = 0; i < K::VST; ++i) {
-      mbar_init(&m.v_full[i], fill);
-      mbar_init(&m.v_empty[i], 1);
+      mbar_init(&m.v_full[i], K::kLoadThreads);
+      mbar_init(&m.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.s_full[i], 1);
       mbar_init(&m.p_full[i][0], 128);
       mbar_init(&m.p_full[i][1], 128);
       mbar_init(&m.o_full[i], 1);
+      mbar_init(&m.turn[i], 1);
+      mbar_init(&m.drain[i], 1);
     }
-    mbar_init(&m.drain, 1);
     mbar_fence_init();
   }
+  if (K::I8 && threadIdx.x < kTile) m.ones[threadIdx.x] = 1.f;
   if (warp == K::kMmaWarp) tmem_alloc(&m.tmem, kTmemCols);
   pdl_wait();
   if (warp == 0) make_plan(a, &m.plan, lane);
@@ -904,19 +897,23 @@ __global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const
     regs_up<K::kRegsSoftmax>();
     K::softmax(a, m, tmem, warp, lane);
   } else {
-    if (K::I8 && warp >= 12) regs_down<K::kRegsMma>(); else regs_down<K::kRegsFill>();  // whole warpgroups
-    if (warp == K::kMmaWarp) {
-      const bool ok = K::issue(a, m, smem_u32(smem), tmem);
-      if (!ok) {
-        // products in flight end before TMEM goes back
-        if (elect_one()) mma_commit(&m.drain);
+    if (warp < K::kMmaWarp) {
+      regs_down<K::kRegsLoad>();
+      K::load(a, m, smem, threadIdx.x - K::kLoadWarp * 32, lane);
+    } else {
+      regs_down<K::kRegsIssue>();
+      if (warp == K::kQWarp) {
+        if (lane == 0) K::load_q(a, m, smem);
         __syncwarp();
-        mbar_wait_bounded(&m.drain, 0);
+      } else if (warp < K::kQWarp) {
+        const int t = warp - K::kMmaWarp;
+        if (!K::issue(a, m, smem_u32(smem), tmem, t)) {
+          // products in flight end before TMEM goes back
+          if (elect_one()) mma_commit(&m.drain[t]);
+          __syncwarp();
+          mbar_wait_bounded(&m.drain[t], 0);
+        }
       }
-    } else if constexpr (K::I8) {
-      if (warp < 12) K::convert(a, m, smem, threadIdx.x - K::kFillWarp * 32);
-    } else if (warp <= K::kFillWarp + 1) {
-      K::fill(a, m, smem, warp == K::kFillWarp + 1, lane);
     }
   }
   pdl_trigger();
@@ -956,20 +953,6 @@ bool make_q_tmap(CUtensorMap* map, const void* q, const spg_params& p, int total
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// K pool: 64 channels of one page of one kv-head per box
-bool make_half_tmap(CUtensorMap* map, const void* pool, const spg_params& p) {
-  const auto fn = encoder();
-  const long long rows = static_cast<long long>(p.num_phys_pages) * p.num_kv_heads * p.page_size;
-  if (!fn || rows > 0x7fffffffLL) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.head_dim), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.head_dim) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(p.page_size)};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(map, p.kv_dtype == SPG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int part_rows(const spg_params& p, int total_q) {
   const long long rows = static_cast<long long>(total_q) * (p.num_q_heads / p.num_kv_heads);
@@ -980,13 +963,6 @@ template <typename T, typename TQ, int D>
 cudaError_t chunk_typed(const spg_params& p, ChunkArgs& a, const void* q, cudaStream_t st) {
   using K = Kernel<T, TQ, D>;
   if (!make_q_tmap(&a.tmq, q, p, a.total_q)) return cudaErrorNotSupported;
-  if constexpr (!K::I8) {
-    const long long rows = static_cast<long long>(p.num_phys_pages) * p.num_kv_heads * p.page_size;
-    bool whole = false;
-    if (!make_half_tmap(&a.tmk, a.k_pool, p) || !make_kv_tmap(&a.tmv, a.v_pool, p.kv_dtype, rows, D, p.page_size, &whole))
-      return cudaErrorNotSupported;
-    a.v_whole = whole ? 1 : 0;
-  }
   const auto kern = k_chunk<T, TQ, D>;
   const size_t smem = 1024 + K::Lay::misc + sizeof(typename K::M);
   const cudaError_t e = ensure_smem(kern, smem);
