@@ -37,6 +37,7 @@ static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255);
 //   flags     [4][B*Hkv] int32 (scheduled step)
 //   slices    [B*Hkv][n_sel] int2 (scheduled step)
 //   iq        [B*Hkv][8] int32 (scheduled step, sketch selector)
+//   mass      arrival counters, then partial sums (attention mass)
 size_t workspace_bytes(const spg_params& p) {
   const size_t B = p.batch, Hq = p.num_q_heads, Hkv = p.num_kv_heads;
   const size_t d = p.head_dim, MP = p.max_pages_per_seq;
@@ -51,6 +52,7 @@ size_t workspace_bytes(const spg_params& p) {
   off += align256(sizeof(int32_t) * 4 * B * Hkv);        // per-unit flags
   off += align256(sizeof(int2) * B * Hkv * n_sel);       // selection slices
   off += align256(sizeof(int32_t) * 8 * B * Hkv);        // index queries
+  off += align256(mass_workspace_bytes());               // parts of attention mass items
   return off;
 }
 
@@ -81,6 +83,9 @@ Workspace carve_workspace(const spg_params& p, void* ws) {
   w.slices = reinterpret_cast<int2*>(base + off);
   off += align256(sizeof(int2) * B * Hkv * n_sel);
   w.iq = reinterpret_cast<int32_t*>(base + off);
+  off += align256(sizeof(int32_t) * 8 * B * Hkv);
+  w.mass_counters = reinterpret_cast<int32_t*>(base + off);
+  w.mass_part = reinterpret_cast<float*>(base + off + kMassCounterBytes);
   return w;
 }
 

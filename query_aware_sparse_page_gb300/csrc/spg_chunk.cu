@@ -38,171 +38,67 @@
 //
 // Roundings: P to the 16-bit type (as the products take it) and the result;
 // everything else is fp32.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 
-#include "spg_chunk_common.cuh"
+#include "spg_deal.cuh"
 #include "spg_internal.h"
-#include "spg_tcgen05.cuh"
+#include "spg_tile_load.cuh"
 
 namespace spg {
 namespace {
 
-constexpr int kTile = 128;           // rows of a Q tile, tokens of a step
-constexpr int kItemRows = 2 * kTile;
-constexpr int kMaxCtas = 160;        // shares of the plan (one per SM)
-constexpr int kMaxParts = 32;        // most parts an average item is split into
+constexpr int kItemRows = 2 * kTile;  // rows of a Q tile, and tokens of a step: kTile
 constexpr uint32_t kTmemCols = 512;  // S0 S1 O0 O1, 128 columns each
 
+// ---- the plan -----------------------------------------------------------------------
+// An item is 256 rows, a step 128 of the tokens its rows see.
+struct RowItems : ChunkShape {
+  __device__ int tokens() const { return kItemRows / G; }  // new tokens of an item
+  __device__ int items(const ChunkSeq& s) const { return (s.n + tokens() - 1) / tokens(); }
+  // the first m items: sum of ceil((pos0 + i q) / 128), the last one ends with the sequence
+  __device__ long long steps(const ChunkSeq& s, int m) const {
+    const int q = tokens(), full = min(m, s.n / q);
+    long long sum = 0;
+    if (q >= kTile) {
+      sum = static_cast<long long>(full) * ((s.pos0 + kTile - 1) / kTile) + static_cast<long long>(q / kTile) * full * (full + 1) / 2;
+    } else {
+      const int per = kTile / q;
+      for (int r = 1; r <= per && r <= full; ++r) {
+        const long long cnt = (full - r) / per + 1;
+        sum += cnt * ((s.pos0 + r * q + kTile - 1) / kTile) + cnt * (cnt - 1) / 2;
+      }
+    }
+    return m > full ? sum + (s.L + kTile - 1) / kTile : sum;
+  }
+};
+struct Seg : Part {
+  int row0, n_rows, last;  // rows of the sequence; the last token any of them sees
+};
+struct SegIter : PartIter<RowItems> {
+  using PartIter::PartIter;
+  __device__ bool next(Seg& s) {
+    if (!PartIter::next(s)) return false;
+    const int q = sh.tokens();
+    s.row0 = s.item * kItemRows;
+    s.n_rows = min(kItemRows, s.sq.n * sh.G - s.row0);
+    s.last = s.sq.pos0 + min((s.item + 1) * q, s.sq.n) - 1;
+    return true;
+  }
+};
+
 struct ChunkArgs {
+  RowItems sh;
   CUtensorMap tmq;
   const void *k_pool, *v_pool;
   const __half *k_scale, *v_scale;
-  const int32_t *q_start, *page_table, *seq_lens;
+  const int32_t* page_table;
   void* out;
   float* lse;
   int32_t *err, *counters;
   float* part;  // [2 * CTAs][D + 2][part_rows]: O by channel, then m and l, so that a warp's rows are neighbours
-  int B, Hkv, G, S, MP, n_phys, total_q, part_rows;
+  int Hkv, G, S, MP, n_phys, part_rows;
   float scale_log2;
-};
-
-// ---- the plan -----------------------------------------------------------------------
-// sum of ceil((pos0 + i q) / 128) for i = 1 .. m: the steps of a sequence's
-// first m full items, q = 256 / G new tokens each
-__device__ __forceinline__ long long full_item_steps(int pos0, int q, int m) {
-  if (q >= kTile) return static_cast<long long>(m) * ((pos0 + kTile - 1) / kTile) + static_cast<long long>(q / kTile) * m * (m + 1) / 2;
-  long long sum = 0;
-  const int per = kTile / q;
-  for (int r = 1; r <= per && r <= m; ++r) {
-    const long long cnt = (m - r) / per + 1;
-    sum += cnt * ((pos0 + r * q + kTile - 1) / kTile) + cnt * (cnt - 1) / 2;
-  }
-  return sum;
-}
-// steps of the sequence's first `items` items (one kv-head)
-__device__ __forceinline__ long long item_steps(const ChunkSeq& s, int q, int items) {
-  const int full = min(items, s.n / q);
-  long long sum = full_item_steps(s.pos0, q, full);
-  if (items > full) sum += (s.L + kTile - 1) / kTile;
-  return sum;
-}
-
-struct Plan {
-  long long total, lo, hi;  // steps in all, and this CTA's
-  long long item_first;     // first step of the item that lo lies in
-  int ctas, b, h, item;
-};
-
-// one whole warp
-__device__ void make_plan(const ChunkArgs& a, Plan* out, int lane) {
-  const int q = kItemRows / a.G;
-  long long total = 0, items = 0;
-  int32_t bad = 0;
-  for (int b = lane; b < a.B; b += 32) {
-    const ChunkSeq s = chunk_seq(a.q_start, a.seq_lens, b, a.total_q, a.MP * a.S, bad);
-    const int ni = (s.n + q - 1) / q;
-    total += a.Hkv * item_steps(s, q, ni);
-    items += static_cast<long long>(a.Hkv) * ni;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    items += __shfl_xor_sync(0xffffffffu, items, o);
-  }
-  if (bad && blockIdx.x == 0) record_error(a.err, bad);
-  Plan p{};
-  p.total = total;
-  long long n = min(static_cast<long long>(gridDim.x), total);
-  n = min(n, items * kMaxParts);
-  p.ctas = static_cast<int>(n);
-  const int c = blockIdx.x;
-  if (c >= n) {
-    if (lane == 0) *out = p;  // lo = hi = 0: nothing to do
-    return;
-  }
-  p.lo = c * total / n;
-  p.hi = (c + 1) * total / n;
-  long long base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    long long w = 0;
-    ChunkSeq s{};
-    if (b < a.B) {
-      s = chunk_seq(a.q_start, a.seq_lens, b, a.total_q, a.MP * a.S, bad);
-      w = a.Hkv * item_steps(s, q, (s.n + q - 1) / q);
-    }
-    long long incl = w;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const long long first = base + incl - w;
-    if (p.lo >= first && p.lo < first + w) {  // one lane
-      const long long per_head = w / a.Hkv;
-      p.b = b;
-      p.h = static_cast<int>((p.lo - first) / per_head);
-      const long long rest = (p.lo - first) % per_head;
-      int x = 0, y = (s.n + q - 1) / q - 1;  // the last item that starts at or before rest
-      while (x < y) {
-        const int mid = (x + y + 1) >> 1;
-        if (item_steps(s, q, mid) <= rest) x = mid; else y = mid - 1;
-      }
-      p.item = x;
-      p.item_first = first + p.h * per_head + item_steps(s, q, x);
-      *out = p;
-    }
-    base += __shfl_sync(0xffffffffu, incl, 31);
-    if (base > p.lo) break;
-  }
-}
-
-// A CTA's share of one item: steps [k0, k1) of its nk.
-struct Seg {
-  ChunkSeq sq;
-  int b, h, row0, n_rows, last, k0, k1, nk;
-  long long item_first;
-};
-struct SegIter {
-  long long pos, hi, item_first;
-  int b, h, item;
-  ChunkSeq sq;
-  __device__ SegIter(const ChunkArgs& a, const Plan& p) : pos(p.lo), hi(p.hi), item_first(p.item_first), b(p.b), h(p.h), item(p.item) {
-    if (pos < hi) load(a);
-  }
-  __device__ void load(const ChunkArgs& a) {
-    int32_t bad = 0;
-    sq = chunk_seq(a.q_start, a.seq_lens, b, a.total_q, a.MP * a.S, bad);
-  }
-  __device__ bool next(const ChunkArgs& a, Seg& s) {
-    if (pos >= hi) return false;
-    const int q = kItemRows / a.G;
-    s.sq = sq;
-    s.b = b;
-    s.h = h;
-    s.row0 = item * kItemRows;
-    s.n_rows = min(kItemRows, sq.n * a.G - s.row0);
-    s.last = sq.pos0 + min((item + 1) * q, sq.n) - 1;  // the last token any row sees
-    s.nk = s.last / kTile + 1;
-    s.item_first = item_first;
-    s.k0 = static_cast<int>(pos - item_first);
-    s.k1 = static_cast<int>(min(static_cast<long long>(s.nk), hi - item_first));
-    pos = item_first + s.k1;
-    if (s.k1 == s.nk) {
-      item_first += s.nk;
-      if (++item * q >= sq.n) {
-        item = 0;
-        if (++h == a.Hkv) {
-          h = 0;
-          if (pos < hi) do { ++b; load(a); } while (sq.n == 0);
-        }
-      }
-    }
-    return true;
-  }
 };
 
 // ---- shared memory ---------------------------------------------------------------------
@@ -224,25 +120,6 @@ struct Misc {
   float ml[kTile][2];                            // stream 1's m and l, joined by stream 0
   alignas(16) float ones[I8 ? kTile : 1];
   alignas(16) float scales[I8 ? VST : 1][2][I8 ? kTile : 1];  // int8: scale * key scale, 16 * value scale of a step's tokens
-};
-
-// A wait: false, and recorded, when it ran out (as mbar_wait_bounded, in few
-// instructions: the issuing warp's path has five of them per step).
-struct Waiter {
-  int32_t* err;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t phase) const {
-    if (mbar_try_wait(bar, phase & 1)) return true;
-    uint64_t t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-#pragma unroll 1
-    for (int i = 0; i < (1 << 22); ++i) {
-      if (mbar_try_wait(bar, phase & 1)) return true;
-      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-      if (t - t0 > 100ull * 1000 * 1000) break;
-    }
-    record_error(err, SPG_DEVERR_TIMEOUT);
-    return false;
-  }
 };
 
 template <typename T, typename TQ, int D>
@@ -309,9 +186,9 @@ struct Kernel {
         mma_ts(tO, tS + 8 * ks, v + ks * (16 * 128 >> 4), idO, acc || ks > 0);
       }
     };
-    SegIter it(a, m.plan);
+    SegIter it(a.sh, m.plan);
     Seg s;
-    while (uniform(it.next(a, s))) {
+    while (uniform(it.next(s))) {
       const int n = uniform(s.k1 - s.k0);
       // two tiles of rows: both streams take every step; one: alternate ones
       const int step = uniform(s.n_rows) > kTile ? 1 : 2, qt = step == 1 ? t : 0;
@@ -383,9 +260,9 @@ struct Kernel {
   static __device__ void load_q(const ChunkArgs& a, M& m, uint8_t* smem) {
     const Waiter wait{a.err};
     uint32_t c = 0;
-    SegIter it(a, m.plan);
+    SegIter it(a.sh, m.plan);
     Seg s;
-    for (; it.next(a, s); ++c) {
+    for (; it.next(s); ++c) {
       if (c > 0 && !wait(&m.q_empty, c - 1)) return;
       const int tiles = s.n_rows > kTile ? 2 : 1;
       mbar_arrive_expect_tx(&m.q_full, tiles * Lay::kTileBytes);
@@ -397,81 +274,7 @@ struct Kernel {
   }
 
   // ---- loads ----------------------------------------------------------------------------------
-  // A thread's pieces of a tile are one 16-byte column of every kPieces-th row.
-  static constexpr int kCpr = D * static_cast<int>(sizeof(T)) / 16;  // pieces of a row
-  static constexpr int kRowsPer = kLoadThreads / kCpr;              // rows of the threads together
-  static constexpr int kPieces = kTile / kRowsPer;
-
-  // pages of step k, one per lane
-  static __device__ __forceinline__ int page_of(const ChunkArgs& a, const Seg& s, const int32_t* pt, int k, int lane) {
-    const int lp = k * (kTile / a.S) + lane;
-    if (lane >= kTile / a.S || k >= s.k1 || lp * a.S > s.last) return -1;
-    const int page = pt[lp];
-    return page >= 0 && page < a.n_phys ? page : -1;
-  }
-  static __device__ __forceinline__ void issue_copies(const ChunkArgs& a, const Seg& s, const void* pool, int k, int page, int s_log2,
-                                                      int tid, uint32_t dst) {
-    const int c = tid % kCpr, r0 = tid / kCpr;
-    const uint8_t* base = static_cast<const uint8_t*>(pool) + c * 16;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int r = r0 + i * kRowsPer;
-      const int pg = __shfl_sync(0xffffffffu, page, r >> s_log2);
-      const bool live = pg >= 0 && k * kTile + r < s.sq.L;
-      const size_t row = (((static_cast<size_t>(live ? pg : 0) * a.Hkv + s.h) << s_log2) + (r & (a.S - 1)));
-      uint32_t to;
-      if constexpr (I8)
-        to = r * D + c * 16;
-      else
-        to = (c >> 3) * Lay::kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-      copy16(dst + to, base + row * (D * sizeof(T)), live);
-    }
-  }
-
-  // four bytes -> two pairs, exact
-  static __device__ __forceinline__ void widen4(uint32_t r, uint32_t& lo, uint32_t& hi) {
-    const uint32_t u = r ^ 0x80808080u;
-    if constexpr (std::is_same<TQ, __half>::value) {
-      // the byte under an exponent byte is 1024 + code + 128
-      uint32_t x, y;
-      asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(x) : "r"(u), "r"(0x64646464u));
-      asm("prmt.b32 %0, %1, %2, 0x4342;" : "=r"(y) : "r"(u), "r"(0x64646464u));
-      const __half2 bias = __floats2half2_rn(1152.f, 1152.f);
-      const __half2 hx = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
-      const __half2 hy = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
-      lo = *reinterpret_cast<const uint32_t*>(&hx);
-      hi = *reinterpret_cast<const uint32_t*>(&hy);
-    } else {
-      float f[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // 2^23 + code + 128
-        f[i] = __uint_as_float(0x4b000000u | ((u >> (8 * i)) & 0xffu)) - 8388736.f;
-      lo = pack2<TQ>(f[0], f[1]);
-      hi = pack2<TQ>(f[2], f[3]);
-    }
-  }
-  // int8: the codes in the tile's upper half become the tile
-  static __device__ __forceinline__ void widen(uint8_t* tile, int tid) {
-    uint4 w[kPieces];
-    const uint8_t* raw = tile + Lay::kTileBytes / 2;
-    const int x = tid % kCpr, r0 = tid / kCpr, c = 2 * x;  // two 16-byte pieces of 16-bit values
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) w[i] = *reinterpret_cast<const uint4*>(raw + (r0 + i * kRowsPer) * D + x * 16);
-    bar_sync(3, kLoadThreads);  // every code is in a register
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int r = r0 + i * kRowsPer;
-      uint4 lo, hi;
-      widen4(w[i].x, lo.x, lo.y);
-      widen4(w[i].y, lo.z, lo.w);
-      widen4(w[i].z, hi.x, hi.y);
-      widen4(w[i].w, hi.z, hi.w);
-      uint8_t* row = tile + (c >> 3) * Lay::kHalf + r * 128;
-      *reinterpret_cast<uint4*>(row + (((c & 7) ^ (r & 7)) << 4)) = lo;
-      *reinterpret_cast<uint4*>(row + ((((c & 7) + 1) ^ (r & 7)) << 4)) = hi;
-    }
-  }
-
+  using Tiles = TileLoader<T, TQ, D>;
   static __device__ void load(const ChunkArgs& a, M& m, uint8_t* smem, int tid, int lane) {
     // as in softmax(): after a wait that ran out the others are skipped
     bool dead = false;
@@ -486,22 +289,22 @@ struct Kernel {
     int open = 0;
     const auto finish = [&](bool is_v) {
       uint8_t* tile = smem + (is_v ? Lay::v_off + vw * Lay::kTileBytes : Lay::k_off + kw * Lay::kTileBytes);
-      widen(tile, tid);  // a thread widens what it copied
+      Tiles::widen(tile, tid, 3);  // a thread widens what it copied
       fence_proxy_async();
       mbar_arrive(is_v ? &m.v_full[vw] : &m.k_full[kw]);
       uint32_t& w = is_v ? vw : kw;
       if (++w == static_cast<uint32_t>(is_v ? VST : KST)) w = 0;
     };
-    SegIter it(a, m.plan);
+    SegIter it(a.sh, m.plan);
     Seg s;
-    while (it.next(a, s)) {
+    while (it.next(s)) {
       const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
-      int page = page_of(a, s, pt, s.k0, lane);
+      const auto pages = [&](int k) { return k < s.k1 ? Tiles::page_of(pt, k * kTile, s.last + 1, a.S, a.n_phys, lane) : -1; };
+      int page = pages(s.k0);
       for (int k = s.k0; k < s.k1; ++k) {
-        const int ahead = page_of(a, s, pt, k + 1, lane);
+        const int ahead = pages(k + 1);
         if (kr > 0) wait(&m.k_empty[ki], kr - 1);
-        const uint32_t kt = sm + Lay::k_off + ki * Lay::kTileBytes;
-        issue_copies(a, s, a.k_pool, k, page, s_log2, tid, kt + (I8 ? Lay::kTileBytes / 2 : 0));
+        Tiles::copy(a.k_pool, a.Hkv, s.h, s_log2, k * kTile, s.sq.L, page, tid, sm + Lay::k_off + ki * Lay::kTileBytes);
         if constexpr (I8) {
           copy_commit();
           if (open == 2) {  // the K of the step before
@@ -524,8 +327,7 @@ struct Kernel {
           }
         }
         if (vr > 0) wait(&m.v_empty[vi], vr - 1);
-        const uint32_t vt = sm + Lay::v_off + vi * Lay::kTileBytes;
-        issue_copies(a, s, a.v_pool, k, page, s_log2, tid, vt + (I8 ? Lay::kTileBytes / 2 : 0));
+        Tiles::copy(a.v_pool, a.Hkv, s.h, s_log2, k * kTile, s.sq.L, page, tid, sm + Lay::v_off + vi * Lay::kTileBytes);
         if constexpr (I8) {
           copy_commit();
           m.scales[vi][0][tid] = sk;
@@ -584,9 +386,9 @@ struct Kernel {
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t tS = lanes + t * 128, tO = lanes + 256 + t * 128;
     uint32_t sc = 0, oc = 0, vc = 0;
-    SegIter it(a, m.plan);
+    SegIter it(a.sh, m.plan);
     Seg s;
-    while (it.next(a, s)) {
+    while (it.next(s)) {
       const bool two = s.n_rows > kTile;
       const int r = two ? t * kTile + tile_row : tile_row;  // row of the item
       const int pos = s.sq.pos0 + (s.row0 + r) / a.G;
@@ -731,7 +533,7 @@ struct Kernel {
       vc += s.k1 - s.k0;
 
       // ---- the segment's end ----
-      const bool whole = s.k0 == 0 && s.k1 == s.nk;
+      const bool whole = s.whole();
       wait(&m.o_full[t], oc);
       float f0 = 1.f, f1 = 0.f;
       if (!two) {  // the rows' two streams
@@ -762,8 +564,7 @@ struct Kernel {
           f1 *= inv;
         }
         const size_t orow = live ? out_row(a, s, r) : 0;
-        const int c_slot = 2 * blockIdx.x + (s.k0 > 0 ? 0 : 1);
-        float* part = part_at(a, c_slot, live ? r : 0);
+        float* part = part_at(a, own_slot(s), live ? r : 0);
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -807,9 +608,8 @@ struct Kernel {
 
   // Counts a part of an item in; the last to arrive joins them all.
   static __device__ void join(const ChunkArgs& a, M& m, const Seg& s, int tid) {
-    const long long n = m.plan.ctas, total = m.plan.total;
-    const int c0 = static_cast<int>(((s.item_first + 1) * n - 1) / total);
-    const int c1 = static_cast<int>(((s.item_first + s.nk) * n - 1) / total);
+    const PartRange pr(m.plan, s);
+    const int c0 = pr.c0, c1 = pr.c1;
     __threadfence();
     bar_sync(1, 256);
     if (tid == 0) m.last = atomicAdd(&a.counters[c0], 1) == c1 - c0;
@@ -820,7 +620,7 @@ struct Kernel {
     const bool two = s.n_rows > kTile;
     const int r = two ? tid : tid % kTile, d0 = two ? 0 : tid / kTile * (D / 2), d1 = two ? D : d0 + D / 2;
     if (r < s.n_rows) {
-      const auto at = [&](int c) { return part_at(a, c == c0 ? 2 * c + 1 : 2 * c, r); };
+      const auto at = [&](int c) { return part_at(a, pr.slot(c), r); };
       float mm = -INFINITY, l = 0.f;
 #pragma unroll 4
       for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(at(c) + D * a.part_rows));
@@ -887,7 +687,7 @@ __global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const
   if (K::I8 && threadIdx.x < kTile) m.ones[threadIdx.x] = 1.f;
   if (warp == K::kMmaWarp) tmem_alloc(&m.tmem, kTmemCols);
   pdl_wait();
-  if (warp == 0) make_plan(a, &m.plan, lane);
+  if (warp == 0) make_plan(a.sh, &m.plan, a.err, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -927,32 +727,6 @@ __global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const
 
 // ---- host ------------------------------------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
-// q as [total_q][Hkv][G][d]; a box is 64 channels of 128 rows (token, head of the group)
-bool make_q_tmap(CUtensorMap* map, const void* q, const spg_params& p, int total_q) {
-  const auto fn = encoder();
-  if (!fn) return false;
-  const cuuint64_t d = p.head_dim, G = p.num_q_heads / p.num_kv_heads, Hkv = p.num_kv_heads;
-  const cuuint64_t dims[4] = {d, G, Hkv, static_cast<cuuint64_t>(total_q)};
-  const cuuint64_t strides[3] = {d * 2, G * d * 2, Hkv * G * d * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(kTile / G)};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, p.q_dtype == SPG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int part_rows(const spg_params& p, int total_q) {
   const long long rows = static_cast<long long>(total_q) * (p.num_q_heads / p.num_kv_heads);
@@ -962,7 +736,7 @@ int part_rows(const spg_params& p, int total_q) {
 template <typename T, typename TQ, int D>
 cudaError_t chunk_typed(const spg_params& p, ChunkArgs& a, const void* q, cudaStream_t st) {
   using K = Kernel<T, TQ, D>;
-  if (!make_q_tmap(&a.tmq, q, p, a.total_q)) return cudaErrorNotSupported;
+  if (!make_q_tmap(&a.tmq, q, p, a.sh.total_q, kTile)) return cudaErrorNotSupported;
   const auto kern = k_chunk<T, TQ, D>;
   const size_t smem = 1024 + K::Lay::misc + sizeof(typename K::M);
   const cudaError_t e = ensure_smem(kern, smem);
@@ -985,9 +759,14 @@ cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_
   a.v_pool = v_pool;
   a.k_scale = static_cast<const __half*>(k_scale);
   a.v_scale = static_cast<const __half*>(v_scale);
-  a.q_start = r.q_start;
+  a.sh.q_start = r.q_start;
+  a.sh.seq_lens = r.seq_lens;
+  a.sh.B = p.batch;
+  a.sh.Hkv = p.num_kv_heads;
+  a.sh.G = p.num_q_heads / p.num_kv_heads;
+  a.sh.total_q = r.total_q;
+  a.sh.max_tokens = p.max_pages_per_seq * p.page_size;
   a.page_table = r.page_table;
-  a.seq_lens = r.seq_lens;
   a.out = out;
   a.lse = lse;
   uint8_t* base = static_cast<uint8_t*>(ws);
@@ -995,13 +774,11 @@ cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_
   base += round256(workspace_bytes(p));
   a.counters = reinterpret_cast<int32_t*>(base);
   a.part = reinterpret_cast<float*>(base + round256(sizeof(int32_t) * kMaxCtas));
-  a.B = p.batch;
   a.Hkv = p.num_kv_heads;
   a.G = p.num_q_heads / p.num_kv_heads;
   a.S = p.page_size;
   a.MP = p.max_pages_per_seq;
   a.n_phys = p.num_phys_pages;
-  a.total_q = r.total_q;
   a.part_rows = part_rows(p, r.total_q);
   a.scale_log2 = (p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.head_dim))) * kLog2e;
 #define SPG_CHUNK(T, TQ) \

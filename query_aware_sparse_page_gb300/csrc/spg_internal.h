@@ -25,7 +25,11 @@ struct Workspace {
   int32_t* sched_flags;  // [4][B*Hkv] per-unit flags; zero between calls
   int2* slices;          // [B*Hkv][n_sel] (physical page, valid tokens) of the selection
   int32_t* iq;           // [B*Hkv][8] sketch index queries
+  int32_t* mass_counters;  // arrivals of an item's parts (spg_mass.cu); zero between calls
+  float* mass_part;        // their sums
 };
+constexpr size_t kMassCounterBytes = 2048;  // ahead of the sums
+size_t mass_workspace_bytes();
 
 size_t workspace_bytes(const spg_params& p);
 
@@ -39,6 +43,10 @@ size_t workspace_bytes(const spg_params& p);
 // described (dtype, alignment, size) or the encoder is unavailable.
 bool make_kv_tmap(CUtensorMap* map, const void* pool, int kv_dtype, long long rows, int head_dim,
                   int page_size, bool* whole_page);
+// Tensor map of q as [total_q][Hkv][G][head_dim]; a box is 64 channels of
+// `rows` rows (new token, head of the group) of one kv-head, rows past
+// total_q zeros.
+bool make_q_tmap(CUtensorMap* map, const void* q, const spg_params& p, int total_q, int rows);
 Workspace carve_workspace(const spg_params& p, void* ws);
 
 int n_sel_pages(const spg_params& p);

@@ -1,210 +1,471 @@
-// Attention weight received by every cached token (paged_attention_mass).
+// Attention weight received by every cached token (paged_attention_mass), on
+// the tcgen05 tensor cores.
 //
-// S^T = K Q^T with 64 tokens as the rows: a lane sums exp(scale s - lse) over
-// the query columns it holds, so a token's mass needs no atomics and its
-// order of summation is fixed.
+// An item is 256 tokens of one (batch, kv-head), two tiles of 128; a step is
+// 128 rows (head r % G of new token r / G) that see them:
+//   S^T = K Q^T   tokens are TMEM lanes, rows its columns
+//   sum of exp2(scale s - lse) along a lane, by the thread that owns the token
+// so that a token's sum needs no exchange between threads, no atomics, and
+// has a fixed order.  The keys of an item stay in shared memory while the
+// rows pass by; with few rows (a decode step) the keys pass by and the rows
+// stay.  One exponential per (row, token) and one product of the head_dim:
+// with 128 channels the tensor cores and the exponentials take about the
+// same time, so two accumulators per tile keep both going.
+//
+// The steps of all items are dealt out evenly (spg_deal.cuh).  A part of an
+// item leaves its 256 sums in the workspace, and the part that arrives last
+// adds them in order.
+//
+// Nothing is rounded to fewer than 32 bits.
+#include <algorithm>
 #include <cmath>
 
-#include "spg_chunk_common.cuh"
+#include "spg_deal.cuh"
 #include "spg_internal.h"
+#include "spg_tile_load.cuh"
 
 namespace spg {
 namespace {
 
-constexpr int kRows = 64;   // rows of a tile
-constexpr int kTok = 64;    // tokens per step
-constexpr int kThreads = 128;
+constexpr int kItemTokens = 2 * kTile;
+constexpr uint32_t kTmemCols = 512;  // two accumulators of 128 columns for each of the two tiles
 
-// Shared tile of 16-bit rows of D channels: 16-byte piece c of row r at c ^ (r % 8).
-template <int D>
-__device__ __forceinline__ uint32_t tile_at(uint32_t base, int r, int c) {
-  return base + r * (D * 2) + ((c ^ (r & 7)) << 4);
-}
-
-// `rows` tokens from t0 of one (batch, kv-head) into a tile, int8 codes as
-// exact 16-bit values; tokens at or past `end`, or of a bad page, are zeros
-// and their mask entry (and scale) says so.
-template <typename T, typename TQ, int D, int ROWS, int THREADS>
-__device__ __forceinline__ void load_tokens(const T* pool, const __half* scale, const int32_t* pt, int Hkv, int h,
-                                            int S, int n_phys, int t0, int end, uint8_t* tile, float* s_scale,
-                                            int32_t* err) {
-  constexpr int CPR = D / 8;
-  for (int i = threadIdx.x; i < ROWS * CPR; i += THREADS) {
-    const int r = i / CPR, c = i % CPR, t = t0 + r;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    float sc = 0.f;
-    if (t < end) {
-      const int page = pt[t / S];
-      if (page >= 0 && page < n_phys) {
-        const size_t row = (static_cast<size_t>(page) * Hkv + h) * S + t % S;
-        sc = 1.f;
-        if constexpr (sizeof(T) == 1) {
-          if (scale) sc = __half2float(scale[row]);
-          float x[8];
-          load_cvt<int8_t, 8>(reinterpret_cast<const int8_t*>(pool) + row * D + 8 * c, x);
-          w = make_uint4(pack2<TQ>(x[0], x[1]), pack2<TQ>(x[2], x[3]), pack2<TQ>(x[4], x[5]), pack2<TQ>(x[6], x[7]));
-        } else {
-          w = *reinterpret_cast<const uint4*>(pool + row * D + 8 * c);
-        }
-      } else if (c == 0) {
-        record_error(err, SPG_DEVERR_PAGE_ID);
-        sc = -1.f;
-      } else {
-        sc = -1.f;
-      }
+struct TokenItems : ChunkShape {
+  __device__ int items(const ChunkSeq& s) const { return (s.L + kItemTokens - 1) / kItemTokens; }
+  // row tiles of the sequence, and the first that sees token t
+  __device__ int row_tiles(const ChunkSeq& s) const { return (s.n * G + kTile - 1) / kTile; }
+  __device__ int first_tile(const ChunkSeq& s, int t) const { return t > s.pos0 ? (t - s.pos0) * G / kTile : 0; }
+  // item k is seen by the row tiles from floor((256 k - pos0) G / 128) on: 2 k G - ceil(pos0 G / 128)
+  // past pos0 (an item without rows still counts one step, its decay)
+  __device__ long long steps(const ChunkSeq& s, int m) const {
+    if (s.n == 0) return m;
+    const long long rt = row_tiles(s);
+    const int early = min(m, s.pos0 / kItemTokens + 1);
+    long long sum = early * rt;
+    if (m > early) {
+      const long long c = (static_cast<long long>(s.pos0) * G + kTile - 1) / kTile, cnt = m - early;
+      sum += cnt * (rt + c) - 2ll * G * (cnt * (early + m - 1) / 2);
     }
-    *reinterpret_cast<uint4*>(tile + r * (D * 2) + ((c ^ (r & 7)) << 4)) = w;
-    if (c == 0 && s_scale) s_scale[r] = sc;  // negative: bad page
+    return sum;
   }
-}
+};
 
 struct MassArgs {
-  const void *q, *k_pool;
+  TokenItems sh;
+  CUtensorMap tmq;
+  const void* k_pool;
   const __half* k_scale;
-  const int32_t *q_start, *page_table, *seq_lens;
+  const int32_t* page_table;
   const float *lse, *mass_in;
   float* mass_out;
-  int32_t* err;
-  int B, Hkv, S, MP, n_phys, total_q;
+  int32_t *err, *counters;
+  float* part;  // [2 * CTAs][256]
+  int Hkv, G, S, MP, n_phys;
   float scale_log2, decay;
 };
 
-template <typename T, typename TQ, int D, int G>
-__global__ void __launch_bounds__(kThreads) k_mass(const __grid_constant__ MassArgs a) {
-  constexpr int KS = D / 16;
-  extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* s_k = smem;
-  uint8_t* s_q = smem + kTok * D * 2;
-  __shared__ float s_ks[kTok], s_lse[kRows];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = blockIdx.y, b = unit / a.Hkv, h = unit % a.Hkv, t0 = blockIdx.x * kTok, Hq = a.Hkv * G;
-  pdl_wait();
-  int32_t bad = 0;
-  const ChunkSeq sq = chunk_seq(a.q_start, a.seq_lens, b, a.total_q, a.MP * a.S, bad);
-  if (bad && blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, bad);
-  if (t0 >= sq.L) return;
-  load_tokens<T, TQ, D, kTok, kThreads>(static_cast<const T*>(a.k_pool), a.k_scale,
-                                        a.page_table + static_cast<size_t>(b) * a.MP, a.Hkv, h, a.S, a.n_phys, t0, sq.L,
-                                        s_k, s_ks, a.err);
-  __syncthreads();
-  const int g = lane >> 2, tq = lane & 3, mi = lane >> 3, r8 = lane & 7;
-  uint32_t ka[KS][4];
-  const uint32_t kb = smem_u32(s_k), qb = smem_u32(s_q);
-#pragma unroll
-  for (int j = 0; j < KS; ++j) ldmatrix_x4(ka[j], tile_at<D>(kb, warp * 16 + (mi & 1) * 8 + r8, 2 * j + (mi >> 1)));
-  float ks[2], sum[2] = {0.f, 0.f};
-  int tok[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    tok[e] = t0 + warp * 16 + g + 8 * e;
-    ks[e] = s_ks[warp * 16 + g + 8 * e];
+// A part of an item with the rows it takes.
+struct Seg : Part {
+  int tile0, tiles;  // row tiles [tile0, tile0 + tiles)
+};
+struct SegIter : PartIter<TokenItems> {
+  using PartIter::PartIter;
+  __device__ bool next(Seg& s) {
+    if (!PartIter::next(s)) return false;
+    s.tile0 = sh.first_tile(s.sq, s.item * kItemTokens) + s.k0;
+    s.tiles = s.sq.n == 0 ? 0 : s.k1 - s.k0;
+    return true;
   }
-  // rows that see at least the tile's first token
-  const int first = max(0, t0 - sq.pos0) * G;
-  for (int r0 = first; r0 < sq.n * G; r0 += kRows) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
-      const int r = i / (D / 8), c = i % (D / 8), rr = r0 + r;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      const size_t row = static_cast<size_t>(sq.start + rr / G) * Hq + h * G + rr % G;
-      if (rr < sq.n * G) w = *reinterpret_cast<const uint4*>(static_cast<const TQ*>(a.q) + row * D + 8 * c);
-      *reinterpret_cast<uint4*>(s_q + r * (D * 2) + ((c ^ (r & 7)) << 4)) = w;
-      if (c == 0) {
-        const float e = rr < sq.n * G ? a.lse[row] : -INFINITY;
-        s_lse[r] = e == -INFINITY ? INFINITY : e * kLog2e;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < kRows / 16; ++n) {
-      float s[2][4] = {};
-#pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        uint32_t r[4];
-        ldmatrix_x4(r, tile_at<D>(qb, n * 16 + (mi >> 1) * 8 + r8, 2 * j + (mi & 1)));
-        mma_16816<TQ>(s[0], ka[j], r[0], r[1]);
-        mma_16816<TQ>(s[1], ka[j], r[2], r[3]);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = n * 16 + i * 8 + 2 * tq + (e & 1);
-          const float k = sizeof(T) == 1 ? ks[e >> 1] * a.scale_log2 : a.scale_log2;
-          if (tok[e >> 1] <= sq.pos0 + (r0 + c) / G) sum[e >> 1] += exp2f(fmaf(s[i][e], k, -s_lse[c]));
+};
+// Which tile of rows is in shared memory: it stays while the next step wants
+// the same one.  Every role follows the same rule.
+struct RowRing {
+  int b = -1, h = -1, tile = -1;
+  __device__ bool same(const Seg& s, int t) const { return s.b == b && s.h == h && t == tile; }
+  __device__ void set(const Seg& s, int t) { b = s.b, h = s.h, tile = t; }
+};
+
+template <int D>
+struct Layout {
+  static constexpr uint32_t kTileBytes = D / 64 * kTile * 128;
+  static constexpr int QST = 3;
+  static constexpr uint32_t k_off = 0, q_off = 4 * kTileBytes, misc = q_off + QST * kTileBytes;
+};
+template <int QST>
+struct Misc {
+  uint64_t k_full[2], k_empty[2], q_full[QST], q_empty[QST], s_full[2][2], s_empty[2][2], drain[2];
+  Plan plan;
+  uint32_t tmem;
+  int last;
+  alignas(16) float neg_lse[QST][kTile];  // -lse in the log2 domain; -inf for rows that count nothing
+};
+
+template <typename T, typename TQ, int D>
+struct Kernel {
+  static constexpr bool I8 = sizeof(T) == 1;
+  using Lay = Layout<D>;
+  using M = Misc<Lay::QST>;
+  using Tiles = TileLoader<T, TQ, D>;
+  static constexpr int QST = Lay::QST;
+  // warps 0-7 sums, 8-11 keys, 12 and 13 issue for one tile each, 14 rows
+  static constexpr int kThreads = 512, kLoadWarp = 8, kMmaWarp = 12, kRowWarp = 14;
+
+  // ---- products of one tile's keys with every row tile (whole warp, one lane issues) ------
+  static __device__ bool issue(const MassArgs& a, M& m, uint32_t smem, uint32_t tmem, int t) {
+    const auto wait = [&](uint64_t* bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, Waiter{a.err}(bar, phase)) != 0;
+    };
+    const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    constexpr uint32_t kStep = Lay::kTileBytes >> 4, kHalf = kTile * 128;
+    tmem = uniform(tmem) + t * 256;
+    const uint32_t dk = desc_k_major(smem + Lay::k_off) + t * kStep, dq = desc_k_major(smem + Lay::q_off);
+    uint32_t kc = 0, qi = 0, qr = 0, sc = 0;
+    bool have = false;  // a row tile in use
+    RowRing ring;
+    SegIter it(a.sh, m.plan);
+    Seg s;
+    while (uniform(it.next(s))) {
+      const int tiles = uniform(s.tiles);
+      if (tiles == 0) continue;
+      if (!wait(&m.k_full[kc & 1], kc >> 1)) return false;
+      fence_proxy_async();
+      for (int j = 0; j < tiles; ++j) {
+        const int tile = s.tile0 + j;
+        if (!uniform(ring.same(s, tile))) {
+          if (have) {
+            if (elect_one()) mma_commit(&m.q_empty[qi]);
+            __syncwarp();
+            if (++qi == QST) qi = 0, ++qr;
+          }
+          have = true;
+          ring.set(s, tile);
+          if (!wait(&m.q_full[qi], qr)) return false;
         }
+        const uint32_t buf = sc & 1;
+        if (sc >= 2 && !wait(&m.s_empty[t][buf], (sc >> 1) - 1)) return false;
+        tc_fence_after();
+        // columns in use, in sixteens
+        const int cols = min(kTile, (s.sq.n * a.G - tile * kTile + 15) & ~15);
+        const uint32_t id = instr_desc<TQ>(kTile, uniform(cols), false);
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32u) >> 4;
+            mma_ss(tmem + buf * 128, dk + (kc & 1) * 2 * kStep + off, dq + qi * kStep + off, id, ks > 0);
+          }
+          mma_commit(&m.s_full[t][buf]);
+          if (j == tiles - 1) mma_commit(&m.k_empty[kc & 1]);
+        }
+        __syncwarp();
+        ++sc;
+      }
+      ++kc;
+    }
+    return true;
+  }
+
+  // ---- rows: their tile by TMA, their lse by hand (whole warp) -------------------------------
+  static __device__ void load_rows(const MassArgs& a, M& m, uint8_t* smem, int lane) {
+    uint32_t qi = 0, qr = 0;
+    bool have = false;
+    RowRing ring;
+    SegIter it(a.sh, m.plan);
+    Seg s;
+    while (it.next(s)) {
+      for (int j = 0; j < s.tiles; ++j) {
+        const int tile = s.tile0 + j;
+        if (ring.same(s, tile)) continue;
+        if (have && ++qi == QST) qi = 0, ++qr;
+        have = true;
+        ring.set(s, tile);
+        float v[kTile / 32];
+#pragma unroll
+        for (int i = 0; i < kTile / 32; ++i) {
+          const int r = tile * kTile + lane + 32 * i;
+          v[i] = -INFINITY;
+          if (r < s.sq.n * a.G) {
+            const float e = a.lse[static_cast<size_t>(s.sq.start + r / a.G) * (a.Hkv * a.G) + s.h * a.G + r % a.G];
+            if (e != -INFINITY) v[i] = -e * kLog2e;
+          }
+        }
+        if (!__all_sync(0xffffffffu, qr == 0 || Waiter{a.err}(&m.q_empty[qi], qr - 1))) return;
+#pragma unroll
+        for (int i = 0; i < kTile / 32; ++i) m.neg_lse[qi][lane + 32 * i] = v[i];
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&m.q_full[qi], Lay::kTileBytes);
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_tile_4d(smem + Lay::q_off + qi * Lay::kTileBytes + hf * kTile * 128, &a.tmq, hf * 64, 0, s.h,
+                        s.sq.start + tile * kTile / a.G, &m.q_full[qi]);
+        }
+      }
     }
   }
+
+  // ---- keys: both tiles of an item, one item ahead ---------------------------------------------
+  static __device__ void load_keys(const MassArgs& a, M& m, uint8_t* smem, int tid, int lane) {
+    bool dead = false;  // after a wait that ran out the others are skipped
+    const auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
+    };
+    const int s_log2 = 31 - __clz(a.S);
+    uint32_t kc = 0, done = 0;
+    const auto finish = [&] {  // int8: the older of the items in flight
+      const uint32_t buf = done++ & 1;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-    sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-    if (tq == 0 && tok[e] < sq.L) {
-      const size_t at = static_cast<size_t>(unit) * a.MP * a.S + tok[e];
-      float old = 0.f;
-      if (a.mass_in && a.decay > 0.f && tok[e] < sq.pos0) old = a.mass_in[at] * a.decay;
-      a.mass_out[at] = old + (ks[e] < 0.f ? 0.f : sum[e]);
+      for (int t = 0; t < 2; ++t) Tiles::widen(smem + Lay::k_off + (2 * buf + t) * Lay::kTileBytes, tid, 3);
+      fence_proxy_async();
+      mbar_arrive(&m.k_full[buf]);
+    };
+    SegIter it(a.sh, m.plan);
+    Seg s;
+    while (it.next(s)) {
+      if (s.tiles == 0) continue;
+      const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
+      const uint32_t buf = kc & 1;
+      const int t0 = s.item * kItemTokens;
+      int page[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) page[t] = Tiles::page_of(pt, t0 + t * kTile, s.sq.L, a.S, a.n_phys, lane);
+      if (kc >= 2) wait(&m.k_empty[buf], (kc >> 1) - 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        Tiles::copy(a.k_pool, a.Hkv, s.h, s_log2, t0 + t * kTile, s.sq.L, page[t], tid,
+                    smem_u32(smem) + Lay::k_off + (2 * buf + t) * Lay::kTileBytes);
+      if constexpr (I8) {
+        copy_commit();
+        if (kc >= 1) {
+          copy_wait<1>();
+          finish();
+        }
+      } else {
+        copy_arrive(&m.k_full[buf]);
+      }
+      ++kc;
     }
+    copy_commit();
+    copy_wait<0>();
+    if (I8 && done < kc) finish();
+  }
+
+  // ---- sums -----------------------------------------------------------------------------------------
+  static __device__ void sums(const MassArgs& a, M& m, uint32_t tmem, int warp, int lane) {
+    bool dead = false;
+    const auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
+    };
+    const int t = warp >> 2, tid = threadIdx.x;
+    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * 256;
+    uint32_t sc = 0, qi = 0, qr = 0;
+    bool have = false;
+    RowRing ring;
+    SegIter it(a.sh, m.plan);
+    Seg s;
+    while (it.next(s)) {
+      const int tok = s.item * kItemTokens + tid;  // threads 0-127: tile 0, 128-255: tile 1
+      const size_t at = (static_cast<size_t>(s.b) * a.Hkv + s.h) * a.MP * a.S + tok;
+      const bool live = tok < s.sq.L;
+      // what the token needs from memory, while its keys are on their way
+      bool ok = live;
+      float k = a.scale_log2, old = 0.f;
+      if (live) {
+        const int page = a.page_table[static_cast<size_t>(s.b) * a.MP + tok / a.S];
+        ok = page >= 0 && page < a.n_phys;
+        if (!ok && s.tiles > 0) record_error(a.err, SPG_DEVERR_PAGE_ID);
+        if constexpr (I8)
+          if (ok) k *= __half2float(a.k_scale[(static_cast<size_t>(page) * a.Hkv + s.h) * a.S + tok % a.S]);
+        if (a.mass_in && a.decay > 0.f && tok < s.sq.pos0 && s.k0 == 0) old = a.mass_in[at] * a.decay;
+      }
+      const uint64_t k2 = f32x2(k, k);
+      uint64_t sum0 = f32x2(0.f, 0.f), sum1 = sum0;
+      for (int j = 0; j < s.tiles; ++j) {
+        const int tile = s.tile0 + j;
+        if (!ring.same(s, tile)) {
+          if (have) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.q_empty[qi]);
+            if (++qi == QST) qi = 0, ++qr;
+          }
+          have = true;
+          ring.set(s, tile);
+          wait(&m.q_full[qi], qr);
+        }
+        const float* nl = m.neg_lse[qi];
+        const uint32_t buf = sc & 1;
+        wait(&m.s_full[t][buf], sc >> 1);
+        ++sc;
+        tc_fence_after();
+        const int cols = min(kTile, s.sq.n * a.G - tile * kTile);
+        // rows from which on the token is seen (its own is the first)
+        const int from = (tok - s.sq.pos0) * a.G - tile * kTile;
+        const bool masked = cols < kTile || (s.item + 1) * kItemTokens - 1 > s.sq.pos0 + tile * kTile / a.G;
+        // 32 columns in flight while 32 are summed
+        uint32_t x[2][32];
+        tmem_ld32(x[0], tS + buf * 128);
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t(&u)[32] = x[(c / 32) & 1];
+          if (c < cols) {  // the same for the whole block
+            tmem_wait_ld();
+            if (c + 32 < cols) tmem_ld32(x[(c / 32 + 1) & 1], tS + buf * 128 + c + 32);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float p = c + i < from || c + i >= cols ? 0.f : ex2(fmaf(__uint_as_float(u[i]), k, nl[c + i]));
+                const float q = c + i + 1 < from || c + i + 1 >= cols ? 0.f : ex2(fmaf(__uint_as_float(u[i + 1]), k, nl[c + i + 1]));
+                sum0 = add_f32x2(sum0, f32x2(p, q));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const ulonglong2 e = *reinterpret_cast<const ulonglong2*>(nl + c + i);
+                const float2 p = unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), k2, e.x));
+                const float2 q = unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(u[i + 2]), __uint_as_float(u[i + 3])), k2, e.y));
+                sum0 = add_f32x2(sum0, f32x2(ex2(p.x), ex2(p.y)));
+                sum1 = add_f32x2(sum1, f32x2(ex2(q.x), ex2(q.y)));
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&m.s_empty[t][buf]);
+      }
+      const float2 p = unpack_f32x2(sum0), q = unpack_f32x2(sum1);
+      const float sum = ok ? (p.x + p.y) + (q.x + q.y) : 0.f;
+      if (s.whole()) {
+        if (live) a.mass_out[at] = old + sum;
+      } else {
+        __stcg(a.part + own_slot(s) * kItemTokens + tid, sum);
+        join(a, m, s, tid, at, live);
+      }
+    }
+  }
+
+  // Counts a part of an item in; the last to arrive adds them up.
+  static __device__ void join(const MassArgs& a, M& m, const Seg& s, int tid, size_t at, bool live) {
+    const PartRange pr(m.plan, s);
+    __threadfence();
+    bar_sync(1, 256);
+    if (tid == 0) m.last = atomicAdd(&a.counters[pr.c0], 1) == pr.c1 - pr.c0;
+    bar_sync(2, 256);
+    if (!m.last) return;
+    __threadfence();
+    float sum = 0.f;
+    for (int c = pr.c0; c <= pr.c1; ++c) sum += __ldcg(a.part + pr.slot(c) * kItemTokens + tid);
+    if (live) {
+      float old = 0.f;
+      if (a.mass_in && a.decay > 0.f && s.item * kItemTokens + tid < s.sq.pos0) old = a.mass_in[at] * a.decay;
+      a.mass_out[at] = old + sum;
+    }
+    if (tid == 0) a.counters[pr.c0] = 0;  // ready for the next call
+  }
+};
+
+template <typename T, typename TQ, int D>
+__global__ void __launch_bounds__(512, 1) k_mass(const __grid_constant__ MassArgs a) {
+  using K = Kernel<T, TQ, D>;
+  using M = typename K::M;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  M& m = *reinterpret_cast<M*>(smem + K::Lay::misc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.k_full[i], K::Tiles::kThreads);
+      mbar_init(&m.k_empty[i], 2);
+      mbar_init(&m.drain[i], 1);
+      for (int j = 0; j < 2; ++j) {
+        mbar_init(&m.s_full[i][j], 1);
+        mbar_init(&m.s_empty[i][j], kTile);
+      }
+    }
+    for (int i = 0; i < K::QST; ++i) {
+      mbar_init(&m.q_full[i], 1);
+      mbar_init(&m.q_empty[i], 2 + 8);  // the issuing warps and the summing ones
+    }
+    mbar_fence_init();
+  }
+  if (warp == K::kMmaWarp) tmem_alloc(&m.tmem, kTmemCols);
+  pdl_wait();
+  if (warp == 0) make_plan(a.sh, &m.plan, a.err, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem;
+  if (warp < K::kLoadWarp) {
+    K::sums(a, m, tmem, warp, lane);
+  } else if (warp < K::kMmaWarp) {
+    K::load_keys(a, m, smem, threadIdx.x - K::kLoadWarp * 32, lane);
+  } else if (warp < K::kRowWarp) {
+    const int t = warp - K::kMmaWarp;
+    if (!K::issue(a, m, smem_u32(smem), tmem, t)) {
+      if (elect_one()) mma_commit(&m.drain[t]);  // products in flight end before TMEM goes back
+      __syncwarp();
+      mbar_wait_bounded(&m.drain[t], 0);
+    }
+  } else if (warp == K::kRowWarp) {
+    K::load_rows(a, m, smem, lane);
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == K::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-template <typename T, typename TQ, int D, int G>
-cudaError_t mass_typed(const spg_params& p, const MassArgs& a, cudaStream_t st) {
-  const auto kern = k_mass<T, TQ, D, G>;
-  const size_t smem = (kTok + kRows) * D * 2;
+template <typename T, typename TQ, int D>
+cudaError_t mass_typed(const spg_params& p, MassArgs& a, const void* q, cudaStream_t st) {
+  using K = Kernel<T, TQ, D>;
+  // (without rows the map is not used; any readable address describes it)
+  if (a.sh.total_q > 0 && !make_q_tmap(&a.tmq, q, p, a.sh.total_q, kTile)) return cudaErrorNotSupported;
+  const auto kern = k_mass<T, TQ, D>;
+  const size_t smem = 1024 + K::Lay::misc + sizeof(typename K::M);
   const cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  const int tiles = static_cast<int>((static_cast<long long>(p.max_pages_per_seq) * p.page_size + kTok - 1) / kTok);
-  return launch_pdl(kern, dim3(tiles, p.batch * p.num_kv_heads), dim3(kThreads), smem, st, a);
-}
-
-#define SPG_DG(FN, T, TQ)                                            \
-  switch (p.head_dim * 16 + p.num_q_heads / p.num_kv_heads) {        \
-    case 128 * 16 + 1: return FN<T, TQ, 128, 1>(p, a, stream);       \
-    case 128 * 16 + 2: return FN<T, TQ, 128, 2>(p, a, stream);       \
-    case 128 * 16 + 4: return FN<T, TQ, 128, 4>(p, a, stream);       \
-    case 128 * 16 + 8: return FN<T, TQ, 128, 8>(p, a, stream);       \
-    case 64 * 16 + 1: return FN<T, TQ, 64, 1>(p, a, stream);         \
-    case 64 * 16 + 2: return FN<T, TQ, 64, 2>(p, a, stream);         \
-    case 64 * 16 + 4: return FN<T, TQ, 64, 4>(p, a, stream);         \
-    case 64 * 16 + 8: return FN<T, TQ, 64, 8>(p, a, stream);         \
-    default: return cudaErrorInvalidValue;                           \
-  }
-#define SPG_TYPES(FN)                                                \
-  if (p.kv_dtype == SPG_F16) { SPG_DG(FN, __half, __half) }          \
-  if (p.kv_dtype == SPG_BF16) { SPG_DG(FN, __nv_bfloat16, __nv_bfloat16) } \
-  if (p.q_dtype == SPG_F16) { SPG_DG(FN, int8_t, __half) }           \
-  SPG_DG(FN, int8_t, __nv_bfloat16)
-
-float scale_log2(const spg_params& p) {
-  return (p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.head_dim))) * kLog2e;
+  return launch_pdl(kern, dim3(std::min(device_sm_count(), kMaxCtas)), dim3(K::kThreads), smem, st, a);
 }
 
 }  // namespace
+
+static_assert(kMassCounterBytes >= sizeof(int32_t) * kMaxCtas, "a counter per CTA");
+size_t mass_workspace_bytes() { return kMassCounterBytes + sizeof(float) * 2 * kMaxCtas * kItemTokens; }
 
 cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_pool, const void* k_scale,
                         const float* lse, const float* mass_in, float* mass_out, float decay, const Workspace& ws,
                         cudaStream_t stream) {
   MassArgs a{};
-  a.q = r.q;
+  a.sh.q_start = r.q_start;
+  a.sh.seq_lens = r.seq_lens;
+  a.sh.B = p.batch;
+  a.sh.Hkv = p.num_kv_heads;
+  a.sh.G = p.num_q_heads / p.num_kv_heads;
+  a.sh.total_q = r.total_q;
+  a.sh.max_tokens = p.max_pages_per_seq * p.page_size;
   a.k_pool = k_pool;
   a.k_scale = static_cast<const __half*>(k_scale);
-  a.q_start = r.q_start;
   a.page_table = r.page_table;
-  a.seq_lens = r.seq_lens;
   a.lse = lse;
   a.mass_in = mass_in;
   a.mass_out = mass_out;
   a.err = ws.err;
-  a.B = p.batch;
+  a.counters = ws.mass_counters;
+  a.part = ws.mass_part;
   a.Hkv = p.num_kv_heads;
+  a.G = a.sh.G;
   a.S = p.page_size;
   a.MP = p.max_pages_per_seq;
   a.n_phys = p.num_phys_pages;
-  a.total_q = r.total_q;
-  a.scale_log2 = scale_log2(p);
+  a.scale_log2 = (p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.head_dim))) * kLog2e;
   a.decay = decay;
-  SPG_TYPES(mass_typed)
+#define SPG_MASS(T, TQ) \
+  return p.head_dim == 128 ? mass_typed<T, TQ, 128>(p, a, r.q, stream) : mass_typed<T, TQ, 64>(p, a, r.q, stream)
+  if (p.kv_dtype == SPG_F16) SPG_MASS(__half, __half);
+  if (p.kv_dtype == SPG_BF16) SPG_MASS(__nv_bfloat16, __nv_bfloat16);
+  if (p.q_dtype == SPG_F16) SPG_MASS(int8_t, __half);
+  SPG_MASS(int8_t, __nv_bfloat16);
+#undef SPG_MASS
 }
 
 }  // namespace spg

@@ -173,6 +173,25 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A wait: false, and recorded, when it ran out (as mbar_wait_bounded, in few
+// instructions: the issuing warp's path has five of them per step).
+struct Waiter {
+  int32_t* err;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t phase) const {
+    if (mbar_try_wait(bar, phase & 1)) return true;
+    uint64_t t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+#pragma unroll 1
+    for (int i = 0; i < (1 << 22); ++i) {
+      if (mbar_try_wait(bar, phase & 1)) return true;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (t - t0 > 100ull * 1000 * 1000) break;
+    }
+    record_error(err, SPG_DEVERR_TIMEOUT);
+    return false;
+  }
+};
+
 // named barrier of `n` threads (whole warps)
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 

@@ -69,4 +69,17 @@ bool make_kv_tmap(CUtensorMap* map, const void* pool, int kv_dtype, long long ro
   return r == CUDA_SUCCESS;
 }
 
+bool make_q_tmap(CUtensorMap* map, const void* q, const spg_params& p, int total_q, int rows) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t d = p.head_dim, G = p.num_q_heads / p.num_kv_heads, Hkv = p.num_kv_heads;
+  const cuuint64_t dims[4] = {d, G, Hkv, static_cast<cuuint64_t>(total_q)};
+  const cuuint64_t strides[3] = {d * 2, G * d * 2, Hkv * G * d * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(rows / G)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, p.q_dtype == SPG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace spg
