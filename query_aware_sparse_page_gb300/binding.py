@@ -13,6 +13,8 @@ import ctypes
 import os
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
+import torch
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libspg.so")
 
@@ -296,64 +298,60 @@ def dense_decode_attention(p, q, k_pool, v_pool, k_scale, v_scale, page_table, s
 
 
 # ---- chunks of new tokens ----------------------------------------------------------
-_ELEM = {F16: "float16", BF16: "bfloat16", I8: "int8"}
+_ELEM = {F16: torch.float16, BF16: torch.bfloat16, I8: torch.int8}
+
+
+def _refuse(name, t, shape, dtype):
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    raise ValueError("libspg takes contiguous device tensors")
 
 
 def _take(name, t, shape, dtype):
     """Device pointer of a tensor that has to be contiguous, of this shape and type."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if str(t.dtype) != f"torch.{dtype}":
-        raise ValueError(f"{name}: {t.dtype}, expected torch.{dtype}")
-    return _ptr(t)
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _refuse(name, t, shape, dtype)
+    return t.data_ptr()
 
 
 def _take_rows(name, t, shape, dtype):
     """Pointer and row stride of a tensor whose rows are contiguous."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if str(t.dtype) != f"torch.{dtype}":
-        raise ValueError(f"{name}: {t.dtype}, expected torch.{dtype}")
-    if not t.is_cuda:
-        raise ValueError("libspg takes device tensors")
-    if t.numel() and not t[0].is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
+        _refuse(name, t, shape, dtype)
+    row, head, one = t.stride()
+    if t.numel() and (one != 1 or (shape[1] > 1 and head != shape[2])):
         raise ValueError(f"{name}: the heads of one token have to be contiguous")
-    n = shape[1] * shape[2]
-    return c_void_p(t.data_ptr()), int(t.stride(0)) if shape[0] > 1 else n
+    return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
 
 
 def _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, q_start=None):
-    pool = (p.num_phys_pages, p.num_kv_heads, p.page_size, p.head_dim)
-    r = [_take("k_pool", k_pool, pool, _ELEM[p.kv_dtype]), _take("v_pool", v_pool, pool, _ELEM[p.kv_dtype]),
-         _take("k_scale", k_scale, pool[:3], "float16"), _take("v_scale", v_scale, pool[:3], "float16"),
-         _take("page_table", page_table, (p.batch, p.max_pages_per_seq), "int32"),
-         _take("seq_lens", seq_lens, (p.batch,), "int32"), _take("q_start", q_start, (p.batch + 1,), "int32")]
-    return r
+    pool, kv = (p.num_phys_pages, p.num_kv_heads, p.page_size, p.head_dim), _ELEM[p.kv_dtype]
+    return (_take("k_pool", k_pool, pool, kv), _take("v_pool", v_pool, pool, kv),
+            _take("k_scale", k_scale, pool[:3], torch.float16), _take("v_scale", v_scale, pool[:3], torch.float16),
+            _take("page_table", page_table, (p.batch, p.max_pages_per_seq), torch.int32),
+            _take("seq_lens", seq_lens, (p.batch,), torch.int32),
+            _take("q_start", q_start, (p.batch + 1,), torch.int32))
 
 
-class _on:
-    """The device the workspace lives on made current, and the stream to launch on there."""
-
-    def __init__(self, ws, stream):
-        import torch
-
-        if ws is None:
-            raise ValueError("a workspace is needed")
-        self.guard = torch.cuda.device(ws.device) if ws.is_cuda else None
-        self.stream, self.ws = stream, ws
-
-    def __enter__(self):
-        if self.guard is None:
-            raise ValueError("libspg takes device tensors")
-        self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+def _call(fn, where, ws, stream, *args):
+    """fn(*args, workspace, its bytes, stream) with the workspace's device current."""
+    if ws is None or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("a contiguous workspace on the device is needed")
+    dev = ws.device.index
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    size = ws.numel() * ws.element_size()
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, ws.data_ptr(), size, stream), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, ws.data_ptr(), size, stream), where)
 
 
 def spg_chunk_workspace_size(p: spg_params, total_q: int) -> int:
@@ -372,60 +370,51 @@ def spg_rope_freqs(rope: spg_rope, head_dim: int):
 
 def paged_rope_append(p, rope, q, k, v, q_start, page_table, seq_lens, k_pool, v_pool, k_scale=None,
                       v_scale=None, q_out=None, positions=None, ws=None, stream=None):
-    T, d = k.shape[0], p.head_dim
-    qd = _ELEM[p.q_dtype]
+    T, d, qd = k.shape[0], p.head_dim, _ELEM[p.q_dtype]
     qp, qs = _take_rows("q", q, (T, p.num_q_heads, d), qd)
     kp, ks = _take_rows("k", k, (T, p.num_kv_heads, d), qd)
     vp, vs = _take_rows("v", v, (T, p.num_kv_heads, d), qd)
     kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table,
                                                      seq_lens, q_start)
     out = _take("q_out", q_out, (T, p.num_q_heads, d), qd)
-    pos = _take("positions", positions, (T,), "int32")
-    with _on(ws, stream) as s:
-        wp, wn = _ws(ws)
-        _check(LIB.paged_rope_append(
-            ctypes.byref(p), None if rope is None else ctypes.byref(rope), T, qp, qs, kp, ks, vp, vs, st, pos,
-            pt, sl, kpool, vpool, ksc, vsc, out, wp, wn, s), "paged_rope_append")
+    pos = _take("positions", positions, (T,), torch.int32)
+    _call(LIB.paged_rope_append, "paged_rope_append", ws, stream, ctypes.byref(p),
+          None if rope is None else ctypes.byref(rope), T, qp, qs, kp, ks, vp, vs, st, pos, pt, sl, kpool, vpool,
+          ksc, vsc, out)
 
 
 def paged_chunk_attention(p, q, q_start, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, out,
                           lse=None, ws=None, stream=None):
-    T, rows = q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim)
-    qp, op = _take("q", q, rows, _ELEM[p.q_dtype]), _take("out", out, rows, _ELEM[p.q_dtype])
-    lp = _take("lse", lse, rows[:2], "float32")
+    T, rows, qd = q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim), _ELEM[p.q_dtype]
+    qp, op = _take("q", q, rows, qd), _take("out", out, rows, qd)
+    lp = _take("lse", lse, rows[:2], torch.float32)
     kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table,
                                                      seq_lens, q_start)
-    with _on(ws, stream) as s:
-        wp, wn = _ws(ws)
-        _check(LIB.paged_chunk_attention(ctypes.byref(p), T, qp, st, kpool, vpool, ksc, vsc, pt, sl, op, lp, wp,
-                                         wn, s), "paged_chunk_attention")
+    _call(LIB.paged_chunk_attention, "paged_chunk_attention", ws, stream, ctypes.byref(p), T, qp, st, kpool, vpool,
+          ksc, vsc, pt, sl, op, lp)
 
 
 def paged_attention_mass(p, q, q_start, k_pool, k_scale, page_table, seq_lens, lse, mass_in, mass_out,
                          decay=1.0, ws=None, stream=None):
     T, rows = q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim)
     m = (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size)
-    qp, lp = _take("q", q, rows, _ELEM[p.q_dtype]), _take("lse", lse, rows[:2], "float32")
-    mi, mo = _take("mass_in", mass_in, m, "float32"), _take("mass_out", mass_out, m, "float32")
+    qp, lp = _take("q", q, rows, _ELEM[p.q_dtype]), _take("lse", lse, rows[:2], torch.float32)
+    mi, mo = _take("mass_in", mass_in, m, torch.float32), _take("mass_out", mass_out, m, torch.float32)
     kpool, _, ksc, _, pt, sl, st = _take_cache(p, k_pool, None, k_scale, None, page_table, seq_lens, q_start)
-    with _on(ws, stream) as s:
-        wp, wn = _ws(ws)
-        _check(LIB.paged_attention_mass(ctypes.byref(p), T, qp, st, kpool, ksc, pt, sl, lp, mi, mo, float(decay),
-                                        wp, wn, s), "paged_attention_mass")
+    _call(LIB.paged_attention_mass, "paged_attention_mass", ws, stream, ctypes.byref(p), T, qp, st, kpool, ksc, pt,
+          sl, lp, mi, mo, float(decay))
 
 
 def paged_cache_evict(p, mass, keep, n_sink, n_recent, k_pool, v_pool, k_scale, v_scale, page_table,
                       dst_page_table, seq_lens, kept, new_lens, mass_out, ws=None, stream=None):
+    m, keep = (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size), int(keep)
+    mi, mo = _take("mass", mass, m, torch.float32), _take("mass_out", mass_out, m, torch.float32)
     kpool, vpool, ksc, vsc, pt, sl, _ = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens)
-    m = (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size)
-    mi, mo = _take("mass", mass, m, "float32"), _take("mass_out", mass_out, m, "float32")
-    dst = _take("dst_page_table", dst_page_table, (p.batch, p.max_pages_per_seq), "int32")
-    kp = _take("kept", kept, (p.batch, p.num_kv_heads, int(keep)), "int32")
-    nl = _take("new_lens", new_lens, (p.batch,), "int32")
-    with _on(ws, stream) as s:
-        wp, wn = _ws(ws)
-        _check(LIB.paged_cache_evict(ctypes.byref(p), mi, int(keep), int(n_sink), int(n_recent), kpool, vpool, ksc,
-                                     vsc, pt, dst, sl, kp, nl, mo, wp, wn, s), "paged_cache_evict")
+    dst = _take("dst_page_table", dst_page_table, (p.batch, p.max_pages_per_seq), torch.int32)
+    kp = _take("kept", kept, (p.batch, p.num_kv_heads, keep), torch.int32)
+    nl = _take("new_lens", new_lens, (p.batch,), torch.int32)
+    _call(LIB.paged_cache_evict, "paged_cache_evict", ws, stream, ctypes.byref(p), mi, keep, int(n_sink),
+          int(n_recent), kpool, vpool, ksc, vsc, pt, dst, sl, kp, nl, mo)
 
 
 def spg_read_device_error(ws, stream=None) -> int:

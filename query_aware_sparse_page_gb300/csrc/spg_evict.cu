@@ -7,17 +7,19 @@
 // the key of the last one kept is found by histograms of the range that the
 // keys still in question span, 2048 bins a pass, at most three passes; one
 // more pass writes the kept positions in order, the first of the equal ones
-// by position.  The kept masses move along in the same pass: a position
-// never moves up, and a tile is read before anything is written at or before
-// its end, so mass_out may be mass.
+// by position, and their masses.  A cluster of up to 8 CTAs shares one
+// (batch, kv-head): each reads its tokens' masses once, into shared memory
+// (all of them before any is written, so mass_out may be mass), and the
+// passes meet in the first CTA's histogram over distributed shared memory.
 //
-// Compacting moves rows of d channels.  To pages of its own it is a gather,
-// split over tokens.  Within the same pages a destination slot j is also the
-// source of some later destination, so the order matters: sources ascend
-// with their destinations and never lie before them, hence a CTA that takes
-// the tokens in order and reads a tile (and the next) before it writes the
-// first never loses one.  CTAs of one (batch, kv-head) then split the row's
-// channels (and K from V), which never meet.
+// Compacting moves rows of d channels.  To pages of its own it is a gather:
+// a CTA resolves the pages of 128 kept tokens, then streams their K and V
+// rows with all loads independent.  Within the same pages a destination slot
+// j is also the source of some later destination, so the order matters:
+// sources ascend with their destinations and never lie before them, hence a
+// CTA that takes the tokens in order and reads a step (and the next) before
+// it writes the first never loses one.  The CTAs of one (batch, kv-head)
+// then split the row's channels (and K from V), which never meet.
 #include <algorithm>
 
 #include "spg_chunk_common.cuh"
@@ -26,9 +28,12 @@
 namespace spg {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
-constexpr int kPer = 4;  // keys of a thread per tile of the ordered pass
+constexpr int kPer = 8;  // tokens of a thread per tile of the ordered pass
+constexpr int kMaxCluster = 8;
+// masses of one CTA that stay in shared memory (else they are read again)
+constexpr int kMaxResident = 48 * 1024;
 
 struct EvictArgs {
   const float* mass;
@@ -37,7 +42,7 @@ struct EvictArgs {
   int32_t *kept, *new_lens, *err;
   uint8_t *k_pool, *v_pool;
   __half *k_scale, *v_scale;
-  int Hkv, S, MP, n_phys, keep, n_sink, n_recent, row_bytes, slices, lpr_log2, in_place;
+  int Hkv, S, MP, n_phys, keep, n_sink, n_recent, row_bytes, resident;
 };
 
 __device__ __forceinline__ uint32_t mass_key(float m) { return m != m ? 0u : score_key(m); }
@@ -69,16 +74,24 @@ __device__ __forceinline__ int block_scan(int v, int* s, int& total) {
   return base + incl - v;
 }
 
+// Cluster of gridDim.x CTAs for unit blockIdx.y; CTA r has the r-th share of
+// the sequence's tokens.
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
+  extern __shared__ float s_mass[];  // the CTA's masses, where they fit
   __shared__ int s_hist[kBins];
   __shared__ int s_scan[33];
-  __shared__ uint32_t s_lo, s_hi;
-  __shared__ int s_bin, s_need;
+  __shared__ uint32_t s_range[2];            // of the unforced keys: min, max (whole cluster, in the first CTA)
+  __shared__ int s_bin, s_need;              // found by the first CTA
+  __shared__ int s_count[kMaxCluster][2];    // per CTA: tokens above the threshold, and equal to it
+  const int tid = threadIdx.x, rank = blockIdx.x, C = gridDim.x, unit = blockIdx.y, b = unit / a.Hkv;
+  if (tid == 0) {
+    s_range[0] = 0xffffffffu;
+    s_range[1] = 0u;
+  }
   pdl_wait();
-  const int unit = blockIdx.x, b = unit / a.Hkv, tid = threadIdx.x;
   int L = a.seq_lens[b];
   if (L < 0 || L > a.MP * a.S) {
-    if (tid == 0) record_error(a.err, SPG_DEVERR_SEQ_LEN);
+    if (tid == 0 && rank == 0) record_error(a.err, SPG_DEVERR_SEQ_LEN);
     L = 0;
   }
   const size_t N = static_cast<size_t>(a.MP) * a.S;
@@ -86,101 +99,127 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   float* mass_out = a.mass_out + unit * N;
   int32_t* kept = a.kept + static_cast<size_t>(unit) * a.keep;
   const int new_len = min(L, a.keep);
-  if (tid == 0 && unit % a.Hkv == 0) a.new_lens[b] = new_len;
-  for (int j = new_len + tid; j < a.keep; j += kSelThreads) kept[j] = -1;
+  if (tid == 0 && rank == 0 && unit % a.Hkv == 0) a.new_lens[b] = new_len;
+  for (int j = new_len + rank * kSelThreads + tid; j < a.keep; j += C * kSelThreads) kept[j] = -1;
 
-  // the unforced tokens [lo_t, hi_t), `need` of them kept
-  const int lo_t = min(a.n_sink, L), hi_t = max(lo_t, L - a.n_recent);
-  int need = L <= a.keep ? hi_t - lo_t : a.keep - (L - (hi_t - lo_t));
-  uint32_t thr = 0;     // keys above thr are kept, and the first `need` equal to it
-  const bool all = need >= hi_t - lo_t;
-  if (all) {
-    need = hi_t - lo_t;
-  } else if (need > 0) {
-    if (tid == 0) {
-      s_lo = 0xffffffffu;
-      s_hi = 0u;
-    }
-    __syncthreads();
-    uint32_t mn = 0xffffffffu, mx = 0u;
-    for (int t = lo_t + tid; t < hi_t; t += kSelThreads) {
-      const uint32_t k = mass_key(mass[t]);
+  // this CTA's tokens
+  const int share = (L + C - 1) / C, t_lo = min(rank * share, L), t_hi = min(t_lo + share, L);
+  const auto at = [&](int t) { return a.resident ? s_mass[t - t_lo] : mass[t]; };
+  // the unforced tokens [f_lo, f_hi), `need` of them kept
+  const int f_lo = min(a.n_sink, L), f_hi = max(f_lo, L - a.n_recent);
+  int need = L <= a.keep ? f_hi - f_lo : a.keep - (L - (f_hi - f_lo));
+  const bool all = need >= f_hi - f_lo;
+  const int u_lo = max(t_lo, f_lo), u_hi = min(t_hi, f_hi);  // this CTA's unforced ones
+  uint32_t mn = 0xffffffffu, mx = 0u;
+  for (int t = t_lo + tid; t < t_hi; t += kSelThreads) {
+    const float v = mass[t];
+    if (a.resident) s_mass[t - t_lo] = v;
+    if (t >= f_lo && t < f_hi) {
+      const uint32_t k = mass_key(v);
       mn = min(mn, k);
       mx = max(mx, k);
     }
+  }
+  cluster_sync();  // the first CTA's range is set up, every mass has been read
+  uint32_t thr = 0;  // keys above thr are kept, and the first `need` equal to it
+  if (!all && need > 0) {
     mn = __reduce_min_sync(0xffffffffu, mn);
     mx = __reduce_max_sync(0xffffffffu, mx);
-    if ((tid & 31) == 0) {
-      atomicMin(&s_lo, mn);
-      atomicMax(&s_hi, mx);
+    if ((tid & 31) == 0 && mn <= mx) {
+      atomicMin(&s_range[0], mn);
+      atomicMax(&s_range[1], mx);
     }
     __syncthreads();
-    uint32_t lo = s_lo, hi = s_hi;
-    while (lo < hi) {
+    if (rank != 0 && tid == 0) {
+      red_cluster_min(map_rank(&s_range[0], 0), s_range[0]);
+      red_cluster_max(map_rank(&s_range[1], 0), s_range[1]);
+    }
+    cluster_sync();
+    uint32_t lo = static_cast<uint32_t>(ld_cluster_s32(map_rank(&s_range[0], 0)));
+    uint32_t hi = static_cast<uint32_t>(ld_cluster_s32(map_rank(&s_range[1], 0)));
+    while (lo < hi) {  // the same in every CTA
       // bins of 2^shift keys over [lo, hi]
       const int shift = max(0, 32 - __clz(hi - lo) - 11);
       for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-      __syncthreads();
-      for (int t = lo_t + tid; t < hi_t; t += kSelThreads) {
-        const uint32_t k = mass_key(mass[t]);
+      cluster_sync();
+      for (int t = u_lo + tid; t < u_hi; t += kSelThreads) {
+        const uint32_t k = mass_key(at(t));
         if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1);
       }
       __syncthreads();
-      // from the top: the bin in which the need-th key lies (threads take two bins each, descending)
-      const int c0 = s_hist[kBins - 1 - 2 * tid], c1 = s_hist[kBins - 2 - 2 * tid];
-      int total;
-      const int before = block_scan(c0 + c1, s_scan, total);
-      if (before < need && before + c0 >= need) {
-        s_bin = kBins - 1 - 2 * tid;
-        s_need = need - before;
-      } else if (before + c0 < need && before + c0 + c1 >= need) {
-        s_bin = kBins - 2 - 2 * tid;
-        s_need = need - before - c0;
+      if (rank != 0)
+        for (int i = tid; i < kBins; i += kSelThreads)
+          if (s_hist[i]) red_cluster_add(map_rank(&s_hist[i], 0), s_hist[i]);
+      cluster_sync();
+      if (rank == 0) {
+        // from the top: the bin in which the need-th key lies (threads take four bins each, descending)
+        int c[4], sum = 0, total;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += c[i] = s_hist[kBins - 1 - 4 * tid - i];
+        int before = block_scan(sum, s_scan, total);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (before < need && before + c[i] >= need) {
+            s_bin = kBins - 1 - 4 * tid - i;
+            s_need = need - before;
+          }
+          before += c[i];
+        }
       }
-      __syncthreads();
-      need = s_need;
-      const uint32_t first = lo + (static_cast<uint32_t>(s_bin) << shift);
-      const uint32_t last = min(hi, first + ((1u << shift) - 1u));
+      cluster_sync();
+      need = ld_cluster_s32(map_rank(&s_need, 0));
+      const uint32_t first = lo + (static_cast<uint32_t>(ld_cluster_s32(map_rank(&s_bin, 0))) << shift);
+      hi = min(hi, first + ((1u << shift) - 1u));
       lo = first;
-      hi = last;
-      __syncthreads();
     }
     thr = lo;
   }
 
-  // the kept positions in order
+  // the kept positions in order: how many this CTA's tokens follow
+  const auto above = [&](int t, uint32_t k) { return all || t < f_lo || t >= f_hi || (need > 0 && k > thr); };
+  int n_above = 0, n_equal = 0;
+  for (int t = t_lo + tid; t < t_hi; t += kSelThreads) {
+    const uint32_t k = mass_key(at(t));
+    if (above(t, k)) ++n_above;
+    else if (need > 0 && k == thr) ++n_equal;
+  }
+  int all_above, all_equal;
+  block_scan(n_above, s_scan, all_above);
+  block_scan(n_equal, s_scan, all_equal);
+  if (tid < C) {
+    st_cluster_u32(map_rank(&s_count[rank][0], tid), all_above);
+    st_cluster_u32(map_rank(&s_count[rank][1], tid), all_equal);
+  }
+  cluster_sync();  // (nothing remote is touched after it)
   int out = 0, equal = 0;
-  for (int t0 = 0; t0 < L; t0 += kSelThreads * kPer) {
+  for (int r = 0; r < rank; ++r) {
+    out += s_count[r][0];
+    equal += s_count[r][1];
+  }
+  out += min(equal, max(need, 0));
+  for (int t0 = t_lo; t0 < t_hi; t0 += kSelThreads * kPer) {
     float m[kPer];
-    bool above[kPer], eq[kPer];
-    int n_above = 0, n_eq = 0;
+    unsigned take = 0, eq = 0;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) {
       const int t = t0 + tid * kPer + e;
       m[e] = 0.f;
-      above[e] = eq[e] = false;
-      if (t < L) {
-        m[e] = mass[t];
+      if (t < t_hi) {
+        m[e] = at(t);
         const uint32_t k = mass_key(m[e]);
-        above[e] = all || t < lo_t || t >= hi_t || (need > 0 && k > thr);
-        eq[e] = !above[e] && need > 0 && k == thr;
+        if (above(t, k)) take |= 1u << e;
+        else if (need > 0 && k == thr) eq |= 1u << e;
       }
-      n_above += above[e];
-      n_eq += eq[e];
     }
     int total_eq, total;
-    int e0 = equal + block_scan(n_eq, s_scan, total_eq);
-    int n = n_above;
+    int e0 = equal + block_scan(__popc(eq), s_scan, total_eq);
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
-      if (eq[e] && e0++ < need) {
-        above[e] = true;
-        ++n;
-      }
-    int o = out + block_scan(n, s_scan, total);  // a barrier: every mass of the tile is in registers
+      if ((eq >> e & 1u) && e0++ < need) take |= 1u << e;
+    int o = out + block_scan(__popc(take), s_scan, total);  // a barrier: every mass of the tile is in registers
 #pragma unroll
     for (int e = 0; e < kPer; ++e)
-      if (above[e]) {
+      if (take >> e & 1u) {
         kept[o] = t0 + tid * kPer + e;
         mass_out[o] = m[e];
         ++o;
@@ -191,60 +230,102 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   pdl_trigger();
 }
 
+// row of the pool that holds token t of kv-head h (-1: a bad page)
+__device__ __forceinline__ long long pool_row(const EvictArgs& a, const int32_t* pt, int h, int t) {
+  const int page = pt[t / a.S];
+  if (page < 0 || page >= a.n_phys) {
+    record_error(a.err, SPG_DEVERR_PAGE_ID);
+    return -1;
+  }
+  return (static_cast<long long>(page) * a.Hkv + h) * a.S + t % a.S;
+}
+
+// ---- to pages of its own ---------------------------------------------------------
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 4;  // rows of a thread per step
+constexpr int kMoveRows = 128;  // kept tokens of a CTA
 
-// CTA (x, y, z): tokens of chunk x, slice y (K's, then V's, then the scales) of unit z
-__global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_constant__ EvictArgs a) {
+// CTA (x, y): kept tokens 128 x .. of unit y, K and V
+template <int ROW>  // bytes
+__global__ void __launch_bounds__(kMoveThreads) k_evict_gather(const __grid_constant__ EvictArgs a) {
+  __shared__ long long s_from[kMoveRows], s_to[kMoveRows];
   pdl_wait();
-  const int unit = blockIdx.z, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x;
-  const int n = a.new_lens[b];
-  const int32_t* kept = a.kept + static_cast<size_t>(unit) * a.keep;
-  const int32_t* src_pt = a.page_table + static_cast<size_t>(b) * a.MP;
-  const int32_t* dst_pt = a.dst_table + static_cast<size_t>(b) * a.MP;
-  const bool scales = static_cast<int>(blockIdx.y) == 2 * a.slices;
-  const bool is_v = static_cast<int>(blockIdx.y) >= a.slices;
-  uint8_t* pool = is_v ? a.v_pool : a.k_pool;
-  const int lpr = scales ? 0 : a.lpr_log2;  // log2 of the threads of one row slice
-  const int slice = scales ? 0 : blockIdx.y % a.slices;
-  const size_t col = (static_cast<size_t>(slice) << (lpr + 4)) + 16 * (tid & ((1 << lpr) - 1));
-  const int per_step = (kMoveThreads >> lpr) * kMoveRows;
-  const int steps = (n + per_step - 1) / per_step;
-  const int s0 = static_cast<int>(static_cast<long long>(blockIdx.x) * steps / gridDim.x);
-  const int s1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * steps / gridDim.x);
-
-  uint4 w[2][kMoveRows];
-  const auto slot = [&](const int32_t* pt, int t) -> long long {
-    const int page = pt[t / a.S];
-    if (page < 0 || page >= a.n_phys) {
-      record_error(a.err, SPG_DEVERR_PAGE_ID);
-      return -1;
+  const int unit = blockIdx.y, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x, j0 = blockIdx.x * kMoveRows;
+  const int n = min(kMoveRows, a.new_lens[b] - j0);
+  if (n <= 0) return;
+  if (tid < n) {
+    const long long from = pool_row(a, a.page_table + static_cast<size_t>(b) * a.MP, h,
+                                    a.kept[static_cast<size_t>(unit) * a.keep + j0 + tid]);
+    const long long to = pool_row(a, a.dst_table + static_cast<size_t>(b) * a.MP, h, j0 + tid);
+    s_from[tid] = from;
+    s_to[tid] = from < 0 ? -1 : to;
+    if (a.k_scale && from >= 0 && to >= 0) {
+      a.k_scale[to] = a.k_scale[from];
+      a.v_scale[to] = a.v_scale[from];
     }
-    return (static_cast<long long>(page) * a.Hkv + h) * a.S + t % a.S;
-  };
-  long long dst[2][kMoveRows];
-  const auto load = [&](int step, uint4 (&v)[kMoveRows], long long (&d)[kMoveRows]) {
+  }
+  __syncthreads();
+  constexpr int LPR = ROW / 16, PER = kMoveThreads / LPR;  // threads of a row, rows at a time
+  constexpr int STEPS = kMoveRows / PER, U = STEPS < 8 ? STEPS : 8;
+  const int r0 = tid / LPR, col = tid % LPR * 16;
+#pragma unroll 1
+  for (int kv = 0; kv < 2; ++kv) {
+    uint8_t* pool = (kv ? a.v_pool : a.k_pool) + col;
+#pragma unroll 1
+    for (int s = 0; s < STEPS; s += U) {
+      uint4 w[U];
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r) {
-      const int j = step * per_step + r * (kMoveThreads >> lpr) + (tid >> lpr);
-      d[r] = -1;
-      if (j < n) {
-        const int t = kept[j];
-        const long long from = slot(src_pt, t);
-        if (from >= 0 && !(a.in_place && t == j)) {
-          d[r] = slot(dst_pt, j);
-          if (scales)
-            v[r].x = static_cast<uint32_t>(__half_as_ushort(a.k_scale[from])) |
-                     (static_cast<uint32_t>(__half_as_ushort(a.v_scale[from])) << 16);
-          else
-            v[r] = *reinterpret_cast<const uint4*>(pool + from * a.row_bytes + col);
-        }
+      for (int i = 0; i < U; ++i) {
+        const int r = r0 + (s + i) * PER;
+        if (r < n && s_to[r] >= 0) w[i] = __ldcs(reinterpret_cast<const uint4*>(pool + s_from[r] * ROW));
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int r = r0 + (s + i) * PER;
+        if (r < n && s_to[r] >= 0) *reinterpret_cast<uint4*>(pool + s_to[r] * ROW) = w[i];
       }
     }
-  };
-  const auto store = [&](const uint4 (&v)[kMoveRows], const long long (&d)[kMoveRows]) {
+  }
+}
+
+// ---- within the same pages ---------------------------------------------------------
+constexpr int kShiftRows = 8;        // rows of a thread per step
+constexpr int kSliceBytes = 32;      // a CTA's channels
+
+// CTA (x, y): slice x (K's, then V's, then the scales) of unit y
+__global__ void __launch_bounds__(kMoveThreads) k_evict_shift(const __grid_constant__ EvictArgs a) {
+  pdl_wait();
+  const int unit = blockIdx.y, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x;
+  const int n = a.new_lens[b], slices = a.row_bytes / kSliceBytes, slice = blockIdx.x % slices;
+  const int32_t* kept = a.kept + static_cast<size_t>(unit) * a.keep;
+  const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.MP;
+  const bool scales = static_cast<int>(blockIdx.x) == 2 * slices;
+  uint8_t* pool = static_cast<int>(blockIdx.x) >= slices ? a.v_pool : a.k_pool;
+  const int lpr = scales ? 1 : kSliceBytes / 16;  // threads of a row's slice
+  const int col = slice * kSliceBytes + tid % lpr * 16, rows = kMoveThreads / lpr;
+  const int per_step = rows * kShiftRows, steps = (n + per_step - 1) / per_step;
+  uint4 w[2][kShiftRows];
+  long long dst[2][kShiftRows];
+  const auto load = [&](int step, uint4 (&v)[kShiftRows], long long (&d)[kShiftRows]) {
 #pragma unroll
-    for (int r = 0; r < kMoveRows; ++r)
+    for (int r = 0; r < kShiftRows; ++r) {
+      const int j = step * per_step + r * rows + tid / lpr;
+      d[r] = -1;
+      if (j >= n) continue;
+      const int t = kept[j];
+      if (t == j) continue;  // already there
+      const long long from = pool_row(a, pt, h, t);
+      if (from < 0) continue;
+      d[r] = pool_row(a, pt, h, j);
+      if (scales)
+        v[r].x = static_cast<uint32_t>(__half_as_ushort(a.k_scale[from])) |
+                 (static_cast<uint32_t>(__half_as_ushort(a.v_scale[from])) << 16);
+      else
+        v[r] = *reinterpret_cast<const uint4*>(pool + from * a.row_bytes + col);
+    }
+  };
+  const auto store = [&](const uint4 (&v)[kShiftRows], const long long (&d)[kShiftRows]) {
+#pragma unroll
+    for (int r = 0; r < kShiftRows; ++r)
       if (d[r] >= 0) {
         if (scales) {
           a.k_scale[d[r]] = __ushort_as_half(static_cast<unsigned short>(v[r].x & 0xffffu));
@@ -254,14 +335,14 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(const __grid_consta
         }
       }
   };
-  if (s0 < s1) load(s0, w[0], dst[0]);
-  for (int s = s0; s < s1; s += 2) {
-    if (s + 1 < s1) load(s + 1, w[1], dst[1]);
-    if (a.in_place) __syncthreads();  // every row of this step (and the next) is in registers
+  if (steps > 0) load(0, w[0], dst[0]);
+  for (int s = 0; s < steps; s += 2) {
+    if (s + 1 < steps) load(s + 1, w[1], dst[1]);
+    __syncthreads();  // every row of this step (and the next) is in registers
     store(w[0], dst[0]);
-    if (s + 1 >= s1) break;
-    if (s + 2 < s1) load(s + 2, w[0], dst[0]);
-    if (a.in_place) __syncthreads();
+    if (s + 1 >= steps) break;
+    if (s + 2 < steps) load(s + 2, w[0], dst[0]);
+    __syncthreads();
     store(w[1], dst[1]);
   }
 }
@@ -276,16 +357,18 @@ cudaError_t launch_evict(const spg_params& p, const float* mass, int keep, int n
   a.mass = mass;
   a.mass_out = mass_out;
   a.page_table = page_table;
-  a.in_place = dst_table == nullptr || dst_table == page_table;
-  a.dst_table = a.in_place ? page_table : dst_table;
+  a.dst_table = dst_table;
+  const bool in_place = dst_table == nullptr || dst_table == page_table;
   a.seq_lens = seq_lens;
   a.kept = kept;
   a.new_lens = new_lens;
   a.err = err;
   a.k_pool = static_cast<uint8_t*>(k_pool);
   a.v_pool = static_cast<uint8_t*>(v_pool);
-  a.k_scale = static_cast<__half*>(k_scale);
-  a.v_scale = static_cast<__half*>(v_scale);
+  if (p.kv_dtype == SPG_I8) {
+    a.k_scale = static_cast<__half*>(k_scale);
+    a.v_scale = static_cast<__half*>(v_scale);
+  }
   a.Hkv = p.num_kv_heads;
   a.S = p.page_size;
   a.MP = p.max_pages_per_seq;
@@ -294,23 +377,44 @@ cudaError_t launch_evict(const spg_params& p, const float* mass, int keep, int n
   a.n_sink = n_sink;
   a.n_recent = n_recent;
   a.row_bytes = p.head_dim * (p.kv_dtype == SPG_I8 ? 1 : 2);
-  // within the same pages the rows' 64-byte pieces, to pages of its own whole rows
-  const int slice_bytes = a.in_place ? 64 : a.row_bytes;
-  a.slices = a.row_bytes / slice_bytes;
-  a.lpr_log2 = 0;
-  while ((16 << a.lpr_log2) < slice_bytes) ++a.lpr_log2;
   const int units = p.batch * p.num_kv_heads;
-  cudaError_t e = launch_pdl(k_evict_select, dim3(units), dim3(kSelThreads), 0, stream, a);
+  const long long most = static_cast<long long>(p.max_pages_per_seq) * p.page_size;
+  // one CTA up to 2048 tokens, then as many as keep that share, up to 8
+  int C = 1;
+  while (C < kMaxCluster && most > 2048ll * C) C *= 2;
+  const long long share = (most + C - 1) / C;
+  a.resident = share <= kMaxResident ? 1 : 0;
+  // not resident: a later CTA's writes would meet an earlier one's reads in mass itself
+  if (!a.resident) C = 1;
+  const size_t smem = a.resident ? sizeof(float) * share : 0;
+  cudaError_t e = ensure_smem(k_evict_select, smem);
   if (e != cudaSuccess) return e;
-  int chunks = 1;
-  if (!a.in_place) {
-    const int per_step = (kMoveThreads >> a.lpr_log2) * kMoveRows;
-    const long long most = static_cast<long long>(p.max_pages_per_seq) * p.page_size;
-    const int steps = static_cast<int>((std::min<long long>(keep, most) + per_step - 1) / per_step);
-    chunks = std::max(1, std::min(steps, (8 * device_sm_count() + 2 * units - 1) / (2 * units)));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(C, units);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, k_evict_select, a);
+  if (e != cudaSuccess) return e;
+  if (in_place) {
+    const int x = 2 * (a.row_bytes / kSliceBytes) + (p.kv_dtype == SPG_I8 ? 1 : 0);
+    return launch_pdl(k_evict_shift, dim3(x, units), dim3(kMoveThreads), 0, stream, a);
   }
-  const int y = 2 * a.slices + (p.kv_dtype == SPG_I8 ? 1 : 0);
-  return launch_pdl(k_evict_move, dim3(chunks, y, units), dim3(kMoveThreads), 0, stream, a);
+  const dim3 grid(static_cast<unsigned>((std::min<long long>(keep, most) + kMoveRows - 1) / kMoveRows), units);
+  switch (a.row_bytes) {
+    case 256: return launch_pdl(k_evict_gather<256>, grid, dim3(kMoveThreads), 0, stream, a);
+    case 128: return launch_pdl(k_evict_gather<128>, grid, dim3(kMoveThreads), 0, stream, a);
+    default: return launch_pdl(k_evict_gather<64>, grid, dim3(kMoveThreads), 0, stream, a);
+  }
 }
 
 }  // namespace spg

@@ -387,10 +387,18 @@ def test_evict_ties_and_odd_masses(spg, masses, in_place):
     check_evict(spg, [700, 100, 5000], 300, 3, 20, "f16", "f16", 64, 16, in_place, masses)
 
 
-def check_evict(spg, lens, keep, sink, recent, kv, q, d, S, in_place, masses):
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("masses", ["lognormal", "three"])
+def test_evict_tables_past_shared_memory(spg, masses, in_place):
+    """A page table of more tokens than a cluster's shared memory holds masses of."""
+    check_evict(spg, [3000, 40], 500, 2, 33, "bf16", "bf16", 64, 16, in_place, masses, mp=25000)
+    check_evict(spg, [30000], 20000, 2, 33, "i8", "f16", 64, 16, in_place, masses)
+
+
+def check_evict(spg, lens, keep, sink, recent, kv, q, d, S, in_place, masses, mp=0):
     B, hkv = len(lens), 2
     dst_pages = [-(-min(L, keep) // S) for L in lens]
-    c = R.Chunk(4, hkv, d, S, kv, q, lens, [0] * B, extra_pages=0 if in_place else sum(dst_pages))
+    c = R.Chunk(4, hkv, d, S, kv, q, lens, [0] * B, extra_pages=0 if in_place else sum(dst_pages), mp=mp)
     r = Run(spg, c)
     g = torch.Generator().manual_seed(9)
     N = c.mp * S
