@@ -132,6 +132,11 @@ size_t chunk_workspace_bytes(const spg_params& p, int total_q);
 cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_pool,
                         const void* k_scale, const float* lse, const float* mass_in,
                         float* mass_out, float decay, const Workspace& ws, cudaStream_t stream);
+// launch_mass for few rows per sequence; cudaErrorNotSupported, before
+// launching, for pools it does not take
+cudaError_t launch_mass_few(const spg_params& p, const ChunkRows& r, const void* k_pool,
+                            const void* k_scale, const float* lse, const float* mass_in,
+                            float* mass_out, float decay, int32_t* err, cudaStream_t stream);
 // dst_table NULL (or page_table itself): compact within the sequences' pages
 cudaError_t launch_evict(const spg_params& p, const float* mass, int keep, int n_sink, int n_recent,
                          void* k_pool, void* v_pool, void* k_scale, void* v_scale,

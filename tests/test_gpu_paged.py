@@ -88,6 +88,8 @@ RAGGED = [  # lens, new, rows behind
     ([0, 17, 64, 1], [0, 17, 3, 1], 5),
     ([129, 0, 700, 33], [1, 0, 130, 0], 0),
     ([1000, 255, 256, 257], [2, 255, 1, 128], 3),
+    ([300, 0, 77, 16, 1000], [2, 0, 1, 0, 1], 0),  # few rows everywhere
+    ([600, 601, 9, 40], [0, 30, 0, 1], 1),         # few on average, in one sequence
 ]
 
 
