@@ -54,24 +54,30 @@ constexpr uint32_t kTmemCols = 512;  // S0 S1 O0 O1, 128 columns each
 // ---- the plan -----------------------------------------------------------------------
 // An item is 256 rows, a step 128 of the tokens its rows see.
 struct RowItems : ChunkShape {
-  __device__ int tokens() const { return kItemRows / G; }  // new tokens of an item
-  __device__ int items(const ChunkSeq& s) const { return (s.n + tokens() - 1) / tokens(); }
+  // joining a part costs about as much as a step
+  static constexpr int kLeast = 2;
+  __device__ int log2_tokens() const { return 8 - g_log2; }  // new tokens of an item: 256 / G
+  __device__ int items(const ChunkSeq& s) const { return (s.n + (1 << log2_tokens()) - 1) >> log2_tokens(); }
+  // one past the last token that item i sees
+  __device__ int seen(const ChunkSeq& s, int i) const { return s.pos0 + min((i + 1) << log2_tokens(), s.n); }
+  __device__ int item_steps(const ChunkSeq& s, int i) const { return (seen(s, i) + kTile - 1) / kTile; }
   // the first m items: sum of ceil((pos0 + i q) / 128), the last one ends with the sequence
   __device__ long long steps(const ChunkSeq& s, int m) const {
-    const int q = tokens(), full = min(m, s.n / q);
+    const int lq = log2_tokens(), q = 1 << lq, full = min(m, s.n >> lq);
     long long sum = 0;
     if (q >= kTile) {
       sum = static_cast<long long>(full) * ((s.pos0 + kTile - 1) / kTile) + static_cast<long long>(q / kTile) * full * (full + 1) / 2;
     } else {
-      const int per = kTile / q;
-      for (int r = 1; r <= per && r <= full; ++r) {
-        const long long cnt = (full - r) / per + 1;
+      const int lp = 7 - lq;  // 128 / q items to a step
+      for (int r = 1; r <= 1 << lp && r <= full; ++r) {
+        const long long cnt = ((full - r) >> lp) + 1;
         sum += cnt * ((s.pos0 + r * q + kTile - 1) / kTile) + cnt * (cnt - 1) / 2;
       }
     }
     return m > full ? sum + (s.L + kTile - 1) / kTile : sum;
   }
 };
+static_assert(kItemRows == 256 && kTile == 128, "the shifts above");
 struct Seg : Part {
   int row0, n_rows, last;  // rows of the sequence; the last token any of them sees
 };
@@ -79,10 +85,9 @@ struct SegIter : PartIter<RowItems> {
   using PartIter::PartIter;
   __device__ bool next(Seg& s) {
     if (!PartIter::next(s)) return false;
-    const int q = sh.tokens();
     s.row0 = s.item * kItemRows;
-    s.n_rows = min(kItemRows, s.sq.n * sh.G - s.row0);
-    s.last = s.sq.pos0 + min((s.item + 1) * q, s.sq.n) - 1;
+    s.n_rows = min(kItemRows, (s.sq.n << sh.g_log2) - s.row0);
+    s.last = sh.seen(s.sq, s.item) - 1;
     return true;
   }
 };
@@ -97,7 +102,7 @@ struct ChunkArgs {
   float* lse;
   int32_t *err, *counters;
   float* part;  // [2 * CTAs][D + 2][part_rows]: O by channel, then m and l, so that a warp's rows are neighbours
-  int Hkv, G, S, MP, n_phys, part_rows;
+  int Hkv, S, s_log2, MP, n_phys, part_rows;
   float scale_log2;
 };
 
@@ -209,8 +214,10 @@ struct Kernel {
       // the key tile of this stream's step j, past those that are the other stream's alone
       const auto next_s = [&](int j) {
         for (; jk <= j && jk < n; ++jk) {
-          if (!wait(&m.k_full[ki], kr)) return false;
-          fence_proxy_async();  // the tile was written with plain copies
+          if (step == 2 || jk == 0) {
+            if (!wait(&m.k_full[ki], kr)) return false;
+            fence_proxy_async();
+          }
           tc_fence_after();
           if (elect_one()) {
             if (jk == j) S(qt); else mbar_arrive(&m.k_empty[ki]);
@@ -224,7 +231,9 @@ struct Kernel {
       pass_turn();
       for (int jv = 0; jv < n; ++jv) {
         if (!wait(&m.v_full[vi], vr)) return false;
-        fence_proxy_async();
+        // (and the next keys, which follow while the turn is held)
+        if (step == 1 && jk < n && !wait(&m.k_full[ki], kr)) return false;
+        fence_proxy_async();  // the tiles were written with plain copies
         if (jv == j) {
           if (!wait(&m.p_full[t][0], sc) || !take_turn()) return false;
           tc_fence_after();
@@ -269,7 +278,7 @@ struct Kernel {
       for (int t = 0; t < tiles; ++t)
         for (int hf = 0; hf < NH; ++hf)
           tma_tile_4d(smem + Lay::q_off + t * Lay::kTileBytes + hf * Lay::kHalf, &a.tmq, hf * 64, 0, s.h,
-                      s.sq.start + (s.row0 + t * kTile) / a.G, &m.q_full);
+                      s.sq.start + ((s.row0 + t * kTile) >> a.sh.g_log2), &m.q_full);
     }
   }
 
@@ -282,7 +291,7 @@ struct Kernel {
       if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
     };
     const uint32_t sm = smem_u32(smem);
-    const int s_log2 = 31 - __clz(a.S);
+    const int s_log2 = a.s_log2;
     uint32_t ki = 0, vi = 0, kr = 0, vr = 0;  // stage and round of the rings
     // int8: tiles copied, not yet widened (at most two: a K and a V)
     uint32_t kw = 0, vw = 0;
@@ -299,7 +308,7 @@ struct Kernel {
     Seg s;
     while (it.next(s)) {
       const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
-      const auto pages = [&](int k) { return k < s.k1 ? Tiles::page_of(pt, k * kTile, s.last + 1, a.S, a.n_phys, lane) : -1; };
+      const auto pages = [&](int k) { return k < s.k1 ? Tiles::page_of(pt, k * kTile, s.last + 1, s_log2, a.n_phys, lane) : -1; };
       int page = pages(s.k0);
       for (int k = s.k0; k < s.k1; ++k) {
         const int ahead = pages(k + 1);
@@ -370,8 +379,8 @@ struct Kernel {
 
   // out and lse of a row from its unnormalised O (element i by o(i)), m and l
   static __device__ __forceinline__ size_t out_row(const ChunkArgs& a, const Seg& s, int r) {
-    const int rr = s.row0 + r;
-    return static_cast<size_t>(s.sq.start + rr / a.G) * (a.Hkv * a.G) + s.h * a.G + rr % a.G;
+    const int rr = s.row0 + r, lg = a.sh.g_log2;
+    return (static_cast<size_t>(s.sq.start + (rr >> lg)) * a.Hkv << lg) + (s.h << lg) + (rr & ((1 << lg) - 1));
   }
 
   static __device__ void softmax(const ChunkArgs& a, M& m, uint32_t tmem, int warp, int lane) {
@@ -391,14 +400,14 @@ struct Kernel {
     while (it.next(s)) {
       const bool two = s.n_rows > kTile;
       const int r = two ? t * kTile + tile_row : tile_row;  // row of the item
-      const int pos = s.sq.pos0 + (s.row0 + r) / a.G;
-      const int pos_first = s.sq.pos0 + (s.row0 + (two ? t * kTile : 0)) / a.G;
+      const int pos = s.sq.pos0 + ((s.row0 + r) >> a.sh.g_log2);
+      const int pos_first = s.sq.pos0 + ((s.row0 + (two ? t * kTile : 0)) >> a.sh.g_log2);
       const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
       // does the segment have a bad page at all?
       bool any_bad = false;
       {
-        const int p1 = min(s.k1 * kTile - 1, s.last) / a.S;
-        for (int lp = s.k0 * kTile / a.S + lane; lp <= p1; lp += 32) {
+        const int p1 = min(s.k1 * kTile - 1, s.last) >> a.s_log2;
+        for (int lp = (s.k0 * kTile >> a.s_log2) + lane; lp <= p1; lp += 32) {
           const int page = pt[lp];
           any_bad |= page < 0 || page >= a.n_phys;
         }
@@ -441,7 +450,7 @@ struct Kernel {
               for (int c = 0; c < kHalfTile; c += 16) {
                 const int tok = t0 + half * kHalfTile + c;
                 if (tok <= s.last) {
-                  const int page = pt[tok / a.S];
+                  const int page = pt[tok >> a.s_log2];
                   if (page < 0 || page >= a.n_phys) bad16 |= 1u << (c / 16);
                 }
               }
@@ -763,7 +772,7 @@ cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_
   a.sh.seq_lens = r.seq_lens;
   a.sh.B = p.batch;
   a.sh.Hkv = p.num_kv_heads;
-  a.sh.G = p.num_q_heads / p.num_kv_heads;
+  a.sh.g_log2 = log2_of(p.num_q_heads / p.num_kv_heads);
   a.sh.total_q = r.total_q;
   a.sh.max_tokens = p.max_pages_per_seq * p.page_size;
   a.page_table = r.page_table;
@@ -775,8 +784,8 @@ cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_
   a.counters = reinterpret_cast<int32_t*>(base);
   a.part = reinterpret_cast<float*>(base + round256(sizeof(int32_t) * kMaxCtas));
   a.Hkv = p.num_kv_heads;
-  a.G = p.num_q_heads / p.num_kv_heads;
   a.S = p.page_size;
+  a.s_log2 = log2_of(p.page_size);
   a.MP = p.max_pages_per_seq;
   a.n_phys = p.num_phys_pages;
   a.part_rows = part_rows(p, r.total_q);

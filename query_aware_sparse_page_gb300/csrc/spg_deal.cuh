@@ -7,6 +7,9 @@
 // prefix sums that the kernel's shape gives in closed form:
 //   Shape::items(s)      items of one kv-head of sequence s
 //   Shape::steps(s, m)   steps of the first m of them
+//   Shape::item_steps(s, i)  steps of item i alone (every role asks at every
+//                        item's start: kept to a few instructions)
+//   Shape::kLeast        fewest steps worth a CTA of their own
 // An item that crosses a border is worked on in parts; the CTAs of the parts
 // are consecutive and each can tell who the others are.  No CTA waits for
 // another: the part that arrives last joins them.
@@ -21,7 +24,7 @@ constexpr int kMaxParts = 32;   // most parts an average item is split into
 
 struct ChunkShape {
   const int32_t *q_start, *seq_lens;
-  int B, Hkv, G, total_q, max_tokens;
+  int B, Hkv, g_log2, total_q, max_tokens;  // 2^g_log2 query heads per kv-head
   __device__ ChunkSeq seq(int b, int32_t& bad) const { return chunk_seq(q_start, seq_lens, b, total_q, max_tokens, bad); }
 };
 
@@ -50,7 +53,7 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane) {
   if (bad && blockIdx.x == 0) record_error(err, bad);
   Plan p{};
   p.total = total;
-  long long n = min(static_cast<long long>(gridDim.x), total);
+  long long n = min(static_cast<long long>(gridDim.x), (total + Shape::kLeast - 1) / Shape::kLeast);
   n = min(n, items * kMaxParts);
   p.ctas = static_cast<int>(n);
   const int c = blockIdx.x;
@@ -108,7 +111,7 @@ template <typename Shape>
 struct PartIter {
   const Shape& sh;
   long long pos, hi, item_first;
-  int b, h, item;
+  int b, h, item, n_items;
   ChunkSeq sq;
   __device__ PartIter(const Shape& shape, const Plan& p)
       : sh(shape), pos(p.lo), hi(p.hi), item_first(p.item_first), b(p.b), h(p.h), item(p.item) {
@@ -117,6 +120,7 @@ struct PartIter {
   __device__ void load() {
     int32_t bad = 0;
     sq = sh.seq(b, bad);
+    n_items = sh.items(sq);
   }
   __device__ bool next(Part& s) {
     if (pos >= hi) return false;
@@ -124,18 +128,18 @@ struct PartIter {
     s.b = b;
     s.h = h;
     s.item = item;
-    s.nk = static_cast<int>(sh.steps(sq, item + 1) - sh.steps(sq, item));
+    s.nk = sh.item_steps(sq, item);
     s.item_first = item_first;
     s.k0 = static_cast<int>(pos - item_first);
     s.k1 = static_cast<int>(min(static_cast<long long>(s.nk), hi - item_first));
     pos = item_first + s.k1;
     if (s.k1 == s.nk) {
       item_first += s.nk;
-      if (++item == sh.items(sq)) {
+      if (++item == n_items) {
         item = 0;
         if (++h == sh.Hkv) {
           h = 0;
-          if (pos < hi) do { ++b; load(); } while (sh.items(sq) == 0);
+          if (pos < hi) do { ++b; load(); } while (n_items == 0);
         }
       }
     }

@@ -50,6 +50,12 @@ bool make_q_tmap(CUtensorMap* map, const void* q, const spg_params& p, int total
 Workspace carve_workspace(const spg_params& p, void* ws);
 
 int n_sel_pages(const spg_params& p);
+// of a power of two
+inline int log2_of(int x) {
+  int n = 0;
+  while ((1 << n) < x) ++n;
+  return n;
+}
 int device_sm_count();
 int max_splits(const spg_params& p);
 

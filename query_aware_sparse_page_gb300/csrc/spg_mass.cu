@@ -31,10 +31,12 @@ constexpr int kItemTokens = 2 * kTile;
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 128 columns for each of the two tiles
 
 struct TokenItems : ChunkShape {
+  static constexpr int kLeast = 1;
   __device__ int items(const ChunkSeq& s) const { return (s.L + kItemTokens - 1) / kItemTokens; }
   // row tiles of the sequence, and the first that sees token t
-  __device__ int row_tiles(const ChunkSeq& s) const { return (s.n * G + kTile - 1) / kTile; }
-  __device__ int first_tile(const ChunkSeq& s, int t) const { return t > s.pos0 ? (t - s.pos0) * G / kTile : 0; }
+  __device__ int row_tiles(const ChunkSeq& s) const { return ((s.n << g_log2) + kTile - 1) / kTile; }
+  __device__ int first_tile(const ChunkSeq& s, int t) const { return t > s.pos0 ? ((t - s.pos0) << g_log2) / kTile : 0; }
+  __device__ int item_steps(const ChunkSeq& s, int i) const { return s.n == 0 ? 1 : row_tiles(s) - first_tile(s, i * kItemTokens); }
   // item k is seen by the row tiles from floor((256 k - pos0) G / 128) on: 2 k G - ceil(pos0 G / 128)
   // past pos0 (an item without rows still counts one step, its decay)
   __device__ long long steps(const ChunkSeq& s, int m) const {
@@ -43,8 +45,8 @@ struct TokenItems : ChunkShape {
     const int early = min(m, s.pos0 / kItemTokens + 1);
     long long sum = early * rt;
     if (m > early) {
-      const long long c = (static_cast<long long>(s.pos0) * G + kTile - 1) / kTile, cnt = m - early;
-      sum += cnt * (rt + c) - 2ll * G * (cnt * (early + m - 1) / 2);
+      const long long c = ((static_cast<long long>(s.pos0) << g_log2) + kTile - 1) / kTile, cnt = m - early;
+      sum += cnt * (rt + c) - ((2ll * (cnt * (early + m - 1) / 2)) << g_log2);
     }
     return sum;
   }
@@ -60,7 +62,7 @@ struct MassArgs {
   float* mass_out;
   int32_t *err, *counters;
   float* part;  // [2 * CTAs][256]
-  int Hkv, G, S, MP, n_phys;
+  int Hkv, S, s_log2, MP, n_phys;
   float scale_log2, decay;
 };
 
@@ -145,7 +147,7 @@ struct Kernel {
         if (sc >= 2 && !wait(&m.s_empty[t][buf], (sc >> 1) - 1)) return false;
         tc_fence_after();
         // columns in use, in sixteens
-        const int cols = min(kTile, (s.sq.n * a.G - tile * kTile + 15) & ~15);
+        const int cols = min(kTile, ((s.sq.n << a.sh.g_log2) - tile * kTile + 15) & ~15);
         const uint32_t id = instr_desc<TQ>(kTile, uniform(cols), false);
         if (elect_one()) {
 #pragma unroll
@@ -166,7 +168,7 @@ struct Kernel {
 
   // ---- rows: their tile by TMA, their lse by hand, read one tile ahead (whole warp) ---------
   static __device__ void load_rows(const MassArgs& a, M& m, uint8_t* smem, int lane) {
-    const int g_log2 = 31 - __clz(a.G);
+    const int g_log2 = a.sh.g_log2;
     RowRing ring;
     SegIter it(a.sh, m.plan);
     Seg s;
@@ -185,8 +187,8 @@ struct Kernel {
 #pragma unroll
       for (int i = 0; i < kTile / 32; ++i) {
         const int r = ring.tile * kTile + lane + 32 * i;
-        v[i] = r < s.sq.n * a.G ? a.lse[(static_cast<size_t>(s.sq.start + (r >> g_log2)) * a.Hkv << g_log2) + (s.h << g_log2) +
-                                        (r & (a.G - 1))]
+        v[i] = r < s.sq.n << g_log2 ? a.lse[(static_cast<size_t>(s.sq.start + (r >> g_log2)) * a.Hkv << g_log2) + (s.h << g_log2) +
+                                        (r & ((1 << g_log2) - 1))]
                                 : -INFINITY;
       }
       return true;
@@ -213,7 +215,7 @@ struct Kernel {
     const auto wait = [&](uint64_t* bar, uint32_t phase) {
       if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
     };
-    const int s_log2 = 31 - __clz(a.S);
+    const int s_log2 = a.s_log2;
     uint32_t kc = 0, copied = 0, done = 0;  // items; tiles
     const auto finish = [&] {               // int8: the oldest of the tiles in flight
       const uint32_t x = done++ & 3;
@@ -231,7 +233,7 @@ struct Kernel {
       const int32_t* pt = a.page_table + static_cast<size_t>(ahead.b) * a.MP;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        page_ahead[t] = Tiles::page_of(pt, ahead.item * kItemTokens + t * kTile, ahead.sq.L, a.S, a.n_phys, lane);
+        page_ahead[t] = Tiles::page_of(pt, ahead.item * kItemTokens + t * kTile, ahead.sq.L, s_log2, a.n_phys, lane);
       return true;
     };
     bool more = next();
@@ -286,7 +288,7 @@ struct Kernel {
     const auto next = [&] {
       if (!it.next(ahead)) return false;
       const int tok = ahead.item * kItemTokens + tid;
-      if (tok < ahead.sq.L) page_ahead = a.page_table[static_cast<size_t>(ahead.b) * a.MP + tok / a.S];
+      if (tok < ahead.sq.L) page_ahead = a.page_table[static_cast<size_t>(ahead.b) * a.MP + (tok >> a.s_log2)];
       return true;
     };
     bool more = next();
@@ -299,7 +301,7 @@ struct Kernel {
       float k = a.scale_log2, old = 0.f;
       if (live && !ok && s.tiles > 0) record_error(a.err, SPG_DEVERR_PAGE_ID);
       if constexpr (I8)
-        if (ok) k *= __half2float(a.k_scale[(static_cast<size_t>(page) * a.Hkv + s.h) * a.S + tok % a.S]);
+        if (ok) k *= __half2float(a.k_scale[(static_cast<size_t>(page) * a.Hkv + s.h) * a.S + (tok & (a.S - 1))]);
       if (live && a.mass_in && a.decay > 0.f && tok < s.sq.pos0 && s.k0 == 0) old = a.mass_in[at] * a.decay;
       more = next();
       const uint64_t k2 = f32x2(k, k);
@@ -321,10 +323,10 @@ struct Kernel {
         wait(&m.s_full[t][buf], sc >> 1);
         ++sc;
         tc_fence_after();
-        const int cols = min(kTile, s.sq.n * a.G - tile * kTile);
+        const int cols = min(kTile, (s.sq.n << a.sh.g_log2) - tile * kTile);
         // rows from which on the token is seen (its own is the first)
-        const int from = (tok - s.sq.pos0) * a.G - tile * kTile;
-        const bool masked = cols < kTile || (s.item + 1) * kItemTokens - 1 > s.sq.pos0 + tile * kTile / a.G;
+        const int from = ((tok - s.sq.pos0) << a.sh.g_log2) - tile * kTile;
+        const bool masked = cols < kTile || (s.item + 1) * kItemTokens - 1 > s.sq.pos0 + (tile * kTile >> a.sh.g_log2);
         // half a row in registers at a time; the accumulator goes back with the second
         uint32_t x[kTile / 2];
         if (masked) {
@@ -485,7 +487,7 @@ cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_p
   a.sh.seq_lens = r.seq_lens;
   a.sh.B = p.batch;
   a.sh.Hkv = p.num_kv_heads;
-  a.sh.G = p.num_q_heads / p.num_kv_heads;
+  a.sh.g_log2 = log2_of(p.num_q_heads / p.num_kv_heads);
   a.sh.total_q = r.total_q;
   a.sh.max_tokens = p.max_pages_per_seq * p.page_size;
   a.k_pool = k_pool;
@@ -498,8 +500,8 @@ cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_p
   a.counters = ws.mass_counters;
   a.part = ws.mass_part;
   a.Hkv = p.num_kv_heads;
-  a.G = a.sh.G;
   a.S = p.page_size;
+  a.s_log2 = log2_of(p.page_size);
   a.MP = p.max_pages_per_seq;
   a.n_phys = p.num_phys_pages;
   a.scale_log2 = (p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.head_dim))) * kLog2e;

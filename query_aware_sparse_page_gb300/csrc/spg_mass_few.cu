@@ -24,9 +24,11 @@ constexpr int kRingBytes = 64 * 1024;  // three CTAs per SM
 constexpr int kMaxSlots = 32;        // one per lane of the filling warp
 
 struct PageItems : ChunkShape {
-  int S;
-  __device__ int items(const ChunkSeq& s) const { return (s.L + S - 1) / S; }
+  static constexpr int kLeast = 4;
+  int s_log2;
+  __device__ int items(const ChunkSeq& s) const { return (s.L + (1 << s_log2) - 1) >> s_log2; }
   __device__ long long steps(const ChunkSeq&, int m) const { return m; }
+  __device__ int item_steps(const ChunkSeq&, int) const { return 1; }
 };
 
 struct FewArgs {
@@ -39,7 +41,7 @@ struct FewArgs {
   const float *lse, *mass_in;
   float* mass_out;
   int32_t* err;
-  int Hkv, G, S, MP, n_phys, slots;
+  int Hkv, g_log2, S, MP, n_phys, slots;
   float scale_log2, decay;
 };
 
@@ -197,7 +199,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3) k_mass_few(const __grid_
   c.advance(warp);
   for (int j = warp; j < n; j += kWarps) {
     const int slot = j % slots;
-    const int n_rows = c.sq.n * a.G, groups = (n_rows + 7) / 8;
+    const int n_rows = c.sq.n << a.g_log2, groups = (n_rows + 7) / 8;
     const int tok0 = c.p * S, nv = min(S, c.sq.L - tok0);
     const size_t at = (static_cast<size_t>(c.b) * a.Hkv + c.h) * a.MP * S + tok0;
     bool ok = false;
@@ -210,7 +212,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3) k_mass_few(const __grid_
       if (c.b == have_b && c.h == have_h && grp == have_g) return;
       have_b = c.b, have_h = c.h, have_g = grp;
       const auto row_of = [&](int r) {
-        return (static_cast<size_t>(c.sq.start) + r / a.G) * (static_cast<size_t>(a.Hkv) * a.G) + c.h * a.G + r % a.G;
+        return ((static_cast<size_t>(c.sq.start) + (r >> a.g_log2)) * a.Hkv << a.g_log2) + (c.h << a.g_log2) +
+               (r & ((1 << a.g_log2) - 1));
       };
       const int r = grp * 8 + g;
       rows.load(r < n_rows ? static_cast<const TQ*>(a.q) + row_of(r) * D : nullptr, lane);
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3) k_mass_few(const __grid_
           // the first row that sees the token, of those at or past pos0
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int from = (tok0 + t0 + g + 8 * e - c.sq.pos0) * a.G - grp * 8 - 2 * t;
+            const int from = ((tok0 + t0 + g + 8 * e - c.sq.pos0) << a.g_log2) - grp * 8 - 2 * t;
             if (from <= 0) sum[e] += exp2f(fmaf(s[2 * e], k[e], -l0));
             if (from <= 1) sum[e] += exp2f(fmaf(s[2 * e + 1], k[e], -l1));
           }
@@ -290,10 +293,10 @@ cudaError_t launch_mass_few(const spg_params& p, const ChunkRows& r, const void*
   a.sh.seq_lens = r.seq_lens;
   a.sh.B = p.batch;
   a.sh.Hkv = p.num_kv_heads;
-  a.sh.G = p.num_q_heads / p.num_kv_heads;
+  a.sh.g_log2 = log2_of(p.num_q_heads / p.num_kv_heads);
   a.sh.total_q = r.total_q;
   a.sh.max_tokens = p.max_pages_per_seq * p.page_size;
-  a.sh.S = p.page_size;
+  a.sh.s_log2 = log2_of(p.page_size);
   a.q = r.q;
   a.k_scale = static_cast<const __half*>(k_scale);
   a.page_table = r.page_table;
@@ -302,7 +305,7 @@ cudaError_t launch_mass_few(const spg_params& p, const ChunkRows& r, const void*
   a.mass_out = mass_out;
   a.err = err;
   a.Hkv = p.num_kv_heads;
-  a.G = a.sh.G;
+  a.g_log2 = a.sh.g_log2;
   a.S = p.page_size;
   a.MP = p.max_pages_per_seq;
   a.n_phys = p.num_phys_pages;

@@ -22,10 +22,10 @@ struct TileLoader {
   static constexpr int kPieces = kTile / kRowsPer;
 
   // the pages of the tile of 128 tokens at t0, one per lane (-1: none before `end`, or a bad one)
-  static __device__ __forceinline__ int page_of(const int32_t* pt, int t0, int end, int S, int n_phys, int lane) {
-    const int t = t0 + lane * S;
-    if (lane >= kTile / S || t >= end) return -1;
-    const int page = pt[t / S];
+  static __device__ __forceinline__ int page_of(const int32_t* pt, int t0, int end, int s_log2, int n_phys, int lane) {
+    const int t = t0 + (lane << s_log2);
+    if (lane >= kTile >> s_log2 || t >= end) return -1;
+    const int page = pt[t >> s_log2];
     return page >= 0 && page < n_phys ? page : -1;
   }
   // copies the tile at t0 of kv-head h; tokens at or past L become zeros
