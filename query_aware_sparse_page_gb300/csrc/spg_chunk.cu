@@ -149,7 +149,9 @@ struct Kernel {
   // One warp's waits and issues for both streams took longer than their
   // products.  The streams' batches (P V of a step, S of the next) go to the
   // tensor cores strictly in turn: left to themselves the two fall into step,
-  // both in their softmax while the tensor cores idle, then both in line.
+  // both in their softmax while the tensor cores idle, then both in line
+  // (976 against 925 us for a prompt piece at 32K; with int8 pages, whose
+  // widening sets the pace, the turns only cost: 545 against 490 us).
   static __device__ bool issue(const ChunkArgs& a, M& m, uint32_t smem, uint32_t tmem, int t) {
     const auto wait = [&](uint64_t* bar, uint32_t phase) {  // the whole warp goes on, or none of it
       return __all_sync(0xffffffffu, Waiter{a.err}(bar, phase)) != 0;
@@ -203,12 +205,12 @@ struct Kernel {
       // (with one tile of rows the streams' batches differ in number, and the
       // keys' bytes bound them anyway)
       const auto take_turn = [&] {
-        if (step == 2) return true;
+        if (I8 || step == 2) return true;
         const uint32_t round = tc++;
         return t == 1 ? wait(&m.turn[1], round) : round == 0 || wait(&m.turn[0], round - 1);
       };
       const auto pass_turn = [&] {
-        if (step == 1 && elect_one()) mbar_arrive(&m.turn[t ^ 1]);
+        if (!I8 && step == 1 && elect_one()) mbar_arrive(&m.turn[t ^ 1]);
         __syncwarp();
       };
       // the key tile of this stream's step j, past those that are the other stream's alone
