@@ -112,7 +112,7 @@ struct Layout {
   static constexpr int NH = D / 64;  // 64-channel halves
   static constexpr uint32_t kHalf = kTile * 128;
   static constexpr uint32_t kTileBytes = NH * kHalf;
-  static constexpr int KST = D == 128 ? (I8 ? 2 : 3) : 4, VST = D == 128 ? 2 : 4;
+  static constexpr int KST = D == 128 ? 2 : 4, VST = D == 128 ? 2 : 4;
   static constexpr uint32_t q_off = 0, k_off = 2 * kTileBytes, v_off = k_off + KST * kTileBytes;
   static constexpr uint32_t misc = v_off + VST * kTileBytes;
 };
@@ -122,7 +122,8 @@ struct Misc {
   Plan plan;
   uint32_t tmem;
   int last;
-  float ml[kTile][2];                            // stream 1's m and l, joined by stream 0
+  float top[2][2][2][kTile];  // largest logit of a step, per stream and half of the tokens
+  float sum[2][2][kTile], max[2][kTile];  // a segment's sums per stream and half, and its m
   alignas(16) float ones[I8 ? kTile : 1];
   alignas(16) float scales[I8 ? VST : 1][2][I8 ? kTile : 1];  // int8: scale * key scale, 16 * value scale of a step's tokens
 };
@@ -133,13 +134,13 @@ struct Kernel {
   using Lay = Layout<D, I8>;
   static constexpr int KST = Lay::KST, VST = Lay::VST, NH = Lay::NH;
   using M = Misc<KST, VST, I8>;
-  // warpgroups 0, 1: softmax; 2: loads; 3: the two issuing warps, the warp
-  // that loads Q, an idle one
-  static constexpr int kThreads = 512, kLoadWarp = 8, kMmaWarp = 12, kQWarp = 14;
-  // registers per thread: 128 at launch, then each warpgroup's share of the
-  // same total; a softmax thread holds half a row of 128 logits
-  static constexpr int kRegsSoftmax = 168, kRegsLoad = 112, kRegsIssue = 64;
-  static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 4 * 128, "the block's registers");
+  // warpgroups 0-3: softmax, two for each stream; 4: loads; 5: the two
+  // issuing warps, the warp that loads Q, an idle one
+  static constexpr int kThreads = 768, kSoftmax = 512, kLoadWarp = 16, kMmaWarp = 20, kQWarp = 22;
+  // registers per thread: 80 at launch, then each warpgroup's share of the
+  // same total
+  static constexpr int kRegsSoftmax = 88, kRegsLoad = 72, kRegsIssue = 56;
+  static_assert(4 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 6 * 80, "the block's registers");
   static constexpr int kLoadThreads = 128;
   // fp16 holds p * 16 * (value scale) for scales up to 255
   static constexpr float kSlack = I8 ? 4.f : 8.f;
@@ -184,13 +185,13 @@ struct Kernel {
       mma_commit(&m.s_full[t]);
       mma_commit(&m.k_empty[ki]);
     };
-    // half the step's tokens: the first half starts while the second is in its softmax
+    // half the step's tokens, each half's P from a warpgroup of its own
     const auto PV = [&](int half, bool acc) {
       const uint32_t v = dv + vi * kStep;
 #pragma unroll
       for (int i = 0; i < kTile / 32; ++i) {
         const int ks = half * (kTile / 32) + i;
-        mma_ts(tO, tS + 8 * ks, v + ks * (16 * 128 >> 4), idO, acc || ks > 0);
+        mma_ts(tO, tS + 64 * half + 8 * i, v + ks * (16 * 128 >> 4), idO, acc || ks > 0);
       }
     };
     SegIter it(a.sh, m.plan);
@@ -369,7 +370,8 @@ struct Kernel {
   }
 
   // ---- softmax ------------------------------------------------------------------------------------
-  // A thread's row over the steps of one stream; m in the log2 domain.
+  // A thread has a row, over half of a step's tokens, and of the output half
+  // of the channels; m in the log2 domain, the same in both threads.
   struct Row {
     float m, l;
   };
@@ -392,10 +394,14 @@ struct Kernel {
     const auto wait = [&](uint64_t* bar, uint32_t phase) {
       if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
     };
-    const int t = warp >> 2, tid = threadIdx.x;  // stream, 0 .. 255
+    // stream, half of the step's tokens (and of the head's channels), row
+    const int t = warp >> 3, h = (warp >> 2) & 1, tid = threadIdx.x;
     const int tile_row = (warp & 3) * 32 + lane;
+    // the two warps of the same 32 rows
+    const int pair = 4 + 4 * t + (warp & 3);
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t tS = lanes + t * 128, tO = lanes + 256 + t * 128;
+    constexpr int kHalf = kTile / 2, kDh = D / 2;
+    const uint32_t tS = lanes + t * 128 + h * kHalf, tO = lanes + 256 + t * 128 + h * kDh;
     uint32_t sc = 0, oc = 0, vc = 0;
     SegIter it(a.sh, m.plan);
     Seg s;
@@ -428,49 +434,45 @@ struct Kernel {
         wait(&m.s_full[t], sc);
         ++sc;
         tc_fence_after();
-        // Half a row of logits in registers at a time: the maximum of the upper
-        // half, then of the lower, which stays; the upper is read again when
-        // its turn comes.  int8: logits times their key scales.
-        constexpr int kHalfTile = kTile / 2;
+        // 32 logits in registers at a time: the maximum of the upper ones,
+        // then of the lower, which stay; the upper are read again when their
+        // turn comes.  int8: logits times their key scales.
         const float* ks = m.ones;
-        if constexpr (I8) ks = m.scales[stage][0];
-        const int t0 = k * kTile;
-        const bool masked = t0 + kTile - 1 > pos_first || any_bad;
-        uint32_t x[kHalfTile];
+        if constexpr (I8) ks = m.scales[stage][0] + h * kHalf;
+        const int t0 = k * kTile + h * kHalf;
+        const bool masked = k * kTile + kTile - 1 > pos_first || any_bad;
+        uint32_t x[32];
         float top = -INFINITY;
 #pragma unroll
-        for (int half = 1; half >= 0; --half) {
-          const uint32_t at = tS + half * kHalfTile;
-          tmem_ld32(x, at);
-          tmem_ld32(x + 32, at + 32);
+        for (int q = 1; q >= 0; --q) {
+          tmem_ld32(x, tS + 32 * q);
           tmem_wait_ld();
           const auto f = [&](int c) { return __uint_as_float(x[c]); };
           if (masked) {
             // the step's last tokens are hidden from some row, or a page is bad (per 16 tokens)
             unsigned bad16 = 0;
             if (any_bad)
-              for (int c = 0; c < kHalfTile; c += 16) {
-                const int tok = t0 + half * kHalfTile + c;
+              for (int c = 0; c < 32; c += 16) {
+                const int tok = t0 + 32 * q + c;
                 if (tok <= s.last) {
                   const int page = pt[tok >> a.s_log2];
                   if (page < 0 || page >= a.n_phys) bad16 |= 1u << (c / 16);
                 }
               }
-            const int lim = pos - t0 - half * kHalfTile;
+            const int lim = pos - t0 - 32 * q;
 #pragma unroll
-            for (int c = 0; c < kHalfTile; ++c) {
-              if constexpr (I8) x[c] = __float_as_uint(f(c) * ks[half * kHalfTile + c]);
+            for (int c = 0; c < 32; ++c) {
+              if constexpr (I8) x[c] = __float_as_uint(f(c) * ks[32 * q + c]);
               if (c > lim || ((bad16 >> (c / 16)) & 1u)) x[c] = 0xff800000u;  // -inf
             }
-            tmem_st32(at, x);
-            tmem_st32(at + 32, x + 32);
+            tmem_st32(tS + 32 * q, x);
           }
           float mx[4] = {top, top, top, top};  // chains that do not wait for one another
           if (I8 && !masked) {
 #pragma unroll
-            for (int c = 0; c < kHalfTile; c += 8) {
-              const float4 u = *reinterpret_cast<const float4*>(ks + half * kHalfTile + c);
-              const float4 w = *reinterpret_cast<const float4*>(ks + half * kHalfTile + c + 4);
+            for (int c = 0; c < 32; c += 8) {
+              const float4 u = *reinterpret_cast<const float4*>(ks + 32 * q + c);
+              const float4 w = *reinterpret_cast<const float4*>(ks + 32 * q + c + 4);
               mx[0] = fmaxf(fmaxf(mx[0], f(c) * u.x), f(c + 4) * w.x);
               mx[1] = fmaxf(fmaxf(mx[1], f(c + 1) * u.y), f(c + 5) * w.y);
               mx[2] = fmaxf(fmaxf(mx[2], f(c + 2) * u.z), f(c + 6) * w.z);
@@ -478,30 +480,39 @@ struct Kernel {
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < kHalfTile; c += 8)
+            for (int c = 0; c < 32; c += 8)
 #pragma unroll
               for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], f(c + i)), f(c + 4 + i));
           }
           top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         }
         if (I8 && masked) ks = m.ones;  // the logits went back with their scales
+        // the row's maximum over both halves (two buffers: the other warp may
+        // be a step ahead)
+        float* mine = &m.top[sc & 1][t][h][tile_row];
+        *mine = top;
+        bar_sync(pair, 64);
+        top = fmaxf(top, m.top[sc & 1][t][h ^ 1][tile_row]);
         if constexpr (!I8) top *= a.scale_log2;
         const bool raise = top > row.m + kSlack;  // -inf + kSlack = -inf: the first finite logit
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__any_sync(0xffffffffu, raise)) {     // the same in both warps
           const float mn = raise ? top : row.m;
           const float factor = row.m == -INFINITY ? (raise ? 0.f : 1.f) : ex2(row.m - mn);
           row.m = mn;
           row.l *= factor;
           if (k >= s.k0 + step) {  // O holds earlier steps (all done: S of this step was issued after them)
+            uint32_t o[16];
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o, tO + c);
+            for (int c = 0; c < kDh; c += 16) {
+              tmem_ld16(o, tO + c);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-              tmem_st32(tO + c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+              tmem_st16(tO + c, o);
             }
+            tmem_wait_st();
+            tc_fence_before();
+            bar_sync(pair, 64);  // the first half's products touch the other's channels too
           }
         }
         const float mm = row.m == -INFINITY ? 0.f : row.m;
@@ -509,35 +520,32 @@ struct Kernel {
         uint64_t l0 = f32x2(0.f, 0.f), l1 = l0;
         if (masked) tmem_wait_st();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (half == 1) tmem_wait_ld();
+        for (int q = 0; q < 2; ++q) {
+          if (q == 1) tmem_wait_ld();
+          uint32_t w[16];
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int c0 = half * kHalfTile + 32 * q;  // first token of these 32
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t z = f32x2(__uint_as_float(x[32 * q + 2 * i]), __uint_as_float(x[32 * q + 2 * i + 1]));
-              uint64_t mul = sc2;
-              if constexpr (I8) mul = *reinterpret_cast<const uint64_t*>(ks + c0 + 2 * i);
-              const float2 e = unpack_f32x2(fma_f32x2(z, mul, nm));
-              float2 p = make_float2(ex2(e.x), ex2(e.y));
-              if (i & 1) l1 = add_f32x2(l1, f32x2(p.x, p.y)); else l0 = add_f32x2(l0, f32x2(p.x, p.y));
-              if constexpr (I8) {
-                const float2 vs = *reinterpret_cast<const float2*>(&m.scales[stage][1][c0 + 2 * i]);
-                p.x *= vs.x;
-                p.y *= vs.y;
-              }
-              w[i] = pack2<TQ>(p.x, p.y);
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t z = f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+            uint64_t mul = sc2;
+            if constexpr (I8) mul = *reinterpret_cast<const uint64_t*>(ks + 32 * q + 2 * i);
+            const float2 e = unpack_f32x2(fma_f32x2(z, mul, nm));
+            float2 p = make_float2(ex2(e.x), ex2(e.y));
+            if (i & 1) l1 = add_f32x2(l1, f32x2(p.x, p.y)); else l0 = add_f32x2(l0, f32x2(p.x, p.y));
+            if constexpr (I8) {
+              const float2 vs = *reinterpret_cast<const float2*>(&m.scales[stage][1][h * kHalf + 32 * q + 2 * i]);
+              p.x *= vs.x;
+              p.y *= vs.y;
             }
-            // the lower half's logits are all in registers, the upper half's lie beyond P
-            tmem_st16(tS + c0 / 2, w);
-            if (half == 0) tmem_ld32(x + 32 * q, tS + kHalfTile + 32 * q);
+            w[i] = pack2<TQ>(p.x, p.y);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&m.p_full[t][half]);
+          // P of the half goes over its own first 32 logits: these are in
+          // registers, and the others are read before the second store
+          if (q == 0) tmem_ld32(x, tS + 32);
+          tmem_st16(tS + 16 * q, w);
         }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&m.p_full[t][h]);
         const float2 s0 = unpack_f32x2(l0), s1 = unpack_f32x2(l1);
         row.l += (s0.x + s0.y) + (s1.x + s1.y);
       }
@@ -545,22 +553,24 @@ struct Kernel {
 
       // ---- the segment's end ----
       const bool whole = s.whole();
+      m.sum[t][h][tile_row] = row.l;
+      if (h == 0) m.max[t][tile_row] = row.m;
       wait(&m.o_full[t], oc);
       float f0 = 1.f, f1 = 0.f;
-      if (!two) {  // the rows' two streams
-        if (t == 1) {
-          m.ml[tile_row][0] = row.m;
-          m.ml[tile_row][1] = row.l;
-        } else {
-          wait(&m.o_full[1], oc);
-        }
-        bar_sync(1, 256);
+      if (two) {
+        bar_sync(pair, 64);
+        row.l += m.sum[t][h ^ 1][tile_row];
+        bar_sync(pair, 64);  // read before the next segment's are written
+      } else {  // the rows' two streams
+        if (t == 0) wait(&m.o_full[1], oc);
+        bar_sync(1, kSoftmax);
         if (t == 0) {
-          const float m1 = m.ml[tile_row][0], l1 = m.ml[tile_row][1];
+          const float m1 = m.max[1][tile_row], l1 = m.sum[1][0][tile_row] + m.sum[1][1][tile_row];
+          const float l0 = m.sum[0][0][tile_row] + m.sum[0][1][tile_row];
           const float mm = fmaxf(row.m, m1);
           f0 = row.m == -INFINITY ? 0.f : ex2(row.m - mm);
           f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
-          row.l = row.l * f0 + l1 * f1;
+          row.l = l0 * f0 + l1 * f1;
           row.m = mm;
         }
       }
@@ -576,43 +586,46 @@ struct Kernel {
         }
         const size_t orow = live ? out_row(a, s, r) : 0;
         float* part = part_at(a, own_slot(s), live ? r : 0);
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o, tO + c);
+#pragma unroll 1
+        for (int c = 0; c < kDh; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(o, tO + c);
           tmem_wait_ld();
           // f0 = 0 stands for rows that saw nothing: their O may not be trusted to be finite
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(f0 == 0.f ? 0.f : __uint_as_float(o[i]) * f0);
           if (both) {
-            uint32_t o1[32];
-            tmem_ld32(o1, tO + 128 + c);
+            uint32_t o1[16];
+            tmem_ld16(o1, tO + 128 + c);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 16; ++i)
               if (f1 != 0.f) o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
           }
           if (live && whole) {
-            TQ* dst = static_cast<TQ*>(a.out) + orow * D + c;
+            TQ* dst = static_cast<TQ*>(a.out) + orow * D + h * kDh + c;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8)
+            for (int i = 0; i < 16; i += 8)
               *reinterpret_cast<uint4*>(dst + i) = make_uint4(pack2<TQ>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
                                                              pack2<TQ>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
                                                              pack2<TQ>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
                                                              pack2<TQ>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
           } else if (live) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) __stcg(part + (c + i) * a.part_rows, __uint_as_float(o[i]));
+            for (int i = 0; i < 16; ++i) __stcg(part + (h * kDh + c + i) * a.part_rows, __uint_as_float(o[i]));
           }
         }
-        if (live && whole && a.lse) a.lse[orow] = row.l > 0.f ? (row.m + log2f(row.l)) * kLn2 : -INFINITY;
-        if (live && !whole) {
-          __stcg(part + D * a.part_rows, row.m);
-          __stcg(part + (D + 1) * a.part_rows, row.l);
+        if (live && h == 0) {
+          if (whole) {
+            if (a.lse) a.lse[orow] = row.l > 0.f ? (row.m + log2f(row.l)) * kLn2 : -INFINITY;
+          } else {
+            __stcg(part + D * a.part_rows, row.m);
+            __stcg(part + (D + 1) * a.part_rows, row.l);
+          }
         }
       }
       tc_fence_before();  // the loads of O come before the next segment's first product
-      if (!two) bar_sync(2, 256);
+      if (!two) bar_sync(2, kSoftmax);
       if (!whole) join(a, m, s, tid);
     }
   }
@@ -622,39 +635,40 @@ struct Kernel {
     const PartRange pr(m.plan, s);
     const int c0 = pr.c0, c1 = pr.c1;
     __threadfence();
-    bar_sync(1, 256);
+    bar_sync(1, kSoftmax);
     if (tid == 0) m.last = atomicAdd(&a.counters[c0], 1) == c1 - c0;
-    bar_sync(2, 256);
+    bar_sync(2, kSoftmax);
     if (!m.last) return;
     __threadfence();
-    // a thread per row, or two with half the channels each
+    // two threads per row with half the channels each, or four with a quarter
     const bool two = s.n_rows > kTile;
-    const int r = two ? tid : tid % kTile, d0 = two ? 0 : tid / kTile * (D / 2), d1 = two ? D : d0 + D / 2;
+    const int r = tid % (two ? kItemRows : kTile), share = two ? D / 2 : D / 4;
+    const int d0 = tid / (two ? kItemRows : kTile) * share, d1 = d0 + share;
     if (r < s.n_rows) {
       const auto at = [&](int c) { return part_at(a, pr.slot(c), r); };
       float mm = -INFINITY, l = 0.f;
-#pragma unroll 4
+#pragma unroll 2
       for (int c = c0; c <= c1; ++c) mm = fmaxf(mm, __ldcg(at(c) + D * a.part_rows));
       if (mm == -INFINITY) mm = 0.f;  // every part's weight is 0
-#pragma unroll 4
+#pragma unroll 2
       for (int c = c0; c <= c1; ++c)
         l = fmaf(__ldcg(at(c) + (D + 1) * a.part_rows), ex2(__ldcg(at(c) + D * a.part_rows) - mm), l);
       const float inv = l > 0.f ? (1.f / kVScale) / l : 0.f;
       const size_t orow = out_row(a, s, r);
       TQ* dst = static_cast<TQ*>(a.out) + orow * D;
-      for (int d = d0; d < d1; d += 32) {
-        float o[32];
+      for (int d = d0; d < d1; d += 16) {
+        float o[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        for (int i = 0; i < 16; ++i) o[i] = 0.f;
         for (int c = c0; c <= c1; ++c) {
           const float* p = at(c);
           const float f = ex2(__ldcg(p + D * a.part_rows) - mm);
           p += d * a.part_rows;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = fmaf(__ldcg(p + i * a.part_rows), f, o[i]);
+          for (int i = 0; i < 16; ++i) o[i] = fmaf(__ldcg(p + i * a.part_rows), f, o[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
+        for (int i = 0; i < 16; i += 8)
           *reinterpret_cast<uint4*>(dst + d + i) =
               make_uint4(pack2<TQ>(o[i] * inv, o[i + 1] * inv), pack2<TQ>(o[i + 2] * inv, o[i + 3] * inv),
                          pack2<TQ>(o[i + 4] * inv, o[i + 5] * inv), pack2<TQ>(o[i + 6] * inv, o[i + 7] * inv));
@@ -666,7 +680,7 @@ struct Kernel {
 };
 
 template <typename T, typename TQ, int D>
-__global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const __grid_constant__ ChunkArgs a) {
+__global__ void __launch_bounds__(768, 1) k_chunk(const __grid_constant__ ChunkArgs a) {
   using K = Kernel<T, TQ, D>;
   using Lay = typename K::Lay;
   using M = typename K::M;
@@ -704,7 +718,7 @@ __global__ void __launch_bounds__((Kernel<T, TQ, D>::kThreads), 1) k_chunk(const
   tc_fence_after();
   const uint32_t tmem = m.tmem;
 
-  if (warp < 8) {
+  if (warp < K::kLoadWarp) {
     regs_up<K::kRegsSoftmax>();
     K::softmax(a, m, tmem, warp, lane);
   } else {
