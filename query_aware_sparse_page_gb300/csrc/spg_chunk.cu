@@ -56,6 +56,8 @@ constexpr uint32_t kTmemCols = 512;  // S0 S1 O0 O1, 128 columns each
 struct RowItems : ChunkShape {
   // joining a part costs about as much as a step
   static constexpr int kLeast = 2;
+  // a short item of 256 rows takes 14000 cycles beside its steps of 3400
+  static constexpr int kExtra = 4;
   __device__ int log2_tokens() const { return 8 - g_log2; }  // new tokens of an item: 256 / G
   __device__ int items(const ChunkSeq& s) const { return (s.n + (1 << log2_tokens()) - 1) >> log2_tokens(); }
   // one past the last token that item i sees
@@ -74,7 +76,8 @@ struct RowItems : ChunkShape {
         sum += cnt * ((s.pos0 + r * q + kTile - 1) / kTile) + cnt * (cnt - 1) / 2;
       }
     }
-    return m > full ? sum + (s.L + kTile - 1) / kTile : sum;
+    if (m > full) sum += (s.L + kTile - 1) / kTile;
+    return sum + static_cast<long long>(m) * kExtra;
   }
 };
 static_assert(kItemRows == 256 && kTile == 128, "the shifts above");
@@ -660,6 +663,7 @@ struct Kernel {
         float o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 2
         for (int c = c0; c <= c1; ++c) {
           const float* p = at(c);
           const float f = ex2(__ldcg(p + D * a.part_rows) - mm);

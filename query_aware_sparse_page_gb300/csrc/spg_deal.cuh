@@ -10,6 +10,8 @@
 //   Shape::item_steps(s, i)  steps of item i alone (every role asks at every
 //                        item's start: kept to a few instructions)
 //   Shape::kLeast        fewest steps worth a CTA of their own
+//   Shape::kExtra        what an item costs beside its steps, in steps: it
+//                        follows them in the count (steps() holds it)
 // An item that crosses a border is worked on in parts; the CTAs of the parts
 // are consecutive and each can tell who the others are.  No CTA waits for
 // another: the part that arrives last joins them.
@@ -123,27 +125,30 @@ struct PartIter {
     n_items = sh.items(sq);
   }
   __device__ bool next(Part& s) {
-    if (pos >= hi) return false;
-    s.sq = sq;
-    s.b = b;
-    s.h = h;
-    s.item = item;
-    s.nk = sh.item_steps(sq, item);
-    s.item_first = item_first;
-    s.k0 = static_cast<int>(pos - item_first);
-    s.k1 = static_cast<int>(min(static_cast<long long>(s.nk), hi - item_first));
-    pos = item_first + s.k1;
-    if (s.k1 == s.nk) {
-      item_first += s.nk;
-      if (++item == n_items) {
-        item = 0;
-        if (++h == sh.Hkv) {
-          h = 0;
-          if (pos < hi) do { ++b; load(); } while (n_items == 0);
+    while (pos < hi) {
+      s.sq = sq;
+      s.b = b;
+      s.h = h;
+      s.item = item;
+      s.nk = sh.item_steps(sq, item);
+      s.item_first = item_first;
+      s.k0 = static_cast<int>(pos - item_first);
+      s.k1 = static_cast<int>(min(static_cast<long long>(s.nk), hi - item_first));
+      const long long end = item_first + s.nk + Shape::kExtra;
+      pos = min(end, hi);
+      if (pos == end) {
+        item_first = end;
+        if (++item == n_items) {
+          item = 0;
+          if (++h == sh.Hkv) {
+            h = 0;
+            if (pos < hi) do { ++b; load(); } while (n_items == 0);
+          }
         }
       }
+      if (s.k0 < s.k1) return true;  // else the share began behind the item's last step
     }
-    return true;
+    return false;
   }
 };
 

@@ -31,7 +31,7 @@ constexpr int kItemTokens = 2 * kTile;
 constexpr uint32_t kTmemCols = 512;  // two accumulators of 128 columns for each of the two tiles
 
 struct TokenItems : ChunkShape {
-  static constexpr int kLeast = 1;
+  static constexpr int kLeast = 1, kExtra = 0;
   __device__ int items(const ChunkSeq& s) const { return (s.L + kItemTokens - 1) / kItemTokens; }
   // row tiles of the sequence, and the first that sees token t
   __device__ int row_tiles(const ChunkSeq& s) const { return ((s.n << g_log2) + kTile - 1) / kTile; }

@@ -24,7 +24,7 @@ constexpr int kRingBytes = 64 * 1024;  // three CTAs per SM
 constexpr int kMaxSlots = 32;        // one per lane of the filling warp
 
 struct PageItems : ChunkShape {
-  static constexpr int kLeast = 4;
+  static constexpr int kLeast = 4, kExtra = 0;
   int s_log2;
   __device__ int items(const ChunkSeq& s) const { return (s.L + (1 << s_log2) - 1) >> s_log2; }
   __device__ long long steps(const ChunkSeq&, int m) const { return m; }
