@@ -142,7 +142,7 @@ struct Kernel {
   static constexpr int kThreads = 768, kSoftmax = 512, kLoadWarp = 16, kMmaWarp = 20, kQWarp = 22;
   // registers per thread: 80 at launch, then each warpgroup's share of the
   // same total
-  static constexpr int kRegsSoftmax = 88, kRegsLoad = 72, kRegsIssue = 56;
+  static constexpr int kRegsSoftmax = 96, kRegsLoad = 56, kRegsIssue = 40;
   static_assert(4 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 6 * 80, "the block's registers");
   static constexpr int kLoadThreads = 128;
   // fp16 holds p * 16 * (value scale) for scales up to 255
@@ -418,6 +418,7 @@ struct Kernel {
       bool any_bad = false;
       {
         const int p1 = min(s.k1 * kTile - 1, s.last) >> a.s_log2;
+#pragma unroll 4
         for (int lp = (s.k0 * kTile >> a.s_log2) + lane; lp <= p1; lp += 32) {
           const int page = pt[lp];
           any_bad |= page < 0 || page >= a.n_phys;
