@@ -222,6 +222,81 @@ def test_chunk_offsets_past_32_bits(spg):
     assert torch.equal(host(r.k_pool[n_phys - c.n_phys + int(c2.page_table[0, j // 16]), 0, j % 16]), src[0])
 
 
+@pytest.mark.parametrize("scale", [0.01, 0.3, 2.0])
+def test_chunk_attention_softmax_scale(spg, scale):
+    """A caller's own scale: the reference's logits are those of q times scale sqrt(d)."""
+    c = R.Chunk(4, 2, 64, 16, "bf16", "bf16", [300, 90], [40, 90])
+    r = Run(spg, c, softmax_scale=scale)
+    r.chunk()
+    assert r.err() == 0
+    exact = c.q
+    c.q = c.q.double() * (scale * 8.0)
+    out, tol, lse, lse_tol = R.attention(c)
+    c.q = exact
+    close(r.out, out, tol, "out")
+    close(r.lse, lse, lse_tol, "lse")
+
+
+def test_chunk_attention_many_sequences_and_odd_heads(spg):
+    """More sequences than a warp has lanes, three kv-heads, prompts, continuations and empty ones."""
+    g = torch.Generator().manual_seed(11)
+    lens = torch.randint(0, 400, (70,), generator=g).tolist()
+    new = [min(L, n) for L, n in zip(lens, torch.randint(0, 90, (70,), generator=g).tolist())]
+    new[3:40:4] = [0] * len(new[3:40:4])
+    for kv, q in (("f16", "f16"), ("i8", "bf16")):
+        c = R.Chunk(6, 3, 64, 32, kv, q, lens, new, pad_rows=7)
+        r = Run(spg, c)
+        r.chunk()
+        assert r.err() == 0
+        check_chunk(r)
+        want, tol = R.mass_of(c, host(r.lse), None, 1.0)
+        m = torch.zeros((70, 3, c.mp * 32), device="cuda")
+        r.mass(r.lse, None, m, 1.0)
+        assert r.err() == 0
+        for b, L in enumerate(lens):
+            close(m[b, :, :L], want[b, :, :L], tol[b, :, :L], "mass")
+
+
+def test_one_workspace_for_chunks_of_all_sizes(spg):
+    """Chunks of other sizes, batches and lengths one after the other on the workspace of the largest."""
+    big = R.Chunk(8, 2, 128, 16, "bf16", "bf16", [4000, 700, 1], [600, 10, 1])
+    small = R.Chunk(8, 2, 128, 16, "bf16", "bf16", [4000, 33, 5], [1, 1, 1], mp=big.mp)
+    rb, rs = Run(spg, big), Run(spg, small)
+    rs.ws = rb.ws
+    for r in (rb, rs, rb, rs):
+        r.out.fill_(7.0)
+        r.lse.fill_(7.0)
+        r.chunk()
+        assert r.err() == 0
+        check_chunk(r)
+
+
+def test_two_streams_with_their_own_workspaces(spg):
+    """Two chunks, their weights and an eviction in flight at once give what they give alone."""
+    rs = [Run(spg, R.Chunk(8, 2, 128, 16, "bf16", "bf16", [3000, 900], [300, 900], seed=s)) for s in (1, 2)]
+    masses = [torch.zeros((2, 2, r.c.mp * 16), device="cuda") for r in rs]
+    alone = []
+    for r, m in zip(rs, masses):
+        r.chunk()
+        r.mass(r.lse, None, m, 1.0)
+        alone.append([t.clone() for t in (r.out, r.lse, m)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in rs]
+    for _ in range(5):
+        for r, m in zip(rs, masses):
+            r.out.zero_(), r.lse.zero_(), m.zero_()
+        torch.cuda.synchronize()
+        for st, r, m in zip(streams, rs, masses):
+            with torch.cuda.stream(st):
+                r.chunk()
+                r.mass(r.lse, None, m, 1.0)
+        torch.cuda.synchronize()
+        for r, m, want in zip(rs, masses, alone):
+            assert r.err() == 0
+            for a, b in zip((r.out, r.lse, m), want):
+                assert torch.equal(a, b)
+
+
 # ---- mass -------------------------------------------------------------------------------------
 
 
@@ -395,6 +470,7 @@ def test_evict_tables_past_shared_memory(spg, masses, in_place):
     """A page table of more tokens than a cluster's shared memory holds masses of."""
     check_evict(spg, [3000, 40], 500, 2, 33, "bf16", "bf16", 64, 16, in_place, masses, mp=25000)
     check_evict(spg, [30000], 20000, 2, 33, "i8", "f16", 64, 16, in_place, masses)
+    check_evict(spg, [20000], 500, 2, 33, "f16", "f16", 64, 16, in_place, masses, mp=24576)  # the most that it holds
 
 
 def check_evict(spg, lens, keep, sink, recent, kv, q, d, S, in_place, masses, mp=0):
