@@ -83,11 +83,24 @@ struct RowItems : ChunkShape {
 static_assert(kItemRows == 256 && kTile == 128, "the shifts above");
 struct Seg : Part {
   int row0, n_rows, last;  // rows of the sequence; the last token any of them sees
+  int rot;
+  // Step i of the part.  They may come in any order, so they start where a CTA
+  // that had walked one item after another from the start of the launch would
+  // be by now: CTAs with items of the same kv-head then read the same keys
+  // and values at about the same time, once from memory and else from L2
+  // (MHA at 32K, where the heads' caches are four times the L2).
+  __device__ int at(int i) const {
+    const int k = k0 + rot + i;
+    return k < k1 ? k : k - (k1 - k0);
+  }
 };
 struct SegIter : PartIter<RowItems> {
-  using PartIter::PartIter;
+  long long lo;
+  __device__ SegIter(const RowItems& shape, const Plan& p) : PartIter(shape, p), lo(p.lo) {}
   __device__ bool next(Seg& s) {
     if (!PartIter::next(s)) return false;
+    const int by_now = static_cast<int>((s.item_first + s.k0 - lo) % s.nk);
+    s.rot = by_now >= s.k0 && by_now < s.k1 ? by_now - s.k0 : 0;
     s.row0 = s.item * kItemRows;
     s.n_rows = min(kItemRows, (s.sq.n << sh.g_log2) - s.row0);
     s.last = sh.seen(s.sq, s.item) - 1;
@@ -314,10 +327,13 @@ struct Kernel {
     Seg s;
     while (it.next(s)) {
       const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
-      const auto pages = [&](int k) { return k < s.k1 ? Tiles::page_of(pt, k * kTile, s.last + 1, s_log2, a.n_phys, lane) : -1; };
-      int page = pages(s.k0);
-      for (int k = s.k0; k < s.k1; ++k) {
-        const int ahead = pages(k + 1);
+      const int n = s.k1 - s.k0;
+      const auto pages = [&](int i) {
+        return i < n ? Tiles::page_of(pt, s.at(i) * kTile, s.last + 1, s_log2, a.n_phys, lane) : -1;
+      };
+      int page = pages(0);
+      for (int i = 0; i < n; ++i) {
+        const int k = s.at(i), ahead = pages(i + 1);
         if (kr > 0) wait(&m.k_empty[ki], kr - 1);
         Tiles::copy(a.k_pool, a.Hkv, s.h, s_log2, k * kTile, s.sq.L, page, tid, sm + Lay::k_off + ki * Lay::kTileBytes);
         if constexpr (I8) {
@@ -428,10 +444,11 @@ struct Kernel {
       }
       Row row{-INFINITY, 0.f};
       const int step = two ? 1 : 2;
-      for (int k = s.k0 + (two ? 0 : t); k < s.k1; k += step) {
+      for (int i = two ? 0 : t; i < s.k1 - s.k0; i += step) {
+        const int k = s.at(i);
         uint32_t stage = 0;
         if constexpr (I8) {
-          const uint32_t c = vc + (k - s.k0);
+          const uint32_t c = vc + i;
           stage = c % VST;
           wait(&m.v_full[stage], c / VST);
         }
@@ -504,7 +521,7 @@ struct Kernel {
           const float factor = row.m == -INFINITY ? (raise ? 0.f : 1.f) : ex2(row.m - mn);
           row.m = mn;
           row.l *= factor;
-          if (k >= s.k0 + step) {  // O holds earlier steps (all done: S of this step was issued after them)
+          if (i >= step) {  // O holds earlier steps (all done: S of this step was issued after them)
             uint32_t o[16];
 #pragma unroll 1
             for (int c = 0; c < kDh; c += 16) {
