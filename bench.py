@@ -41,17 +41,20 @@ NOMINAL_HBM_GBS = 8000.0
 # that workload, and the sha256 of the kernel code it was taken on (see
 # csrc_sha256; profiles/k_fused_<workload>.md).  Reported only while the code
 # matches.
+# The device code of that kernel: other kernels of the library come and go
+# without touching it.
+STEP_SOURCES = ("spg_append.cuh", "spg_attn_core.cuh", "spg_common.cuh", "spg_fused.cu", "spg_select_core.cuh")
 NCU_TRAFFIC = {
     # workload: (DRAM bytes of one launch, code hash, kernel)
-    "llama2-7b-mha-32k": (67_890_432, "ebd83aa240f926a217a97b62897c56d90e8d4000d7273d0df5caa2a35bec27ee", "k_fused"),
-    "long-scan-b4-128k": (205_280_000, "ebd83aa240f926a217a97b62897c56d90e8d4000d7273d0df5caa2a35bec27ee", "k_fused"),
-    "sals-int8-b16-10k-4x": (100_827_136, "ebd83aa240f926a217a97b62897c56d90e8d4000d7273d0df5caa2a35bec27ee", "k_fused"),
+    "llama2-7b-mha-32k": (67_890_432, "33f648d414a0a877f99c31ad00ca840f222dc51519097eba945e93c23b2fefc3", "k_fused"),
+    "long-scan-b4-128k": (205_280_000, "33f648d414a0a877f99c31ad00ca840f222dc51519097eba945e93c23b2fefc3", "k_fused"),
+    "sals-int8-b16-10k-4x": (100_827_136, "33f648d414a0a877f99c31ad00ca840f222dc51519097eba945e93c23b2fefc3", "k_fused"),
 }
 
 
 def csrc_sha256(d: str | None = None) -> str:
-    """sha256 over the kernel sources in d (the package's csrc/ by default;
-    sorted by name; name, then the text with // and /* */ comments removed and
+    """sha256 over STEP_SOURCES in d (the package's csrc/ by default; sorted by
+    name; name, then the text with // and /* */ comments removed and
     whitespace runs collapsed): the code an ncu capture was taken on."""
     import hashlib
     import re
@@ -60,7 +63,7 @@ def csrc_sha256(d: str | None = None) -> str:
         d = os.path.join(os.path.dirname(os.path.abspath(__file__)), "query_aware_sparse_page_gb300", "csrc")
     h = hashlib.sha256()
     for f in sorted(os.listdir(d)):
-        if f.endswith((".cu", ".cuh", ".h")):
+        if f in STEP_SOURCES:
             with open(os.path.join(d, f), encoding="utf-8") as fh:
                 code = re.sub(r"/\*.*?\*/", "", fh.read(), flags=re.S)
             code = re.sub(r"//[^\n]*", "", code)

@@ -45,6 +45,17 @@ struct EvictArgs {
   int Hkv, S, MP, n_phys, keep, n_sink, n_recent, row_bytes, resident;
 };
 
+// atomics on another CTA's shared memory
+__device__ __forceinline__ void red_cluster_add(uint32_t addr, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_cluster_min(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void red_cluster_max(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ uint32_t mass_key(float m) { return m != m ? 0u : score_key(m); }
 
 // exclusive prefix of v over the block, and the total; s: one int per warp + 1
