@@ -15,6 +15,8 @@
  *      reading §3.3, the select -> attend two-kernel boundary),
  *   4. run split-K flash-decoding over the selected pages only and merge the
  *      splits by log-sum-exp (SALS SFAA 四阶段 flow; AICPU Tiling challenge 2).
+ * Around the steps, chunks of new tokens: into the cache, attended, and the
+ * cache evicted by accumulated attention weight (paged_*, further down).
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers, 16-byte aligned, contiguous
@@ -299,7 +301,10 @@ spg_status dense_decode_attention(const spg_params* p, const void* q, const void
 
 /* Workspace bytes that are enough for every entry point of this header with
  * these parameters and chunks of up to total_q rows (at least
- * spg_workspace_size).  Host only. */
+ * spg_workspace_size).  A workspace keeps its bookkeeping where the sizes in
+ * spg_params put it: total_q may vary from call to call, but for another
+ * batch, head count or page table take another workspace, or zero it in
+ * between.  Host only. */
 spg_status spg_chunk_workspace_size(const spg_params* p, int32_t total_q, size_t* bytes);
 
 typedef enum { SPG_ROPE_HALF = 0, SPG_ROPE_INTERLEAVED = 1 } spg_rope_layout;

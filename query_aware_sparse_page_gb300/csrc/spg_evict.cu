@@ -20,6 +20,10 @@
 // CTA that takes the tokens in order and reads a step (and the next) before
 // it writes the first never loses one.  The CTAs of one (batch, kv-head)
 // then split the row's channels (and K from V), which never meet.
+//
+// Measured (GB300): four caches of 128K tokens, GQA 32/8 bf16, to a quarter:
+// selection 48 us (16.8 MB of masses; its passes over shared memory and the
+// cluster barriers between them), gather 161 us (1.07 GB, 6.7 TB/s).
 #include <algorithm>
 
 #include "spg_chunk_common.cuh"

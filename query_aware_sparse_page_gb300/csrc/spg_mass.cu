@@ -16,6 +16,13 @@
 // item leaves its 256 sums in the workspace, and the part that arrives last
 // adds them in order.
 //
+// Measured (GB300): 2048 rows over 32K, GQA 32/8, 577 us, 0.92 PFLOP/s of
+// 1.90.  A summing warp takes 1770 cycles for its 128 columns and 600 to hand
+// the accumulator back, against 1024 of products for both tiles.  Four
+// summing warpgroups instead of two, half the columns each, took 913 us (the
+// 80 registers that leaves spill in the loading warps); keeping whole rows of
+// 128 columns in registers 724.
+//
 // Nothing is rounded to fewer than 32 bits.
 #include <algorithm>
 #include <cmath>

@@ -9,6 +9,10 @@
 // in registers.  exp2(scale s - lse) is summed over a token's rows by the
 // lanes that hold them and written with the old mass in one pass: a token
 // belongs to one page, so nothing is joined.
+//
+// Measured (GB300): one token of each of 16 sequences over int8 keys of 9K to
+// 10K, GQA 32/8: 49 us for 170 MB, 3.5 TB/s (the tile kernel 94 us; the int8
+// decode attention reads its cache at 4.4 TB/s).
 #include <algorithm>
 #include <cmath>
 
@@ -24,11 +28,10 @@ constexpr int kRingBytes = 64 * 1024;  // three CTAs per SM
 constexpr int kMaxSlots = 32;        // one per lane of the filling warp
 
 struct PageItems : ChunkShape {
-  static constexpr int kLeast = 4, kExtra = 0;
+  static constexpr int kLeast = 4;
   int s_log2;
   __device__ int items(const ChunkSeq& s) const { return (s.L + (1 << s_log2) - 1) >> s_log2; }
   __device__ long long steps(const ChunkSeq&, int m) const { return m; }
-  __device__ int item_steps(const ChunkSeq&, int) const { return 1; }
 };
 
 struct FewArgs {

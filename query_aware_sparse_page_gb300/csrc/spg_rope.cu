@@ -13,6 +13,9 @@
 // (each is used by every head) and resolves their cache slots, then each
 // thread takes 16 channels of a head at a time, the two 16-byte pieces that
 // hold both halves of its pairs.
+//
+// Measured (GB300): 8192 tokens of an MHA-32 prompt at d 128, fp16: 71 us for
+// 403 MB, 5.7 TB/s; one token of each of 16 sequences: 6 us.
 #include <cmath>
 
 #include "spg_chunk_common.cuh"
