@@ -25,11 +25,11 @@
 // a ragged batch to 16K).
 //
 // Measured (GB300): 2048 tokens at the end of 32K, MHA-32 fp16, 16-token
-// pages: 0.906 ms, 1.18 PFLOP/s of 1.90 measured.  Products alone take 0.53
+// pages: 0.91 to 0.95 ms, 1.13 to 1.18 PFLOP/s of 1.90 measured.  Products alone take 0.53
 // ms; the rest is the hand-over between the streams (a chain of softmax,
 // issue and products of 3400 cycles per step against 2048 of products) and
 // the copies into shared memory beside them.  Few rows over long caches: 8
-// sequences of 4K to 32K with up to 8 drafted tokens 142 us, 5.1 TB/s.
+// sequences of 4K to 32K with up to 8 drafted tokens 140 us, 5.1 TB/s.
 //
 // The steps of all items, in the order (sequence, kv-head, rows), are dealt
 // out to the CTAs in equal contiguous shares, whatever the lengths: an item

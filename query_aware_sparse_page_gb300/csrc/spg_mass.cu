@@ -16,8 +16,8 @@
 // item leaves its 256 sums in the workspace, and the part that arrives last
 // adds them in order.
 //
-// Measured (GB300): 2048 rows over 32K, GQA 32/8, 577 us, 0.92 PFLOP/s of
-// 1.90.  A summing warp takes 1770 cycles for its 128 columns and 600 to hand
+// Measured (GB300): 2048 rows over 32K, GQA 32/8, 577 to 609 us, 0.9 PFLOP/s
+// of 1.90.  A summing warp takes 1770 cycles for its 128 columns and 600 to hand
 // the accumulator back, against 1024 of products for both tiles.  Four
 // summing warpgroups instead of two, half the columns each, took 913 us (the
 // 80 registers that leaves spill in the loading warps); keeping whole rows of
@@ -484,7 +484,7 @@ cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_p
   // Up to 8 rows per (sequence, kv-head) on average (whatever their
   // distribution) the keys' bytes bound the work, and the page stream reads
   // them faster: a decode step of 16 sequences over int8 keys at 10K takes
-  // 49 us there and 94 us here.
+  // 45 to 49 us there and 94 us here.
   if (static_cast<long long>(r.total_q) * (p.num_q_heads / p.num_kv_heads) <= 8ll * p.batch) {
     const cudaError_t e = launch_mass_few(p, r, k_pool, k_scale, lse, mass_in, mass_out, decay, ws.err, stream);
     if (e != cudaErrorNotSupported) return e;
