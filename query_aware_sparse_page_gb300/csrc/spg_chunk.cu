@@ -25,7 +25,7 @@
 // a ragged batch to 16K).
 //
 // Measured (GB300): 2048 tokens at the end of 32K, MHA-32 fp16, 16-token
-// pages: 0.91 to 0.95 ms, 1.13 to 1.18 PFLOP/s of 1.90 measured.  Products alone take 0.53
+// pages: 0.91 to 0.96 ms, 1.11 to 1.18 PFLOP/s of 1.90 measured.  Products alone take 0.53
 // ms; the rest is the hand-over between the streams (a chain of softmax,
 // issue and products of 3400 cycles per step against 2048 of products) and
 // the copies into shared memory beside them.  Few rows over long caches: 8
@@ -108,7 +108,7 @@ struct SegIter : PartIter<RowItems> {
   __device__ SegIter(const RowItems& shape, const Plan& p) : PartIter(shape, p), lo(p.lo) {}
   __device__ bool next(Seg& s) {
     if (!PartIter::next(s)) return false;
-    const int by_now = static_cast<int>((s.item_first + s.k0 - lo) % s.nk);
+    const int by_now = static_cast<int>(s.item_first + s.k0 - lo) % s.nk;
     s.rot = by_now >= s.k0 && by_now < s.k1 ? by_now - s.k0 : 0;
     s.row0 = s.item * kItemRows;
     s.n_rows = min(kItemRows, (s.sq.n << sh.g_log2) - s.row0);

@@ -11,7 +11,7 @@
 // belongs to one page, so nothing is joined.
 //
 // Measured (GB300): one token of each of 16 sequences over int8 keys of 9K to
-// 10K, GQA 32/8: 45 to 49 us for 170 MB, 3.7 TB/s (the tile kernel 94 us; the int8
+// 10K, GQA 32/8: 44 to 49 us for 170 MB, 3.8 TB/s (the tile kernel 94 us; the int8
 // decode attention reads its cache at 4.4 TB/s).
 #include <algorithm>
 #include <cmath>
