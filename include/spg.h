@@ -362,9 +362,10 @@ spg_status paged_rope_append(const spg_params* p, const spg_rope* rope, int32_t 
  * in: row i of sequence b attends the tokens t <= seq_lens[b] - n_b + i.
  *   out          [total_q][Hq][d] q_dtype
  *   lse          [total_q][Hq] fp32 natural-log log-sum-exp (may be NULL)
- * Logits, softmax statistics and sums in fp32; the probabilities enter the
- * P V product rounded to the 16-bit type (int8 V scales, at most 255, folded
- * in first).  Needs spg_chunk_workspace_size bytes. */
+ * Logits, softmax statistics and sums in fp32; the probabilities (int8 pools:
+ * times their V scales, of any size) enter the P V product rounded to the
+ * 16-bit type, relative to the row's largest.  Needs
+ * spg_chunk_workspace_size bytes. */
 spg_status paged_chunk_attention(const spg_params* p, int32_t total_q, const void* q,
                                  const int32_t* q_start, const void* k_pool, const void* v_pool,
                                  const void* k_scale, const void* v_scale,

@@ -11,9 +11,10 @@
 //   O += P V       A from TMEM, V from shared memory (its rows are the
 //                  contraction: MN-major), O in TMEM
 // with the running maximum m and sum l of the softmax per row.  m is only
-// raised when a (base 2) logit exceeds it by more than kSlack: p stays at
-// most 2^kSlack, O is rescaled in the rare step that raises it, and out = O / l
-// does not depend on m.
+// raised when a (base 2) logit exceeds it by more than kTop, and then set
+// kHead below that logit: p stays at most 2^kTop, O is rescaled in the rare
+// step that raises it, and out = O / l does not depend on m.  kHead keeps the
+// weights of a long tail out of fp16's subnormal range.
 //
 // One CTA per SM, two streams.  With more than 128 rows each has a Q tile of
 // 128 rows over the same keys; with fewer they share the rows and take
@@ -43,10 +44,16 @@
 // products take), and tokens that are not there become zeros on the way.
 // int8 codes land in the upper half of their tile's own space and are widened
 // in place to exact 16-bit values; the key scales then multiply the logits
-// and the value scales (times 16, undone at the end) the probabilities.
+// and the value scales the probabilities.  What enters the product is p times
+// the value scale, so with int8 m follows the largest logit plus log2 of its
+// value scale: the largest weight of a row has the same size whatever the
+// scales are, and the sum of p (larger or smaller by what the scales are)
+// needs no more than fp32's range.
 //
-// Roundings: P to the 16-bit type (as the products take it) and the result;
-// everything else is fp32.
+// Roundings: P (int8: times the value scale) to the 16-bit type, as the
+// products take it, and the result; everything else is fp32.  P as the sum of
+// two 16-bit values, in a first form with some spills, took 2.01 against 0.96
+// ms for the piece at 32K and 228 against 140 us for the drafts.
 #include <algorithm>
 #include <cmath>
 
@@ -59,6 +66,7 @@ namespace {
 
 constexpr int kItemRows = 2 * kTile;  // rows of a Q tile, and tokens of a step: kTile
 constexpr uint32_t kTmemCols = 512;  // S0 S1 O0 O1, 128 columns each
+constexpr float kLeastVScale = 5.9604644775390625e-8f;  // fp16's smallest but 0, which counts as that one
 
 // ---- the plan -----------------------------------------------------------------------
 // An item is 256 rows, a step 128 of the tokens its rows see.
@@ -150,7 +158,8 @@ struct Misc {
   float top[2][2][2][kTile];  // largest logit of a step, per stream and half of the tokens
   float sum[2][2][kTile], max[2][kTile];  // a segment's sums per stream and half, and its m
   alignas(16) float ones[I8 ? kTile : 1];
-  alignas(16) float scales[I8 ? VST : 1][2][I8 ? kTile : 1];  // int8: scale * key scale, 16 * value scale of a step's tokens
+  // int8, of a step's tokens: scale * key scale, value scale, log2 of its size
+  alignas(16) float scales[I8 ? VST : 1][3][I8 ? kTile : 1];
 };
 
 template <typename T, typename TQ, int D>
@@ -167,9 +176,8 @@ struct Kernel {
   static constexpr int kRegsSoftmax = 96, kRegsLoad = 56, kRegsIssue = 40;
   static_assert(4 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 6 * 80, "the block's registers");
   static constexpr int kLoadThreads = 128;
-  // fp16 holds p * 16 * (value scale) for scales up to 255
-  static constexpr float kSlack = I8 ? 4.f : 8.f;
-  static constexpr float kVScale = I8 ? 16.f : 1.f;
+  // the weights of a row are at most 2^15, under fp16's 65504
+  static constexpr float kHead = 7.f, kTop = 15.f;
 
   // ---- the issuing warps, one per stream: all of a warp waits, one elected lane issues -----
   // One warp's waits and issues for both streams took longer than their
@@ -357,21 +365,23 @@ struct Kernel {
           copy_arrive(&m.k_full[ki]);
         }
         if (++ki == KST) ki = 0, ++kr;
-        float sk = 0.f, sv = 0.f;  // int8: scales of the step's token tid
+        __half sk = __ushort_as_half(0), sv = sk;  // int8: scales of the step's token tid
         if constexpr (I8) {
           const int pg = __shfl_sync(0xffffffffu, page, tid >> s_log2);
           if (pg >= 0 && k * kTile + tid < s.sq.L) {
             const size_t at = ((static_cast<size_t>(pg) * a.Hkv + s.h) << s_log2) + (tid & (a.S - 1));
-            sk = __half2float(a.k_scale[at]) * a.scale_log2;
-            sv = __half2float(a.v_scale[at]) * kVScale;
+            sk = a.k_scale[at];
+            sv = a.v_scale[at];
           }
         }
         if (vr > 0) wait(&m.v_empty[vi], vr - 1);
         Tiles::copy(a.v_pool, a.Hkv, s.h, s_log2, k * kTile, s.sq.L, page, tid, sm + Lay::v_off + vi * Lay::kTileBytes);
         if constexpr (I8) {
           copy_commit();
-          m.scales[vi][0][tid] = sk;
-          m.scales[vi][1][tid] = sv;
+          const float v = __half2float(sv);
+          m.scales[vi][0][tid] = __half2float(sk) * a.scale_log2;
+          m.scales[vi][1][tid] = v;
+          m.scales[vi][2][tid] = __log2f(fmaxf(fabsf(v), kLeastVScale));
           if (open == 2) {
             copy_wait<2>();
             finish(true);
@@ -466,9 +476,14 @@ struct Kernel {
         tc_fence_after();
         // 32 logits in registers at a time: the maximum of the upper ones,
         // then of the lower, which stay; the upper are read again when their
-        // turn comes.  int8: logits times their key scales.
+        // turn comes.  int8: logits times their key scales, and for the
+        // maximum plus log2 of their value scales.
         const float* ks = m.ones;
-        if constexpr (I8) ks = m.scales[stage][0] + h * kHalf;
+        const float* lv = m.ones;
+        if constexpr (I8) {
+          ks = m.scales[stage][0] + h * kHalf;
+          lv = m.scales[stage][2] + h * kHalf;
+        }
         const int t0 = k * kTile + h * kHalf;
         const bool masked = k * kTile + kTile - 1 > pos_first || any_bad;
         uint32_t x[32];
@@ -503,11 +518,18 @@ struct Kernel {
             for (int c = 0; c < 32; c += 8) {
               const float4 u = *reinterpret_cast<const float4*>(ks + 32 * q + c);
               const float4 w = *reinterpret_cast<const float4*>(ks + 32 * q + c + 4);
-              mx[0] = fmaxf(fmaxf(mx[0], f(c) * u.x), f(c + 4) * w.x);
-              mx[1] = fmaxf(fmaxf(mx[1], f(c + 1) * u.y), f(c + 5) * w.y);
-              mx[2] = fmaxf(fmaxf(mx[2], f(c + 2) * u.z), f(c + 6) * w.z);
-              mx[3] = fmaxf(fmaxf(mx[3], f(c + 3) * u.w), f(c + 7) * w.w);
+              const float4 ul = *reinterpret_cast<const float4*>(lv + 32 * q + c);
+              const float4 wl = *reinterpret_cast<const float4*>(lv + 32 * q + c + 4);
+              mx[0] = fmaxf(fmaxf(mx[0], fmaf(f(c), u.x, ul.x)), fmaf(f(c + 4), w.x, wl.x));
+              mx[1] = fmaxf(fmaxf(mx[1], fmaf(f(c + 1), u.y, ul.y)), fmaf(f(c + 5), w.y, wl.y));
+              mx[2] = fmaxf(fmaxf(mx[2], fmaf(f(c + 2), u.z, ul.z)), fmaf(f(c + 6), w.z, wl.z));
+              mx[3] = fmaxf(fmaxf(mx[3], fmaf(f(c + 3), u.w, ul.w)), fmaf(f(c + 7), w.w, wl.w));
             }
+          } else if (I8) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], f(c + i) + lv[32 * q + c + i]);
           } else {
 #pragma unroll
             for (int c = 0; c < 32; c += 8)
@@ -524,9 +546,9 @@ struct Kernel {
         bar_sync(pair, 64);
         top = fmaxf(top, m.top[sc & 1][t][h ^ 1][tile_row]);
         if constexpr (!I8) top *= a.scale_log2;
-        const bool raise = top > row.m + kSlack;  // -inf + kSlack = -inf: the first finite logit
+        const bool raise = top > row.m + kTop;  // -inf + kTop = -inf: the first finite logit
         if (__any_sync(0xffffffffu, raise)) {     // the same in both warps
-          const float mn = raise ? top : row.m;
+          const float mn = raise ? top - kHead : row.m;
           const float factor = row.m == -INFINITY ? (raise ? 0.f : 1.f) : ex2(row.m - mn);
           row.m = mn;
           row.l *= factor;
@@ -609,7 +631,7 @@ struct Kernel {
       if (two || t == 0) {
         const bool live = r < s.n_rows;
         const bool both = !two && s.k1 - s.k0 > 1;  // stream 1 has had a step
-        const float inv = row.l > 0.f ? (1.f / kVScale) / row.l : 0.f;
+        const float inv = row.l > 0.f ? 1.f / row.l : 0.f;
         if (whole) {
           f0 *= inv;
           f1 *= inv;
@@ -683,7 +705,7 @@ struct Kernel {
 #pragma unroll 2
       for (int c = c0; c <= c1; ++c)
         l = fmaf(__ldcg(at(c) + (D + 1) * a.part_rows), ex2(__ldcg(at(c) + D * a.part_rows) - mm), l);
-      const float inv = l > 0.f ? (1.f / kVScale) / l : 0.f;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t orow = out_row(a, s, r);
       TQ* dst = static_cast<TQ*>(a.out) + orow * D;
       for (int d = d0; d < d1; d += 16) {

@@ -1,0 +1,145 @@
+"""The paged-chunk operators where they are easily wrong.  References in 64 bits, as in tests/paged_ref.py."""
+import math
+
+import pytest
+import torch
+
+import paged_ref as R
+from test_gpu_paged import Run, close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def spg():
+    import query_aware_sparse_page_gb300 as m
+
+    return m
+
+
+# ---- chunk attention: weights over a wide range ------------------------------------------------
+
+
+def sink_chunk(kv, q, gap, scales, new=3, L=32768, S=64, hq=2, hkv=1, d=128, seed=0):
+    """Token 0 of each sequence `gap` nats above the others, whose logits lie within 0.1 of one another and whose values
+    have one sign, so that weight lost from them shows."""
+    c = R.Chunk(hq, hkv, d, S, kv, q, [L], [new], seed=seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    a = 8.0
+    c.q = (0.05 * torch.randn(c.q.shape, generator=g)).to(c.q.dtype)
+    c.q[..., 0] = a
+    first = int(c.page_table[0, 0])
+    key = gap * math.sqrt(d) / a
+    live = torch.zeros((c.n_phys, S), dtype=torch.bool)
+    for t0 in range(0, L, S):
+        live[int(c.page_table[0, t0 // S]), : min(S, L - t0)] = True
+    live = live[:, None].expand(c.n_phys, hkv, S)
+    if kv == "i8":
+        c.k_pool[..., 0][live] = 0
+        c.k_pool[first, :, 0] = 0
+        c.k_pool[first, :, 0, 0] = 127
+        c.k_scale[live] = 0.005
+        c.k_scale[first, :, 0] = key / 127
+        c.v_pool[live] = c.v_pool[live].abs().clamp(min=1)
+        c.v_scale[live] = scales(live.sum(), g).half()
+    else:
+        c.k_pool[..., 0][live] = 0
+        c.k_pool[first, :, 0] = 0
+        c.k_pool[first, :, 0, 0] = key
+        c.v_pool[live] = c.v_pool[live].abs()
+    return c, first
+
+
+def wide_tolerance(c):
+    """out and its tolerance, relative to what the row holds (terms as in paged_ref.attention): the weights that enter
+    the products are rounded to 16 bits, half a step each; in fp16 they are scaled so that the largest of a row is at
+    least 2^7 in units whose subnormal half step is 2^-25, that is 2^-32 of the largest weight times value scale."""
+    out, tol = torch.zeros((c.T, c.hq, c.d), dtype=R.F64), torch.zeros((c.T, c.hq, c.d), dtype=R.F64)
+    e = torch.finfo(R.DT[c.qdt]).eps / 2
+    for h in range(c.hkv):
+        v = c.tokens(c.v_pool, c.v_scale, 0, h)
+        code = v if c.kv != "i8" else c.tokens(c.v_pool, None, 0, h)
+        page = c.page_table[0, : -(-c.lens[0] // c.S)].long()
+        vs = torch.ones(c.lens[0], dtype=R.F64) if c.kv != "i8" else c.v_scale[page, h].to(R.F64).reshape(-1)[: c.lens[0]]
+        for j in range(c.group):
+            z, size = c.logits(0, h, j)
+            i = h * c.group + j
+            p = torch.softmax(z, dim=1)
+            o, A = p @ v, p @ v.abs()
+            zmax = z.masked_fill(~torch.isfinite(z), 0.0).abs().amax(dim=1)
+            dz = c.d * 2.0 ** -24 * size.amax(dim=1) + 8 * 2.0 ** -24 * (zmax + 1)
+            t = e * (A + o.abs()) + 2 * dz[:, None] * A
+            if c.qdt == "f16":
+                t = t + 2.0 ** -32 * (p * vs).amax(dim=1)[:, None] * code.abs().sum(dim=0)[None] + 2.0 ** -25
+            out[:, i], tol[:, i] = o, 1.01 * t
+    return out, tol
+
+
+SCALES = {
+    "1e-7": lambda n, g: torch.full((n,), 1e-7),
+    "1e-5": lambda n, g: 1e-5 * (0.5 + torch.rand(n, generator=g)),
+    "1e-4": lambda n, g: 1e-4 * (0.5 + torch.rand(n, generator=g)),
+    "1e-2": lambda n, g: 1e-2 * (0.5 + torch.rand(n, generator=g)),
+    "400": lambda n, g: 400.0 * (0.5 + torch.rand(n, generator=g)),
+    "all": lambda n, g: torch.exp2(-20 + 24 * torch.rand(n, generator=g)),
+}
+
+
+@pytest.mark.parametrize("q", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", [0.0, 8.0, 12.0])
+@pytest.mark.parametrize("scales", list(SCALES))
+def test_chunk_int8_value_scales(spg, scales, gap, q):
+    c, _ = sink_chunk("i8", q, gap, SCALES[scales])
+    r = Run(spg, c)
+    r.chunk()
+    assert r.err() == 0
+    out, tol = wide_tolerance(c)
+    close(r.out, out, tol, "out")
+
+
+@pytest.mark.parametrize("new, hq", [(3, 2), (200, 2), (1, 8)])
+def test_chunk_int8_scales_that_differ(spg, new, hq):
+    """A first token with the smallest scale there is, or none, before values of an ordinary size; and the other way
+    round.  In a short prompt too, whose rows see few tokens."""
+    for first_scale, rest in ((2.0 ** -24, 0.02), (0.0, 0.02), (0.02, 2.0 ** -20), (60000.0, 1e-4)):
+        for L in (5000, max(new, 40)):
+            c, first = sink_chunk("i8", "f16", 12.0, lambda n, g: torch.full((n,), rest), new=new, L=L, hq=hq, d=64)
+            c.v_pool.clamp_(max=16)  # 60000 * 16 is past fp16, and what the first token leaves of it is not
+            c.v_scale[first, :, 0] = first_scale
+            if first_scale > 1:
+                c.v_pool[first, :, 0] = 1
+            r = Run(spg, c)
+            r.chunk()
+            assert r.err() == 0
+            out, tol = wide_tolerance(c)
+            close(r.out, out, tol, "out")
+
+
+@pytest.mark.parametrize("scale", [100.0, 300.0, 500.0])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_chunk_int8_large_scales_rising_logits(spg, scale, odd):
+    """Logits that rise by less than the running maximum's slack, over values close to fp16's range."""
+    c, _ = sink_chunk("i8", "f16", 0.0, lambda n, g: torch.full((n,), scale), new=50, L=6000, hq=4)
+    pages = c.page_table[0].long()
+    for t in range(6000):
+        if t // 128 % 2 == odd:  # 2.4 nats above its neighbours
+            pg = pages[t // 64]
+            c.k_pool[pg, :, t % 64, 0] = 127
+            c.k_scale[pg, :, t % 64] = 2.4 * math.sqrt(128) / 8.0 / 127
+            c.k_pool[pg, :, t % 64, 1:] = (c.k_pool[pg, :, t % 64, 1:].float() * 0.18).to(torch.int8)
+    r = Run(spg, c)
+    r.chunk()
+    assert r.err() == 0
+    out, tol = wide_tolerance(c)
+    close(r.out, out, tol, "out")
+
+
+@pytest.mark.parametrize("gap", [8.0, 12.0, 14.0])
+@pytest.mark.parametrize("kv", ["f16", "bf16"])
+def test_chunk_one_token_above_a_long_cache(spg, kv, gap):
+    c, _ = sink_chunk(kv, kv, gap, None, L=40000, S=16)
+    r = Run(spg, c)
+    r.chunk()
+    assert r.err() == 0
+    out, tol = wide_tolerance(c)
+    close(r.out, out, tol, "out")
