@@ -362,6 +362,8 @@ spg_status paged_rope_append(const spg_params* p, const spg_rope* rope, int32_t 
  * in: row i of sequence b attends the tokens t <= seq_lens[b] - n_b + i.
  *   out          [total_q][Hq][d] q_dtype
  *   lse          [total_q][Hq] fp32 natural-log log-sum-exp (may be NULL)
+ * A row that sees no token (its pages are bad) gets out = 0 and lse = -inf, a
+ * row with a NaN among its logits NaN in both.
  * Logits, softmax statistics and sums in fp32; the probabilities (int8 pools:
  * times their V scales, of any size) enter the P V product rounded to the
  * 16-bit type, relative to the row's largest.  Needs

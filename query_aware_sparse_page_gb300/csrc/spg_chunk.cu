@@ -414,6 +414,12 @@ struct Kernel {
     float m, l;
   };
 
+  // Rows that saw nothing have l = 0, out 0 and lse -inf.  A NaN among the
+  // logits passes the maximum by and stays in l: out and lse are NaN, from a
+  // whole item as from its parts.
+  static __device__ __forceinline__ float reciprocal(float l) { return l == 0.f ? 0.f : 1.f / l; }
+  static __device__ __forceinline__ float log_sum(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2; }
+
   // channel 0 of a row in a slot; the next channel is part_rows further
   static __device__ __forceinline__ float* part_at(const ChunkArgs& a, int slot, int row) {
     return a.part + static_cast<size_t>(slot) * (D + 2) * a.part_rows + row;
@@ -631,7 +637,7 @@ struct Kernel {
       if (two || t == 0) {
         const bool live = r < s.n_rows;
         const bool both = !two && s.k1 - s.k0 > 1;  // stream 1 has had a step
-        const float inv = row.l > 0.f ? 1.f / row.l : 0.f;
+        const float inv = reciprocal(row.l);
         if (whole) {
           f0 *= inv;
           f1 *= inv;
@@ -669,7 +675,7 @@ struct Kernel {
         }
         if (live && h == 0) {
           if (whole) {
-            if (a.lse) a.lse[orow] = row.l > 0.f ? (row.m + log2f(row.l)) * kLn2 : -INFINITY;
+            if (a.lse) a.lse[orow] = log_sum(row.m, row.l);
           } else {
             __stcg(part + D * a.part_rows, row.m);
             __stcg(part + (D + 1) * a.part_rows, row.l);
@@ -705,7 +711,7 @@ struct Kernel {
 #pragma unroll 2
       for (int c = c0; c <= c1; ++c)
         l = fmaf(__ldcg(at(c) + (D + 1) * a.part_rows), ex2(__ldcg(at(c) + D * a.part_rows) - mm), l);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = reciprocal(l);
       const size_t orow = out_row(a, s, r);
       TQ* dst = static_cast<TQ*>(a.out) + orow * D;
       for (int d = d0; d < d1; d += 16) {
@@ -726,7 +732,7 @@ struct Kernel {
               make_uint4(pack2<TQ>(o[i] * inv, o[i + 1] * inv), pack2<TQ>(o[i + 2] * inv, o[i + 3] * inv),
                          pack2<TQ>(o[i + 4] * inv, o[i + 5] * inv), pack2<TQ>(o[i + 6] * inv, o[i + 7] * inv));
       }
-      if (d0 == 0 && a.lse) a.lse[orow] = l > 0.f ? (mm + log2f(l)) * kLn2 : -INFINITY;
+      if (d0 == 0 && a.lse) a.lse[orow] = log_sum(mm, l);
     }
     if (tid == 0) a.counters[c0] = 0;  // ready for the next call
   }

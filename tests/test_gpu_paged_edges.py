@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_ref as R
-from test_gpu_paged import Run, close
+from test_gpu_paged import Run, check_chunk, close
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,28 @@ def test_chunk_one_token_above_a_long_cache(spg, kv, gap):
     assert r.err() == 0
     out, tol = wide_tolerance(c)
     close(r.out, out, tol, "out")
+
+
+# ---- rows that hold a NaN ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kv", ["f16", "bf16", "i8"])
+def test_chunk_nan_rows(spg, kv):
+    """A NaN in a row's query makes that row NaN, whether one CTA has its whole work or many share it, and no other."""
+    c = R.Chunk(4, 2, 64, 16, kv, "bf16" if kv == "bf16" else "f16", [40, 5000, 700], [40, 3, 300])
+    r = Run(spg, c)
+    rows = [(5, 1), (41, 2), (43, 0), (342, 3)]
+    clean = r.q.clone()
+    for t, h in rows:
+        r.q[t, h, 7] = math.nan
+    r.chunk()
+    assert r.err() == 0
+    for t, h in rows:
+        assert bool(torch.isnan(r.out[t, h]).all()) and bool(torch.isnan(r.lse[t, h])), (t, h)
+    out, lse = r.out.clone(), r.lse.clone()
+    r.q = clean
+    r.chunk()
+    for t, h in rows:
+        out[t, h], lse[t, h] = r.out[t, h], r.lse[t, h]
+    assert torch.equal(out, r.out) and torch.equal(lse, r.lse)
+    check_chunk(r)
