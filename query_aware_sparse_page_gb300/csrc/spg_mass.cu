@@ -106,6 +106,7 @@ struct Misc {
   Plan plan;
   uint32_t tmem;
   int last;
+  int gaps[QST];  // the tile has rows that count nothing
   alignas(16) float neg_lse[QST][kTile];  // -lse in the log2 domain; -inf for rows that count nothing
 };
 
@@ -205,8 +206,13 @@ struct Kernel {
       if (!__all_sync(0xffffffffu, qr == 0 || Waiter{a.err}(&m.q_empty[qi], qr - 1))) return;
 #pragma unroll
       for (int i = 0; i < kTile / 32; ++i) m.neg_lse[qi][lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
+      bool gap = false;
+#pragma unroll
+      for (int i = 0; i < kTile / 32; ++i) gap |= v[i] == -INFINITY;
+      gap = __any_sync(0xffffffffu, gap);
       __syncwarp();
       if (lane == 0) {
+        m.gaps[qi] = gap;
         mbar_arrive_expect_tx(&m.q_full[qi], Lay::kTileBytes);
         for (int hf = 0; hf < D / 64; ++hf)
           tma_tile_4d(smem + Lay::q_off + qi * Lay::kTileBytes + hf * kTile * 128, &a.tmq, hf * 64, 0, s.h,
@@ -333,7 +339,8 @@ struct Kernel {
         const int cols = min(kTile, (s.sq.n << a.sh.g_log2) - tile * kTile);
         // rows from which on the token is seen (its own is the first)
         const int from = ((tok - s.sq.pos0) << a.sh.g_log2) - tile * kTile;
-        const bool masked = cols < kTile || (s.item + 1) * kItemTokens - 1 > s.sq.pos0 + (tile * kTile >> a.sh.g_log2);
+        // (rows behind the sequence's last are gaps too)
+        const bool masked = m.gaps[qi] || (s.item + 1) * kItemTokens - 1 > s.sq.pos0 + (tile * kTile >> a.sh.g_log2);
         // half a row in registers at a time; the accumulator goes back with the second
         uint32_t x[kTile / 2];
         if (masked) {
@@ -345,8 +352,10 @@ struct Kernel {
               if (c + g < cols) {  // the same for the whole block
 #pragma unroll
                 for (int i = g; i < g + 8; i += 2) {
-                  const float p = c + i < from || c + i >= cols ? 0.f : ex2(fmaf(__uint_as_float(x[i]), k, nl[c + i]));
-                  const float q = c + i + 1 < from || c + i + 1 >= cols ? 0.f : ex2(fmaf(__uint_as_float(x[i + 1]), k, nl[c + i + 1]));
+                  // rows without a log-sum-exp are left out, whatever their products are
+                  const float n0 = nl[c + i], n1 = nl[c + i + 1];
+                  const float p = c + i < from || n0 == -INFINITY ? 0.f : ex2(fmaf(__uint_as_float(x[i]), k, n0));
+                  const float q = c + i + 1 < from || n1 == -INFINITY ? 0.f : ex2(fmaf(__uint_as_float(x[i + 1]), k, n1));
                   sum0 = add_f32x2(sum0, f32x2(p, q));
                 }
               }

@@ -250,12 +250,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kCtas) k_mass_few(const __g
             k[0] *= __half2float(s_scale[slot * S + t0 + g]);
             k[1] *= __half2float(s_scale[slot * S + t0 + g + 8]);
           }
-          // the first row that sees the token, of those at or past pos0
+          // the first row that sees the token, of those at or past pos0; rows
+          // without a log-sum-exp are left out, whatever their products are
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int from = ((tok0 + t0 + g + 8 * e - c.sq.pos0) << a.g_log2) - grp * 8 - 2 * t;
-            if (from <= 0) sum[e] += exp2f(fmaf(s[2 * e], k[e], -l0));
-            if (from <= 1) sum[e] += exp2f(fmaf(s[2 * e + 1], k[e], -l1));
+            if (from <= 0 && l0 != INFINITY) sum[e] += exp2f(fmaf(s[2 * e], k[e], -l0));
+            if (from <= 1 && l1 != INFINITY) sum[e] += exp2f(fmaf(s[2 * e + 1], k[e], -l1));
           }
         }
 #pragma unroll

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_ref as R
-from test_gpu_paged import Run, check_chunk, close
+from test_gpu_paged import Run, check_chunk, close, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +168,25 @@ def test_chunk_nan_rows(spg, kv):
         out[t, h], lse[t, h] = r.out[t, h], r.lse[t, h]
     assert torch.equal(out, r.out) and torch.equal(lse, r.lse)
     check_chunk(r)
+
+
+@pytest.mark.parametrize("hq, hkv, d, kv, q, lens, new", [
+    (4, 2, 64, "f16", "f16", [300, 40], [5, 40]), (8, 2, 128, "bf16", "bf16", [2000], [300]),
+    (4, 2, 128, "i8", "f16", [300, 40], [9, 1]),
+    (4, 2, 64, "f16", "f16", [300, 40], [2, 1]), (4, 2, 128, "i8", "f16", [300, 40], [1, 2]),
+])
+def test_mass_rows_without_lse_add_nothing(spg, hq, hkv, d, kv, q, lens, new):
+    """Rows taken out by lse = -inf add nothing whatever their queries hold."""
+    c = R.Chunk(hq, hkv, d, 16, kv, q, lens, new)
+    lse = R.attention(c)[2].float()
+    gone = [0, c.T - 1]
+    lse[gone] = -math.inf
+    want, tol = R.mass_of(c, lse, None, 1.0)
+    r = Run(spg, c)
+    r.q[gone[0]] = math.nan
+    r.q[gone[1], :, ::2] = math.inf
+    m = torch.full((len(lens), hkv, c.mp * 16), 3.0, device="cuda")
+    r.mass(dev(lse), None, m, 1.0)
+    assert r.err() == 0
+    for b, L in enumerate(lens):
+        close(m[b, :, :L], want[b, :, :L], tol[b, :, :L], "mass")
