@@ -302,8 +302,9 @@ spg_status dense_decode_attention(const spg_params* p, const void* q, const void
 /* Workspace bytes that are enough for every entry point of this header with
  * these parameters and chunks of up to total_q rows (at least
  * spg_workspace_size).  A workspace keeps its bookkeeping where the sizes in
- * spg_params put it: total_q may vary from call to call, but for another
- * batch, head count or page table take another workspace, or zero it in
+ * spg_params put it: total_q and the selector's fields may vary from call to
+ * call (on a workspace that is enough for each), but for another batch, head
+ * count, head_dim or page table take another workspace, or zero it in
  * between.  Host only. */
 spg_status spg_chunk_workspace_size(const spg_params* p, int32_t total_q, size_t* bytes);
 

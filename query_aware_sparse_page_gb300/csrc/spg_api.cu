@@ -30,6 +30,10 @@ static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255);
 // Workspace layout (every region 256-byte aligned):
 //   header    256 B: error word at 0, the scheduled step's queue counters at
 //             64, the bounded-wait test hook at 128
+//   arrivals  of the parts of an item (chunk attention, attention mass).  Here
+//             and not beside the parts, whose place depends on the selector's
+//             fields: a workspace may serve decode steps and chunks with
+//             parameters that differ in those
 //   counters  [B*Hkv] int32: split arrivals of the attention kernel
 //   sel_cnt.  [B*Hkv] int32: scoring CTAs done, for the fused selection
 //   scores    [B*Hkv][MP] fp32 (the scheduled step keeps its keys here)
@@ -37,12 +41,12 @@ static size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255);
 //   flags     [4][B*Hkv] int32 (scheduled step)
 //   slices    [B*Hkv][n_sel] int2 (scheduled step)
 //   iq        [B*Hkv][8] int32 (scheduled step, sketch selector)
-//   mass      arrival counters, then partial sums (attention mass)
+//   mass      partial sums (attention mass)
 size_t workspace_bytes(const spg_params& p) {
   const size_t B = p.batch, Hq = p.num_q_heads, Hkv = p.num_kv_heads;
   const size_t d = p.head_dim, MP = p.max_pages_per_seq;
   const size_t n_sel = p.selector == SPG_SEL_ALL ? 1 : std::max(1, n_sel_pages(p));
-  size_t off = 256;                                      // header: error word, queue counters
+  size_t off = 256 + kPartCounterBytes;                  // header: error word, queue counters; arrivals
   off += align256(sizeof(int32_t) * B * Hkv);            // split arrival counters
   off += align256(sizeof(int32_t) * B * Hkv);            // scoring arrival counters
   off += align256(sizeof(float) * B * Hkv * MP);         // scores / keys
@@ -65,7 +69,8 @@ Workspace carve_workspace(const spg_params& p, void* ws) {
   w.err = reinterpret_cast<int32_t*>(base);
   w.sched_ctr = reinterpret_cast<int32_t*>(base + 64);
   w.hook = reinterpret_cast<int32_t*>(base + 128);
-  size_t off = 256;
+  w.part_counters = reinterpret_cast<int32_t*>(base + 256);
+  size_t off = 256 + kPartCounterBytes;
   w.counters = reinterpret_cast<int32_t*>(base + off);
   off += align256(sizeof(int32_t) * B * Hkv);
   w.sel_counters = reinterpret_cast<int32_t*>(base + off);
@@ -84,8 +89,7 @@ Workspace carve_workspace(const spg_params& p, void* ws) {
   off += align256(sizeof(int2) * B * Hkv * n_sel);
   w.iq = reinterpret_cast<int32_t*>(base + off);
   off += align256(sizeof(int32_t) * 8 * B * Hkv);
-  w.mass_counters = reinterpret_cast<int32_t*>(base + off);
-  w.mass_part = reinterpret_cast<float*>(base + off + kMassCounterBytes);
+  w.mass_part = reinterpret_cast<float*>(base + off);
   return w;
 }
 

@@ -831,7 +831,7 @@ cudaError_t chunk_typed(const spg_params& p, ChunkArgs& a, const void* q, cudaSt
 }  // namespace
 
 size_t chunk_workspace_bytes(const spg_params& p, int total_q) {
-  return round256(workspace_bytes(p)) + round256(sizeof(int32_t) * kMaxCtas) +
+  return round256(workspace_bytes(p)) +
          round256(sizeof(float) * 2 * kMaxCtas * part_rows(p, total_q) * (p.head_dim + 2));
 }
 
@@ -853,11 +853,10 @@ cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_
   a.page_table = r.page_table;
   a.out = out;
   a.lse = lse;
-  uint8_t* base = static_cast<uint8_t*>(ws);
-  a.err = reinterpret_cast<int32_t*>(base);
-  base += round256(workspace_bytes(p));
-  a.counters = reinterpret_cast<int32_t*>(base);
-  a.part = reinterpret_cast<float*>(base + round256(sizeof(int32_t) * kMaxCtas));
+  const Workspace w = carve_workspace(p, ws);
+  a.err = w.err;
+  a.counters = w.part_counters;
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(workspace_bytes(p)));
   a.Hkv = p.num_kv_heads;
   a.S = p.page_size;
   a.s_log2 = log2_of(p.page_size);

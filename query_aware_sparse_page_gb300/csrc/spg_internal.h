@@ -25,10 +25,10 @@ struct Workspace {
   int32_t* sched_flags;  // [4][B*Hkv] per-unit flags; zero between calls
   int2* slices;          // [B*Hkv][n_sel] (physical page, valid tokens) of the selection
   int32_t* iq;           // [B*Hkv][8] sketch index queries
-  int32_t* mass_counters;  // arrivals of an item's parts (spg_mass.cu); zero between calls
-  float* mass_part;        // their sums
+  int32_t* part_counters;  // arrivals of an item's parts (spg_chunk.cu, spg_mass.cu); zero between calls
+  float* mass_part;        // attention mass: the parts' sums
 };
-constexpr size_t kMassCounterBytes = 2048;  // ahead of the sums
+constexpr size_t kPartCounterBytes = 768;  // a counter per CTA
 size_t mass_workspace_bytes();
 
 size_t workspace_bytes(const spg_params& p);

@@ -484,8 +484,8 @@ cudaError_t mass_typed(const spg_params& p, MassArgs& a, const void* q, cudaStre
 
 }  // namespace
 
-static_assert(kMassCounterBytes >= sizeof(int32_t) * kMaxCtas, "a counter per CTA");
-size_t mass_workspace_bytes() { return kMassCounterBytes + sizeof(float) * 2 * kMaxCtas * kItemTokens; }
+static_assert(kPartCounterBytes >= sizeof(int32_t) * kMaxCtas, "a counter per CTA");
+size_t mass_workspace_bytes() { return sizeof(float) * 2 * kMaxCtas * kItemTokens; }
 
 cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_pool, const void* k_scale,
                         const float* lse, const float* mass_in, float* mass_out, float decay, const Workspace& ws,
@@ -513,7 +513,7 @@ cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_p
   a.mass_in = mass_in;
   a.mass_out = mass_out;
   a.err = ws.err;
-  a.counters = ws.mass_counters;
+  a.counters = ws.part_counters;
   a.part = ws.mass_part;
   a.Hkv = p.num_kv_heads;
   a.S = p.page_size;

@@ -190,3 +190,45 @@ def test_mass_rows_without_lse_add_nothing(spg, hq, hkv, d, kv, q, lens, new):
     assert r.err() == 0
     for b, L in enumerate(lens):
         close(m[b, :, :L], want[b, :, :L], tol[b, :, :L], "mass")
+
+
+# ---- one workspace ------------------------------------------------------------------------------
+
+
+def test_one_workspace_under_several_selectors(spg):
+    """Chunks, masses and decode steps take turns on one workspace with parameters that differ in the selector alone."""
+    c = R.Chunk(8, 2, 128, 16, "bf16", "bf16", [3000, 2001], [300, 200])
+    r = Run(spg, c)
+    ps = [r.p] + [c.params(spg, selector="quest", token_budget=16 * n, n_sink_pages=1, n_recent_pages=1) for n in (8, 64, 180)]
+    r.ws = torch.zeros(max(spg.spg_chunk_workspace_size(p, c.T) for p in ps), dtype=torch.uint8, device="cuda")
+    mass = torch.zeros((2, 2, c.mp * 16), device="cuda")
+
+    def chunk(p):
+        r.p = p
+        r.out.fill_(7.0), r.lse.fill_(7.0), mass.fill_(7.0)
+        r.chunk()
+        r.mass(r.lse, None, mass, 1.0)
+        assert r.err() == 0
+        return [t.clone() for t in (r.out, r.lse, mass)]
+
+    want = chunk(ps[0])
+    check_chunk(r)
+    dq = torch.randn((2, 8, 128), device="cuda").bfloat16()
+    steps = {}
+    spg.spg_set_step_kernel(spg.STEP_KERNEL_SCHED)
+    try:
+        for i in (1, 0, 2, 3, 1, 0, 3):
+            if i:
+                buf = spg.alloc_buffers(ps[i])
+                spg.sparse_page_meta_update(ps[i], r.k_pool, None, r.page_table, r.seq_lens, 1, buf.minmax, None, None, None,
+                                            r.ws)
+                spg.sparse_decode_select_attend(ps[i], dq, r.k_pool, r.v_pool, None, None, r.page_table, r.seq_lens,
+                                                buf.minmax, None, None, None, buf.sel, buf.sel_cnt, buf.out, buf.lse, r.ws)
+                assert r.err() == 0
+                first = steps.setdefault(i, (buf.out.clone(), buf.sel.clone()))
+                assert torch.equal(first[0], buf.out) and torch.equal(first[1], buf.sel)
+            for p in (ps[0], ps[i]):
+                for a, b in zip(chunk(p), want):
+                    assert torch.equal(a, b)
+    finally:
+        spg.spg_set_step_kernel(spg.STEP_KERNEL_AUTO)
