@@ -336,7 +336,7 @@ spg_status spg_rope_freqs(const spg_rope* rope, int32_t head_dim, double* inv_fr
  * row: q_out = rotated q; the rotated k and v go to the row's cache slot,
  * converted to kv_dtype (int8: codes rint(x / s) in [-127, 127] with the fp16
  * scale s = absmax / 127 of the token and head, 1 for an all-zero row; x / s
- * in 32 bits, off by at most 2^-15 of a step).
+ * rounded to 32 bits, ties to the even code).
  *   q, k, v      q_dtype, [total_q] rows of [Hq | Hkv | Hkv][d], the rows
  *                q_stride, k_stride, v_stride elements apart (multiples of
  *                8, so that the three may be slices of one projection's

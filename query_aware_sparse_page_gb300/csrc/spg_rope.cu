@@ -164,14 +164,18 @@ __global__ void __launch_bounds__(kThreads) k_rope_append(const __grid_constant_
         __half sc = __float2half_rn(fminf(__fdiv_rn(m, 127.f), 65504.f));
         if (!(__half2float(sc) > 0.f)) sc = __float2half_rn(1.f);
         if (live && !is_q && page >= 0) {
-          // x / sc by one division per row: a quotient within 2^-15 of a
-          // border may go to either side of it
-          const float inv = __fdiv_rn(1.f, __half2float(sc));
+          // the code of the quotient x / sc in 32 bits, by one division per
+          // row: x * (1 / sc) is off by at most 2^-16 where codes are not
+          // clamped and the quotient's own rounding by 2^-18, so that only
+          // values within 2^-15 of a border are divided
+          const float scale = __half2float(sc), inv = __fdiv_rn(1.f, scale);
           uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float z = rintf((e < 8 ? x[e & 7] : y[e & 7]) * inv);
-            const int c = static_cast<int>(fmaxf(-127.f, fminf(127.f, z)));
+            const float v = e < 8 ? x[e & 7] : y[e & 7], z = v * inv;
+            float r = rintf(z);
+            if (fabsf(z - r) > 0.5f - 0x1p-15f) r = rintf(__fdiv_rn(v, scale));
+            const int c = static_cast<int>(fmaxf(-127.f, fminf(127.f, r)));
             w[e >> 2] |= static_cast<uint32_t>(c & 0xff) << (8 * (e & 3));
           }
           const size_t r = (static_cast<size_t>(page) * a.Hkv + hk) * a.S + slot;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_ref as R
-from test_gpu_paged import Run, check_chunk, close, dev
+from test_gpu_paged import Run, check_chunk, close, dev, host
 
 pytestmark = pytest.mark.gpu
 
@@ -232,3 +232,42 @@ def test_one_workspace_under_several_selectors(spg):
                     assert torch.equal(a, b)
     finally:
         spg.spg_set_step_kernel(spg.STEP_KERNEL_AUTO)
+
+
+# ---- rotary append ------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("q", ["f16", "bf16"])
+@pytest.mark.parametrize("d, S", [(64, 16), (128, 64)])
+def test_append_int8_codes_are_those_of_the_quotient(spg, d, S, q):
+    """code = rint(x / s) of the quotient in 32 bits, ties to the even code: rows whose values lie exactly between two
+    codes, and random ones."""
+    c = R.Chunk(8, 8, d, S, "i8", q, [700, 300], [700, 300])
+    bits = 11 if q == "f16" else 8
+    t = 0
+    for m in (1, 3, 5, 7, 9, 11, 13, 15):  # s = m 2^-9, exactly
+        odd = [k for k in range(1, 254, 2) if k * m < 1 << bits]
+        if 127 * m >= 1 << bits:
+            continue
+        for i in range(0, len(odd), d - 1):
+            for sign in (1, -1):
+                row = torch.zeros(d, dtype=R.F64)
+                row[0] = 127 * m * 2.0 ** -9
+                part = odd[i : i + d - 1]
+                row[1 : 1 + len(part)] = sign * torch.tensor(part, dtype=R.F64) * m * 2.0 ** -10
+                for x in (c.k, c.v):
+                    x[t, t % 8] = row.to(x.dtype)
+                assert torch.equal(c.k[t, t % 8].to(R.F64), row)
+                t += 1
+    r = Run(spg, c)
+    r.append(None, torch.empty_like(r.q))
+    assert r.err() == 0
+    pos = torch.cat([torch.arange(700), torch.arange(300)])
+    owner = torch.cat([torch.zeros(700), torch.ones(300)]).long()
+    phys, slot = c.page_table[owner, pos // S].long(), pos % S
+    for x, pool, scale in ((c.k, r.k_pool, r.k_scale), (c.v, r.v_pool, r.v_scale)):
+        s = (x.float().abs().amax(dim=-1) / 127.0).half()
+        s = torch.where(s > 0, s, torch.ones_like(s))
+        code = torch.round(x.float() / s.float()[..., None]).clamp(-127, 127).to(torch.int8)
+        assert torch.equal(host(scale)[phys, :, slot], s)
+        assert torch.equal(host(pool)[phys, :, slot], code)
