@@ -47,6 +47,7 @@ struct EvictArgs {
   uint8_t *k_pool, *v_pool;
   __half *k_scale, *v_scale;
   int Hkv, S, MP, n_phys, keep, n_sink, n_recent, row_bytes, resident;
+  int cluster, tiles;  // CTAs of a unit: of its cluster, and that move its rows
 };
 
 // atomics on another CTA's shared memory
@@ -89,8 +90,9 @@ __device__ __forceinline__ int block_scan(int v, int* s, int& total) {
   return base + incl - v;
 }
 
-// Cluster of gridDim.x CTAs for unit blockIdx.y; CTA r has the r-th share of
-// the sequence's tokens.
+// Units run along x (batch * kv-heads may be more than 65535, a grid's limit in
+// y): a cluster of a.cluster CTAs per unit; CTA r has the r-th share of the
+// sequence's tokens.
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
   extern __shared__ float s_mass[];  // the CTA's masses, where they fit
   __shared__ int s_hist[kBins];
@@ -98,7 +100,8 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const __grid_const
   __shared__ uint32_t s_range[2];            // of the unforced keys: min, max (whole cluster, in the first CTA)
   __shared__ int s_bin, s_need;              // found by the first CTA
   __shared__ int s_count[kMaxCluster][2];    // per CTA: tokens above the threshold, and equal to it
-  const int tid = threadIdx.x, rank = blockIdx.x, C = gridDim.x, unit = blockIdx.y, b = unit / a.Hkv;
+  const int tid = threadIdx.x, C = a.cluster, rank = blockIdx.x % C, unit = blockIdx.x / C,
+            b = unit / a.Hkv;
   if (tid == 0) {
     s_range[0] = 0xffffffffu;
     s_range[1] = 0u;
@@ -259,12 +262,13 @@ __device__ __forceinline__ long long pool_row(const EvictArgs& a, const int32_t*
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 128;  // kept tokens of a CTA
 
-// CTA (x, y): kept tokens 128 x .. of unit y, K and V
+// CTA x of a unit's `tiles`: kept tokens 128 x .., K and V
 template <int ROW>  // bytes
 __global__ void __launch_bounds__(kMoveThreads) k_evict_gather(const __grid_constant__ EvictArgs a) {
   __shared__ long long s_from[kMoveRows], s_to[kMoveRows];
   pdl_wait();
-  const int unit = blockIdx.y, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x, j0 = blockIdx.x * kMoveRows;
+  const int unit = blockIdx.x / a.tiles, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x;
+  const int j0 = blockIdx.x % a.tiles * kMoveRows;
   const int n = min(kMoveRows, a.new_lens[b] - j0);
   if (n <= 0) return;
   if (tid < n) {
@@ -306,15 +310,15 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_gather(const __grid_cons
 constexpr int kShiftRows = 8;        // rows of a thread per step
 constexpr int kSliceBytes = 32;      // a CTA's channels
 
-// CTA (x, y): slice x (K's, then V's, then the scales) of unit y
+// CTA x of a unit's `tiles`: slice x (K's, then V's, then the scales)
 __global__ void __launch_bounds__(kMoveThreads) k_evict_shift(const __grid_constant__ EvictArgs a) {
   pdl_wait();
-  const int unit = blockIdx.y, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x;
-  const int n = a.new_lens[b], slices = a.row_bytes / kSliceBytes, slice = blockIdx.x % slices;
+  const int unit = blockIdx.x / a.tiles, x = blockIdx.x % a.tiles, b = unit / a.Hkv, h = unit % a.Hkv, tid = threadIdx.x;
+  const int n = a.new_lens[b], slices = a.row_bytes / kSliceBytes, slice = x % slices;
   const int32_t* kept = a.kept + static_cast<size_t>(unit) * a.keep;
   const int32_t* pt = a.page_table + static_cast<size_t>(b) * a.MP;
-  const bool scales = static_cast<int>(blockIdx.x) == 2 * slices;
-  uint8_t* pool = static_cast<int>(blockIdx.x) >= slices ? a.v_pool : a.k_pool;
+  const bool scales = x == 2 * slices;
+  uint8_t* pool = x >= slices ? a.v_pool : a.k_pool;
   const int lpr = scales ? 1 : kSliceBytes / 16;  // threads of a row's slice
   const int col = slice * kSliceBytes + tid % lpr * 16, rows = kMoveThreads / lpr;
   const int per_step = rows * kShiftRows, steps = (n + per_step - 1) / per_step;
@@ -401,11 +405,12 @@ cudaError_t launch_evict(const spg_params& p, const float* mass, int keep, int n
   a.resident = share <= kMaxResident ? 1 : 0;
   // not resident: a later CTA's writes would meet an earlier one's reads in mass itself
   if (!a.resident) C = 1;
+  a.cluster = C;
   const size_t smem = a.resident ? sizeof(float) * share : 0;
   cudaError_t e = ensure_smem(k_evict_select, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(C, units);
+  cfg.gridDim = dim3(static_cast<unsigned>(C) * units);
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -421,10 +426,11 @@ cudaError_t launch_evict(const spg_params& p, const float* mass, int keep, int n
   e = cudaLaunchKernelEx(&cfg, k_evict_select, a);
   if (e != cudaSuccess) return e;
   if (in_place) {
-    const int x = 2 * (a.row_bytes / kSliceBytes) + (p.kv_dtype == SPG_I8 ? 1 : 0);
-    return launch_pdl(k_evict_shift, dim3(x, units), dim3(kMoveThreads), 0, stream, a);
+    a.tiles = 2 * (a.row_bytes / kSliceBytes) + (p.kv_dtype == SPG_I8 ? 1 : 0);
+    return launch_pdl(k_evict_shift, dim3(static_cast<unsigned>(a.tiles) * units), dim3(kMoveThreads), 0, stream, a);
   }
-  const dim3 grid(static_cast<unsigned>((std::min<long long>(keep, most) + kMoveRows - 1) / kMoveRows), units);
+  a.tiles = static_cast<int>((std::min<long long>(keep, most) + kMoveRows - 1) / kMoveRows);
+  const dim3 grid(static_cast<unsigned>(a.tiles) * units);
   switch (a.row_bytes) {
     case 256: return launch_pdl(k_evict_gather<256>, grid, dim3(kMoveThreads), 0, stream, a);
     case 128: return launch_pdl(k_evict_gather<128>, grid, dim3(kMoveThreads), 0, stream, a);

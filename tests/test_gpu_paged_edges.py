@@ -271,3 +271,37 @@ def test_append_int8_codes_are_those_of_the_quotient(spg, d, S, q):
         code = torch.round(x.float() / s.float()[..., None]).clamp(-127, 127).to(torch.int8)
         assert torch.equal(host(scale)[phys, :, slot], s)
         assert torch.equal(host(pool)[phys, :, slot], code)
+
+
+# ---- eviction: sizes --------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_evict_more_units_than_a_grid_dimension(spg, in_place):
+    """batch * kv-heads past 65535."""
+    B, H, S, L, keep = 8200, 8, 16, 13, 5
+    p = spg.make_params(batch=B, num_q_heads=H, num_kv_heads=H, head_dim=64, page_size=S, num_phys_pages=2 * B,
+                        max_pages_per_seq=1, kv_dtype="i8", q_dtype="f16", selector="all")
+    ws = torch.zeros(spg.spg_workspace_size(p), dtype=torch.uint8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    pool = lambda: torch.randint(-127, 128, (2 * B, H, S, 64), generator=g, device="cuda").to(torch.int8)  # noqa: E731
+    scale = lambda: torch.rand((2 * B, H, S), generator=g, device="cuda").half()  # noqa: E731
+    k, v, ks, vs = pool(), pool(), scale(), scale()
+    perm = torch.randperm(2 * B, generator=g, device="cuda").int()
+    pt, dst = perm[:B].view(B, 1).contiguous(), perm[B:].view(B, 1).contiguous()
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    mass = torch.rand((B, H, S), generator=g, device="cuda")
+    kept = torch.empty((B, H, keep), dtype=torch.int32, device="cuda")
+    nl = torch.empty(B, dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(mass)
+    order = mass[..., :L].clone()
+    order[..., L - 1] = math.inf  # the last token stays
+    ids = order.topk(keep, dim=-1).indices.sort(dim=-1).values
+    table = pt if in_place else dst
+    want = [x[pt[:, 0].long()].gather(2, ids[..., None].expand(-1, -1, -1, 64) if x.dim() == 4 else ids) for x in (k, v, ks, vs)]
+    spg.paged_cache_evict(p, mass, keep, 0, 1, k, v, ks, vs, pt, None if in_place else dst, lens, kept, nl, out, ws)
+    assert spg.spg_read_device_error(ws) == 0
+    assert torch.equal(kept.long(), ids) and bool((nl == keep).all())
+    assert torch.equal(out[..., :keep], mass.gather(2, ids)) and bool((out[..., keep:] == 0).all())
+    for x, w in zip((k, v, ks, vs), want):
+        assert torch.equal(x[table[:, 0].long()][:, :, :keep], w)
