@@ -408,6 +408,7 @@ spg_status paged_attention_mass(const spg_params* p, int32_t total_q, const void
  *   new_lens     [B] int32, min(seq_lens[b], keep); not seq_lens itself
  *   mass_out     [B][Hkv][MP * S] fp32: the kept tokens' masses in their new
  *                order, entries past new_lens left as they were; may be mass
+ *                (slower where MP * S is more than 393216)
  * n_sink, n_recent >= 0, keep >= 1, n_sink + n_recent <= keep.  Page
  * metadata has to be rebuilt afterwards (sparse_page_meta_update). */
 spg_status paged_cache_evict(const spg_params* p, const float* mass, int32_t keep, int32_t n_sink,

@@ -11,6 +11,11 @@
 // (batch, kv-head): each reads its tokens' masses once, into shared memory
 // (all of them before any is written, so mass_out may be mass), and the
 // passes meet in the first CTA's histogram over distributed shared memory.
+// Under a page table of more than 384K tokens they do not fit and every pass
+// reads them again: the cluster does, or with mass_out = mass one CTA, since
+// a later CTA's writes would meet an earlier one's reads (512K tokens of two
+// kv-heads to a quarter: 0.18 ms the whole call with the cluster, 1.1 ms with
+// one CTA; 4096 tokens of 32 kv-heads under such a table 31 and 33 us).
 //
 // Compacting moves rows of d channels.  To pages of its own it is a gather:
 // a CTA resolves the pages of 128 kept tokens, then streams their K and V
@@ -403,8 +408,7 @@ cudaError_t launch_evict(const spg_params& p, const float* mass, int keep, int n
   while (C < kMaxCluster && most > 2048ll * C) C *= 2;
   const long long share = (most + C - 1) / C;
   a.resident = share <= kMaxResident ? 1 : 0;
-  // not resident: a later CTA's writes would meet an earlier one's reads in mass itself
-  if (!a.resident) C = 1;
+  if (!a.resident && mass_out == mass) C = 1;
   a.cluster = C;
   const size_t smem = a.resident ? sizeof(float) * share : 0;
   cudaError_t e = ensure_smem(k_evict_select, smem);

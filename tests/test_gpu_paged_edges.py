@@ -305,3 +305,43 @@ def test_evict_more_units_than_a_grid_dimension(spg, in_place):
     assert torch.equal(out[..., :keep], mass.gather(2, ids)) and bool((out[..., keep:] == 0).all())
     for x, w in zip((k, v, ks, vs), want):
         assert torch.equal(x[table[:, 0].long()][:, :, :keep], w)
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("masses", ["lognormal", "three"])
+def test_evict_lengths_past_shared_memory(spg, masses, in_place):
+    """A sequence of more tokens than a cluster's shared memory holds masses of, beside a short one."""
+    N, S = 400000, 64
+    g = torch.Generator().manual_seed(4)
+    m = torch.exp(2 * torch.randn((2, 1, N), generator=g)) if masses == "lognormal" else torch.randint(0, 3, (2, 1, N), generator=g).float()
+    lens = [N - 7, 500]
+    p = spg.make_params(batch=2, num_q_heads=1, num_kv_heads=1, head_dim=64, page_size=S, num_phys_pages=2 * (N // S),
+                        max_pages_per_seq=N // S, kv_dtype="i8", q_dtype="f16", selector="all")
+    ws = torch.zeros(spg.spg_workspace_size(p), dtype=torch.uint8, device="cuda")
+    for keep in (390000, 20000):
+        pages = torch.randperm(2 * (N // S), generator=g).int()
+        pt = pages.view(2, -1).cuda()
+        k = torch.randint(-127, 128, (2 * (N // S), 1, S, 64), generator=g).to(torch.int8).cuda()
+        ks = torch.rand((2 * (N // S), 1, S), generator=g).half().cuda()
+        k0, ks0 = k.clone(), ks.clone()
+        mass = m.cuda()
+        out = mass if in_place else torch.full_like(mass, 5.0)
+        kept = torch.empty((2, 1, keep), dtype=torch.int32, device="cuda")
+        nl = torch.empty(2, dtype=torch.int32, device="cuda")
+        spg.paged_cache_evict(p, mass, keep, 4, 100, k, k.clone(), ks, ks.clone(), pt, None,
+                              torch.tensor(lens, dtype=torch.int32, device="cuda"), kept, nl, out, ws)
+        assert spg.spg_read_device_error(ws) == 0
+        assert host(nl).tolist() == [min(L, keep) for L in lens]
+        for b, L in enumerate(lens):
+            w = m[b, 0, :L].double()
+            w[:4] = math.inf
+            w[L - 100 :] = math.inf
+            n = min(L, keep)
+            ids = torch.sort(w, descending=True, stable=True).indices[:n].sort().values
+            assert torch.equal(host(kept)[b, 0, :n].long(), ids) and bool((kept[b, 0, n:] == -1).all())
+            assert torch.equal(host(out)[b, 0, :n], m[b, 0, ids])
+            assert torch.equal(host(out)[b, 0, n:], m[b, 0, n:] if in_place else torch.full((N - n,), 5.0))
+            j, t = torch.arange(n, device="cuda"), ids.cuda()
+            row = pt[b].long()
+            assert torch.equal(k[row[j // S], 0, j % S], k0[row[t // S], 0, t % S])
+            assert torch.equal(ks[row[j // S], 0, j % S], ks0[row[t // S], 0, t % S])
