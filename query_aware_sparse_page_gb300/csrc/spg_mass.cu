@@ -490,11 +490,17 @@ size_t mass_workspace_bytes() { return sizeof(float) * 2 * kMaxCtas * kItemToken
 cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_pool, const void* k_scale,
                         const float* lse, const float* mass_in, float* mass_out, float decay, const Workspace& ws,
                         cudaStream_t stream) {
-  // Up to 8 rows per (sequence, kv-head) on average (whatever their
-  // distribution) the keys' bytes bound the work, and the page stream reads
-  // them faster: a decode step of 16 sequences over int8 keys at 10K takes
-  // 45 to 49 us there and 94 us here.
-  if (static_cast<long long>(r.total_q) * (p.num_q_heads / p.num_kv_heads) <= 8ll * p.batch) {
+  // A decode step has one row per sequence: the keys' bytes bound the work and
+  // the page stream reads them faster (one token of each of 16 sequences at
+  // 10K, GQA 32/8, cold caches: bf16 keys in 16-token pages 70 us there and 83
+  // here, int8 keys in 64-token pages 60 and 87).  With more rows than
+  // sequences one of them may have nearly all, and the tiles take them better:
+  // 127 tokens and a piece of 129 over 2K to 4K 246 us there and 187 here, 31
+  // tokens and a piece of 33 over 32K 244 and 93 (two drafted tokens of each of
+  // 16 sequences would be 70 and 83).  Where other sequences have none, a piece
+  // of 256 rows beside 255 empty ones, 474 and 271, stays there: the host
+  // cannot tell it from a decode step.
+  if (r.total_q <= p.batch) {
     const cudaError_t e = launch_mass_few(p, r, k_pool, k_scale, lse, mass_in, mass_out, decay, ws.err, stream);
     if (e != cudaErrorNotSupported) return e;
   }

@@ -2,7 +2,8 @@
 // keys' bytes are all there is to it.
 //
 // The pages of all (sequence, kv-head) units are dealt out to the CTAs in
-// equal contiguous shares.  A producer warp streams the K pages by TMA into a
+// contiguous shares, equal in pages times groups of 8 rows; a page is the
+// share's that its first step falls into.  A producer warp streams the K pages by TMA into a
 // ring of slots, one lane per slot; four warps take the pages in turn and
 // compute S^T = K Q^T for 16 tokens and 8 rows at a time on mma.sync
 // m16n8k16 (a tcgen05 tile would be 128 x 128 for 8 rows), int8 codes widened
@@ -34,7 +35,9 @@ struct PageItems : ChunkShape {
   static constexpr int kLeast = 4;
   int s_log2;
   __device__ int items(const ChunkSeq& s) const { return (s.L + (1 << s_log2) - 1) >> s_log2; }
-  __device__ long long steps(const ChunkSeq&, int m) const { return m; }
+  // of one page: groups of 8 rows that it meets (without rows, its decay)
+  __device__ int page_steps(const ChunkSeq& s) const { return max(1, ((s.n << g_log2) + 7) >> 3); }
+  __device__ long long steps(const ChunkSeq& s, int m) const { return static_cast<long long>(m) * page_steps(s); }
 };
 
 struct FewArgs {
@@ -51,32 +54,42 @@ struct FewArgs {
   float scale_log2, decay;
 };
 
-// A page of the CTA's share.
+// A page of the CTA's share: page p of the P of (b, h), its first step `pos`.
 struct Cursor {
   const FewArgs& a;
-  int b, h, p, P;
+  long long pos, hi;
+  int b, h, p, P, each;
   ChunkSeq sq;
-  __device__ Cursor(const FewArgs& args, const Plan& plan) : a(args), b(plan.b), h(plan.h), p(plan.item) { load(); }
+  __device__ Cursor(const FewArgs& args, const Plan& plan)
+      : a(args), pos(plan.item_first), hi(plan.hi), b(plan.b), h(plan.h), p(plan.item) {
+    load();
+    if (pos < plan.lo) advance(1);  // the share begins within a page
+  }
+  __device__ bool live() const { return pos < hi; }
   __device__ void load() {
     int32_t bad = 0;
     sq = a.sh.seq(b, bad);
     P = a.sh.items(sq);
+    each = a.sh.page_steps(sq);
   }
-  // k pages on; the caller knows that there are as many
+  // k pages on, or to the end of all pages (which is the end of the share)
   __device__ void advance(int k) {
-    p += k;
-    while (p >= P) {
-      p -= P;
+    while (k >= P - p) {
+      k -= P - p;
+      pos += static_cast<long long>(P - p) * each;
+      p = 0;
       if (++h == a.Hkv) {
         h = 0;
         if (b + 1 >= a.sh.B) {
-          p = 0;
+          pos = hi;
           return;
         }
         ++b;
         load();
       }
     }
+    p += k;
+    pos += static_cast<long long>(k) * each;
   }
 };
 
@@ -152,8 +165,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kCtas) k_mass_few(const __g
   if (warp == 0) make_plan(a.sh, &plan, a.err, lane);
   __syncthreads();
   pdl_trigger();
-  const int n = static_cast<int>(plan.hi - plan.lo);
-  if (n == 0) return;
+  if (plan.lo == plan.hi) return;
 
   if (warp == kWarps) {
     // ---- one lane per slot: slot l takes pages l, l + slots, ... of the share
@@ -162,7 +174,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kCtas) k_mass_few(const __g
       Cursor c(a, plan);
       c.advance(lane);
       int round = 0;
-      for (int j = lane; j < n; j += slots, ++round) {
+      for (; c.live(); c.advance(slots), ++round) {
         int page = -1;
         if (c.sq.n > 0) {
           page = a.page_table[static_cast<size_t>(c.b) * a.MP + c.p];
@@ -187,7 +199,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kCtas) k_mass_few(const __g
         } else {
           mbar_arrive(&full[lane]);
         }
-        if (j + slots < n) c.advance(slots);
       }
       // the last copy of the slot has landed before the CTA leaves
       if (round > 0) mbar_wait_bounded(&full[lane], (round - 1) & 1);
@@ -200,10 +211,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kCtas) k_mass_few(const __g
   int have_b = -1, have_h = -1, have_g = -1;  // whose rows are in registers
   float l0 = 0.f, l1 = 0.f;                   // lse of rows 2t, 2t + 1 in the log2 domain
   const int g = lane >> 2, t = lane & 3;
-  if (warp >= n) return;
   Cursor c(a, plan);
   c.advance(warp);
-  for (int j = warp; j < n; j += kWarps) {
+  for (int j = warp; c.live(); j += kWarps, c.advance(kWarps)) {
     const int slot = j % slots;
     const int n_rows = c.sq.n << a.g_log2, groups = (n_rows + 7) / 8;
     const int tok0 = c.p * S, nv = min(S, c.sq.L - tok0);
@@ -268,7 +278,6 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, kCtas) k_mass_few(const __g
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[slot]);
-    if (j + kWarps < n) c.advance(kWarps);
   }
 }
 

@@ -345,3 +345,33 @@ def test_evict_lengths_past_shared_memory(spg, masses, in_place):
             row = pt[b].long()
             assert torch.equal(k[row[j // S], 0, j % S], k0[row[t // S], 0, t % S])
             assert torch.equal(ks[row[j // S], 0, j % S], ks0[row[t // S], 0, t % S])
+
+
+# ---- uneven batches -------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("hq, hkv, d, S, kv, q", [(8, 2, 128, 16, "bf16", "bf16"), (8, 1, 64, 32, "f16", "f16"),
+                                                  (4, 2, 128, 64, "i8", "f16"), (4, 2, 128, 64, "bf16", "bf16")])
+@pytest.mark.parametrize("at", [0, 17, 39])
+@pytest.mark.parametrize("rows", [40, 64])
+def test_mass_of_a_batch_with_one_piece(spg, hq, hkv, d, S, kv, q, rows, at):
+    """One sequence with nearly all the rows of a batch, whose others have one row or none."""
+    B = 40
+    g = torch.Generator().manual_seed(at)
+    lens = torch.randint(1, 500, (B,), generator=g).tolist()
+    lens[at] = 900
+    new = [b % 3 == 0 for b in range(B)]
+    new = [int(x) for x in new]
+    new[at] = rows - sum(new)
+    c = R.Chunk(hq, hkv, d, S, kv, q, lens, new)
+    r = Run(spg, c)
+    lse = R.attention(c)[2].float()
+    old = torch.rand((B, hkv, c.mp * S), generator=g)
+    want, tol = R.mass_of(c, lse, old, 0.5)
+    for _ in range(2):
+        m = torch.full(old.shape, 3.0, device="cuda")
+        r.mass(dev(lse), dev(old), m, 0.5)
+        assert r.err() == 0
+        for b, L in enumerate(lens):
+            close(m[b, :, :L], want[b, :, :L], tol[b, :, :L], "mass")
+            assert bool((m[b, :, L:] == 3.0).all())
