@@ -29,6 +29,7 @@ constexpr int kWarps = 4;            // that sum; one more fills the ring
 // rings of 64 KB 80.9)
 constexpr int kCtas = 4;
 constexpr int kRingBytes = 48 * 1024;
+constexpr size_t kSmBytes = 228 * 1024;  // shared memory of an SM
 constexpr int kMaxSlots = 32;        // one per lane of the filling warp
 
 struct PageItems : ChunkShape {
@@ -294,7 +295,10 @@ cudaError_t few_typed(const spg_params& p, FewArgs& a, const void* k_pool, cudaS
   const auto kern = k_mass_few<T, TQ, D>;
   const cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(kCtas * device_sm_count()), dim3((kWarps + 1) * 32), smem, st, a);
+  // CTAs that an SM holds at once (each with 1 KB of the system's and up to 2
+  // KB of barriers and plan): the shares are equal, a CTA more would run alone
+  const int ctas = std::min<int>(kCtas, static_cast<int>(kSmBytes / (smem + 3 * 1024)));
+  return launch_pdl(kern, dim3(ctas * device_sm_count()), dim3((kWarps + 1) * 32), smem, st, a);
 }
 
 }  // namespace
