@@ -301,49 +301,56 @@ def dense_decode_attention(p, q, k_pool, v_pool, k_scale, v_scale, page_table, s
 _ELEM = {F16: torch.float16, BF16: torch.bfloat16, I8: torch.int8}
 
 
-def _refuse(name, t, shape, dtype):
+def _refuse(name, t, shape, dtype, dev):
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if min(t.get_device(), dev) >= 0 and t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the workspace on device {dev}")
     raise ValueError("libspg takes contiguous device tensors")
 
 
-def _take(name, t, shape, dtype):
-    """Device pointer of a tensor that has to be contiguous, of this shape and type."""
+def _device(ws):
+    """The workspace's device (-1: the host), which every other tensor has to be on: a kernel there takes them as its
+    own memory."""
+    return -1 if ws is None else ws.get_device()
+
+
+def _take(dev, name, t, shape, dtype):
+    """Device pointer of a tensor that has to be contiguous, of this shape and type, on this device."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _refuse(name, t, shape, dtype)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, shape, dtype, dev)
     return t.data_ptr()
 
 
-def _take_rows(name, t, shape, dtype):
+def _take_rows(dev, name, t, shape, dtype):
     """Pointer and row stride of a tensor whose rows are contiguous."""
     if t is None:
         return None, 0
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda:
-        _refuse(name, t, shape, dtype)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, shape, dtype, dev)
     row, head, one = t.stride()
     if t.numel() and (one != 1 or (shape[1] > 1 and head != shape[2])):
         raise ValueError(f"{name}: the heads of one token have to be contiguous")
     return t.data_ptr(), row if shape[0] > 1 else shape[1] * shape[2]
 
 
-def _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, q_start=None):
+def _take_cache(dev, p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, q_start=None):
     pool, kv = (p.num_phys_pages, p.num_kv_heads, p.page_size, p.head_dim), _ELEM[p.kv_dtype]
-    return (_take("k_pool", k_pool, pool, kv), _take("v_pool", v_pool, pool, kv),
-            _take("k_scale", k_scale, pool[:3], torch.float16), _take("v_scale", v_scale, pool[:3], torch.float16),
-            _take("page_table", page_table, (p.batch, p.max_pages_per_seq), torch.int32),
-            _take("seq_lens", seq_lens, (p.batch,), torch.int32),
-            _take("q_start", q_start, (p.batch + 1,), torch.int32))
+    return (_take(dev, "k_pool", k_pool, pool, kv), _take(dev, "v_pool", v_pool, pool, kv),
+            _take(dev, "k_scale", k_scale, pool[:3], torch.float16), _take(dev, "v_scale", v_scale, pool[:3], torch.float16),
+            _take(dev, "page_table", page_table, (p.batch, p.max_pages_per_seq), torch.int32),
+            _take(dev, "seq_lens", seq_lens, (p.batch,), torch.int32),
+            _take(dev, "q_start", q_start, (p.batch + 1,), torch.int32))
 
 
-def _call(fn, where, ws, stream, *args):
+def _call(dev, fn, where, ws, stream, *args):
     """fn(*args, workspace, its bytes, stream) with the workspace's device current."""
-    if ws is None or not ws.is_cuda or not ws.is_contiguous():
+    if dev < 0 or not ws.is_contiguous():
         raise ValueError("a contiguous workspace on the device is needed")
-    dev = ws.device.index
     if stream is None:
         stream = torch.cuda.current_stream(dev).cuda_stream
     size = ws.numel() * ws.element_size()
@@ -370,50 +377,50 @@ def spg_rope_freqs(rope: spg_rope, head_dim: int):
 
 def paged_rope_append(p, rope, q, k, v, q_start, page_table, seq_lens, k_pool, v_pool, k_scale=None,
                       v_scale=None, q_out=None, positions=None, ws=None, stream=None):
-    T, d, qd = k.shape[0], p.head_dim, _ELEM[p.q_dtype]
-    qp, qs = _take_rows("q", q, (T, p.num_q_heads, d), qd)
-    kp, ks = _take_rows("k", k, (T, p.num_kv_heads, d), qd)
-    vp, vs = _take_rows("v", v, (T, p.num_kv_heads, d), qd)
-    kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table,
+    dev, T, d, qd = _device(ws), k.shape[0], p.head_dim, _ELEM[p.q_dtype]
+    qp, qs = _take_rows(dev, "q", q, (T, p.num_q_heads, d), qd)
+    kp, ks = _take_rows(dev, "k", k, (T, p.num_kv_heads, d), qd)
+    vp, vs = _take_rows(dev, "v", v, (T, p.num_kv_heads, d), qd)
+    kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(dev, p, k_pool, v_pool, k_scale, v_scale, page_table,
                                                      seq_lens, q_start)
-    out = _take("q_out", q_out, (T, p.num_q_heads, d), qd)
-    pos = _take("positions", positions, (T,), torch.int32)
-    _call(LIB.paged_rope_append, "paged_rope_append", ws, stream, ctypes.byref(p),
+    out = _take(dev, "q_out", q_out, (T, p.num_q_heads, d), qd)
+    pos = _take(dev, "positions", positions, (T,), torch.int32)
+    _call(dev, LIB.paged_rope_append, "paged_rope_append", ws, stream, ctypes.byref(p),
           None if rope is None else ctypes.byref(rope), T, qp, qs, kp, ks, vp, vs, st, pos, pt, sl, kpool, vpool,
           ksc, vsc, out)
 
 
 def paged_chunk_attention(p, q, q_start, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, out,
                           lse=None, ws=None, stream=None):
-    T, rows, qd = q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim), _ELEM[p.q_dtype]
-    qp, op = _take("q", q, rows, qd), _take("out", out, rows, qd)
-    lp = _take("lse", lse, rows[:2], torch.float32)
-    kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table,
+    dev, T, rows, qd = _device(ws), q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim), _ELEM[p.q_dtype]
+    qp, op = _take(dev, "q", q, rows, qd), _take(dev, "out", out, rows, qd)
+    lp = _take(dev, "lse", lse, rows[:2], torch.float32)
+    kpool, vpool, ksc, vsc, pt, sl, st = _take_cache(dev, p, k_pool, v_pool, k_scale, v_scale, page_table,
                                                      seq_lens, q_start)
-    _call(LIB.paged_chunk_attention, "paged_chunk_attention", ws, stream, ctypes.byref(p), T, qp, st, kpool, vpool,
+    _call(dev, LIB.paged_chunk_attention, "paged_chunk_attention", ws, stream, ctypes.byref(p), T, qp, st, kpool, vpool,
           ksc, vsc, pt, sl, op, lp)
 
 
 def paged_attention_mass(p, q, q_start, k_pool, k_scale, page_table, seq_lens, lse, mass_in, mass_out,
                          decay=1.0, ws=None, stream=None):
-    T, rows = q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim)
+    dev, T, rows = _device(ws), q.shape[0], (q.shape[0], p.num_q_heads, p.head_dim)
     m = (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size)
-    qp, lp = _take("q", q, rows, _ELEM[p.q_dtype]), _take("lse", lse, rows[:2], torch.float32)
-    mi, mo = _take("mass_in", mass_in, m, torch.float32), _take("mass_out", mass_out, m, torch.float32)
-    kpool, _, ksc, _, pt, sl, st = _take_cache(p, k_pool, None, k_scale, None, page_table, seq_lens, q_start)
-    _call(LIB.paged_attention_mass, "paged_attention_mass", ws, stream, ctypes.byref(p), T, qp, st, kpool, ksc, pt,
+    qp, lp = _take(dev, "q", q, rows, _ELEM[p.q_dtype]), _take(dev, "lse", lse, rows[:2], torch.float32)
+    mi, mo = _take(dev, "mass_in", mass_in, m, torch.float32), _take(dev, "mass_out", mass_out, m, torch.float32)
+    kpool, _, ksc, _, pt, sl, st = _take_cache(dev, p, k_pool, None, k_scale, None, page_table, seq_lens, q_start)
+    _call(dev, LIB.paged_attention_mass, "paged_attention_mass", ws, stream, ctypes.byref(p), T, qp, st, kpool, ksc, pt,
           sl, lp, mi, mo, float(decay))
 
 
 def paged_cache_evict(p, mass, keep, n_sink, n_recent, k_pool, v_pool, k_scale, v_scale, page_table,
                       dst_page_table, seq_lens, kept, new_lens, mass_out, ws=None, stream=None):
-    m, keep = (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size), int(keep)
-    mi, mo = _take("mass", mass, m, torch.float32), _take("mass_out", mass_out, m, torch.float32)
-    kpool, vpool, ksc, vsc, pt, sl, _ = _take_cache(p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens)
-    dst = _take("dst_page_table", dst_page_table, (p.batch, p.max_pages_per_seq), torch.int32)
-    kp = _take("kept", kept, (p.batch, p.num_kv_heads, keep), torch.int32)
-    nl = _take("new_lens", new_lens, (p.batch,), torch.int32)
-    _call(LIB.paged_cache_evict, "paged_cache_evict", ws, stream, ctypes.byref(p), mi, keep, int(n_sink),
+    dev, m, keep = _device(ws), (p.batch, p.num_kv_heads, p.max_pages_per_seq * p.page_size), int(keep)
+    mi, mo = _take(dev, "mass", mass, m, torch.float32), _take(dev, "mass_out", mass_out, m, torch.float32)
+    kpool, vpool, ksc, vsc, pt, sl, _ = _take_cache(dev, p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens)
+    dst = _take(dev, "dst_page_table", dst_page_table, (p.batch, p.max_pages_per_seq), torch.int32)
+    kp = _take(dev, "kept", kept, (p.batch, p.num_kv_heads, keep), torch.int32)
+    nl = _take(dev, "new_lens", new_lens, (p.batch,), torch.int32)
+    _call(dev, LIB.paged_cache_evict, "paged_cache_evict", ws, stream, ctypes.byref(p), mi, keep, int(n_sink),
           int(n_recent), kpool, vpool, ksc, vsc, pt, dst, sl, kp, nl, mo)
 
 
