@@ -295,7 +295,8 @@ spg_status dense_decode_attention(const spg_params* p, const void* q, const void
  *   q            [total_q][Hq][d]      q_dtype
  * A sequence whose q_start or seq_lens entry is bad (SPG_DEVERR_Q_START,
  * SPG_DEVERR_SEQ_LEN) is skipped, a bad page is skipped
- * (SPG_DEVERR_PAGE_ID): its tokens take no part and are not written.
+ * (SPG_DEVERR_PAGE_ID): its tokens take no part and are not written
+ * (paged_attention_mass decays their masses and adds nothing).
  * The selector fields of spg_params play no part here.  Cached values of
  * tokens below seq_lens must be finite; slots past it may hold anything. */
 
@@ -347,7 +348,8 @@ spg_status spg_rope_freqs(const spg_rope* rope, int32_t head_dim, double* inv_fr
  *                cache positions (an evicted cache is shorter than the text
  *                it stands for)
  *   rope         NULL leaves q and k as they are
- * The angles are exact to 2^-32 of a turn at any position.  Page metadata is
+ * The angle at position t is off by at most 2^-26 + t * 2^-54 of a turn (its
+ * 32-bit form, and the frequencies' 64-bit form).  Page metadata is
  * not touched: call sparse_page_meta_update (rebuild == 0 after one token per
  * sequence, else rebuild != 0) before the next selection, or let
  * sparse_decode_step append its one token. */

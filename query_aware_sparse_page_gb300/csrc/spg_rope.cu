@@ -5,8 +5,9 @@
 //   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin) * mscale.
 // The angle is kept as a fraction of a turn in 64-bit fixed point: with
 // F_i = f_i / 2 pi * 2^64, t * F_i mod 2^64 is one integer product whose
-// wrap-around is the reduction, so far positions lose nothing (the error is
-// t * 2^-54 of a turn from F_i itself); its upper 32 bits go to sincospif.
+// wrap-around is the reduction, so that far positions lose only what F_i
+// itself is off by (t * 2^-54 of a turn); its upper 32 bits go to sincospif as
+// a float, which rounds them to 2^-26 of a turn.
 //
 // Bound by bytes: every row of q, k and v is read and written once.  A CTA
 // takes a few tokens: one pass computes their cos and sin into shared memory
