@@ -1,4 +1,5 @@
 """The paged-chunk operators where they are easily wrong.  References in 64 bits, as in tests/paged_ref.py."""
+import decimal
 import math
 
 import pytest
@@ -273,6 +274,44 @@ def test_append_int8_codes_are_those_of_the_quotient(spg, d, S, q):
         assert torch.equal(host(pool)[phys, :, slot], code)
 
 
+def exact_turns(rot, base, positions):
+    """Angles [n][rot / 2] in radians within one turn, from 60 digits."""
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+        f = [(decimal.Decimal(base).ln() * -2 * i / rot).exp() / two_pi for i in range(rot // 2)]
+        return torch.tensor([[float((p * x) % 1 * two_pi) for x in f] for p in positions], dtype=R.F64)
+
+
+@pytest.mark.parametrize("base", [10000, 500000])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_append_positions_to_the_end_of_32_bits(spg, layout, base):
+    """The rotation at any position: the angle is off by at most 2^-26 of a turn (its 32-bit form) and t 2^-54 (the
+    frequency's 64-bit form), with rotate_tol's other terms."""
+    c = R.Chunk(2, 1, 128, 16, "f16", "f16", [64], [64])
+    pos = [0, 1, 2, 2 ** 24 + 1, 2 ** 30 + 12345, 2 ** 31 - 1, 2 ** 31 - 2] + [
+        int(x) for x in torch.randint(0, 2 ** 31 - 1, (57,), generator=torch.Generator().manual_seed(3))]
+    c.q[:] = torch.where(c.q.abs() < 2 ** -3, torch.full_like(c.q, 0.5), c.q)
+    r = Run(spg, c)
+    out = torch.empty_like(r.q)
+    r.append(spg.make_rope(layout=layout, base=float(base)), out, torch.tensor(pos, dtype=torch.int32, device="cuda"))
+    assert r.err() == 0
+    ang = exact_turns(128, base, pos)[:, None]
+    x = c.q.to(R.F64)
+    one = slice(0, 64) if layout == "half" else slice(0, 128, 2)
+    two = slice(64, 128) if layout == "half" else slice(1, 128, 2)
+    want = torch.empty_like(x)
+    want[..., one] = x[..., one] * torch.cos(ang) - x[..., two] * torch.sin(ang)
+    want[..., two] = x[..., two] * torch.cos(ang) + x[..., one] * torch.sin(ang)
+    far = torch.tensor(pos, dtype=R.F64)[:, None, None] * 2.0 ** -54 * 2 * math.pi
+    pair = (x[..., one].abs() + x[..., two].abs()) * far
+    tol = R.rotate_tol(c.q, 128, layout, 1.0)
+    tol[..., one] += pair
+    tol[..., two] += pair
+    e = 2.0 ** -11
+    close(out, want, e * want.abs() + (1 + e) * tol + 2.0 ** -25, "q")
+
+
 # ---- eviction: sizes --------------------------------------------------------------------------------
 
 
@@ -345,44 +384,6 @@ def test_evict_lengths_past_shared_memory(spg, masses, in_place):
             row = pt[b].long()
             assert torch.equal(k[row[j // S], 0, j % S], k0[row[t // S], 0, t % S])
             assert torch.equal(ks[row[j // S], 0, j % S], ks0[row[t // S], 0, t % S])
-
-
-def exact_turns(rot, base, positions):
-    """Angles [n][rot / 2] in radians within one turn, from 60 digits."""
-    with decimal.localcontext() as ctx:
-        ctx.prec = 60
-        two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
-        f = [(decimal.Decimal(base).ln() * -2 * i / rot).exp() / two_pi for i in range(rot // 2)]
-        return torch.tensor([[float((p * x) % 1 * two_pi) for x in f] for p in positions], dtype=R.F64)
-
-
-@pytest.mark.parametrize("base", [10000, 500000])
-@pytest.mark.parametrize("layout", ["half", "interleaved"])
-def test_append_positions_to_the_end_of_32_bits(spg, layout, base):
-    """The rotation at any position: the angle is off by at most 2^-26 of a turn (its 32-bit form) and t 2^-54 (the
-    frequency's 64-bit form), with rotate_tol's other terms."""
-    c = R.Chunk(2, 1, 128, 16, "f16", "f16", [64], [64])
-    pos = [0, 1, 2, 2 ** 24 + 1, 2 ** 30 + 12345, 2 ** 31 - 1, 2 ** 31 - 2] + [
-        int(x) for x in torch.randint(0, 2 ** 31 - 1, (57,), generator=torch.Generator().manual_seed(3))]
-    c.q[:] = torch.where(c.q.abs() < 2 ** -3, torch.full_like(c.q, 0.5), c.q)
-    r = Run(spg, c)
-    out = torch.empty_like(r.q)
-    r.append(spg.make_rope(layout=layout, base=float(base)), out, torch.tensor(pos, dtype=torch.int32, device="cuda"))
-    assert r.err() == 0
-    ang = exact_turns(128, base, pos)[:, None]
-    x = c.q.to(R.F64)
-    one = slice(0, 64) if layout == "half" else slice(0, 128, 2)
-    two = slice(64, 128) if layout == "half" else slice(1, 128, 2)
-    want = torch.empty_like(x)
-    want[..., one] = x[..., one] * torch.cos(ang) - x[..., two] * torch.sin(ang)
-    want[..., two] = x[..., two] * torch.cos(ang) + x[..., one] * torch.sin(ang)
-    far = torch.tensor(pos, dtype=R.F64)[:, None, None] * 2.0 ** -54 * 2 * math.pi
-    pair = (x[..., one].abs() + x[..., two].abs()) * far
-    tol = R.rotate_tol(c.q, 128, layout, 1.0)
-    tol[..., one] += pair
-    tol[..., two] += pair
-    e = 2.0 ** -11
-    close(out, want, e * want.abs() + (1 + e) * tol + 2.0 ** -25, "q")
 
 
 # ---- uneven batches -------------------------------------------------------------------------------
