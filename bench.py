@@ -41,14 +41,15 @@ NOMINAL_HBM_GBS = 8000.0
 # that workload, and the sha256 of the kernel code it was taken on (see
 # csrc_sha256; profiles/k_fused_<workload>.md).  Reported only while the code
 # matches.
-# The device code of that kernel: other kernels of the library come and go
-# without touching it.
-STEP_SOURCES = ("spg_append.cuh", "spg_attn_core.cuh", "spg_common.cuh", "spg_fused.cu", "spg_select_core.cuh")
+# That kernel's source with all it includes, and its tensor maps': other
+# kernels of the library come and go without touching them.
+STEP_SOURCES = ("spg_append.cuh", "spg_attn_core.cuh", "spg_common.cuh", "spg_fused.cu", "spg_internal.h",
+                "spg_select_core.cuh", "spg_tma.cu")
 NCU_TRAFFIC = {
     # workload: (DRAM bytes of one launch, code hash, kernel)
-    "llama2-7b-mha-32k": (67_890_432, "33f648d414a0a877f99c31ad00ca840f222dc51519097eba945e93c23b2fefc3", "k_fused"),
-    "long-scan-b4-128k": (205_280_000, "33f648d414a0a877f99c31ad00ca840f222dc51519097eba945e93c23b2fefc3", "k_fused"),
-    "sals-int8-b16-10k-4x": (100_827_136, "33f648d414a0a877f99c31ad00ca840f222dc51519097eba945e93c23b2fefc3", "k_fused"),
+    "llama2-7b-mha-32k": (67_619_840, "f4e51227135ce389a840a687fe5a684070612805dcffdd0ea03c4fb0d0ba8bc8", "k_fused"),
+    "long-scan-b4-128k": (204_981_760, "f4e51227135ce389a840a687fe5a684070612805dcffdd0ea03c4fb0d0ba8bc8", "k_fused"),
+    "sals-int8-b16-10k-4x": (100_395_264, "f4e51227135ce389a840a687fe5a684070612805dcffdd0ea03c4fb0d0ba8bc8", "k_fused"),
 }
 
 
