@@ -272,7 +272,9 @@ cudaError_t launch_rope_append(const spg_params& p, const spg_rope* rope, const 
   a.MP = p.max_pages_per_seq;
   a.n_phys = p.num_phys_pages;
   a.total_q = r.total_q;
-  // a token per CTA while they are few; 8192 tokens take 74.4 us in pairs, 75.8 one by one
+  // A token per CTA while they are few, then two (cold caches, one by one and
+  // in pairs: MHA-32 fp16 512 tokens 13.5 and 15.5 us, 2048 27.8 and 29.9, 3000
+  // 36.0 and 35.0, 8192 79.0 and 77.0; int8 GQA 32/8 8192 74.9 and 64.7)
   a.tokens = r.total_q > 2048 ? 2 : 1;
   const bool i8 = p.kv_dtype == SPG_I8;
   if (p.q_dtype == SPG_F16)
