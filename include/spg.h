@@ -368,14 +368,22 @@ spg_status paged_rope_append(const spg_params* p, const spg_rope* rope, int32_t 
  * A row that sees no token (its pages are bad) gets out = 0 and lse = -inf, a
  * row with a NaN among its logits NaN in both.
  * Logits, softmax statistics and sums in fp32; the probabilities (int8 pools:
- * times their V scales, of any size) enter the P V product rounded to the
- * 16-bit type, relative to the row's largest.  Needs
- * spg_chunk_workspace_size bytes. */
+ * times their V scales, of any size) enter the P V product as the sum of two
+ * values of the 16-bit type (see spg_set_chunk_parts), relative to the row's
+ * largest.  Needs spg_chunk_workspace_size bytes. */
 spg_status paged_chunk_attention(const spg_params* p, int32_t total_q, const void* q,
                                  const int32_t* q_start, const void* k_pool, const void* v_pool,
                                  const void* k_scale, const void* v_scale,
                                  const int32_t* page_table, const int32_t* seq_lens, void* out,
                                  float* lse, void* ws, size_t ws_bytes, spg_stream_t stream);
+
+/* 16-bit values in whose sum a probability enters paged_chunk_attention's P V
+ * product, process-wide: 2 (the default: 16 bits of it with bf16, 22 with
+ * fp16, so that the result is off by little more than its own rounding) or 1
+ * (half a step per token more, together 1.4 times the error; prompts are 1.3
+ * times as fast).  Not thread-safe with respect to calls on other host
+ * threads.  SPG_EINVAL for other values. */
+spg_status spg_set_chunk_parts(int32_t parts);
 
 /* Attention weight received by every cached token (StreamingLLM/H2O heavy
  * hitters): per (batch, kv-head), over the group's query heads and the

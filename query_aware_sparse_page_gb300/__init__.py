@@ -13,7 +13,7 @@ from .binding import (  # noqa: F401
     sparse_page_score, sparse_page_select, sparse_page_sketch_dots, spg_abi_version, spg_chunk_workspace_size,
     spg_clear_device_error, spg_params, spg_rope, spg_rope_freqs,
     spg_read_device_error, spg_status_str, spg_test_withhold_first_stage, spg_validate, spg_workspace_size, status_str,
-    STEP_KERNEL_AUTO, STEP_KERNEL_CLUSTER, STEP_KERNEL_SCHED, spg_prefer_dense, spg_set_step_kernel, spg_step_kernel,
-    spg_step_launches, step_kernel_name, step_launch_count,
+    STEP_KERNEL_AUTO, STEP_KERNEL_CLUSTER, STEP_KERNEL_SCHED, spg_prefer_dense, spg_set_chunk_parts, spg_set_step_kernel,
+    spg_step_kernel, spg_step_launches, step_kernel_name, step_launch_count,
 )
 from .buffers import DecodeBuffers, alloc_buffers, params_for  # noqa: F401

@@ -133,6 +133,7 @@ def _load():
         "spg_prefer_dense": ([P, c_int32, c_float], c_int32),
         "spg_step_launches": ([P], c_int32),
         "spg_set_step_kernel": ([c_int32], c_int32),
+        "spg_set_chunk_parts": ([c_int32], c_int32),
         "spg_read_device_error": ([v, POINTER(c_int32), v], c_int32),
         "spg_clear_device_error": ([v, v], c_int32),
         "spg_test_withhold_first_stage": ([v, v], c_int32),
@@ -373,6 +374,11 @@ def spg_rope_freqs(rope: spg_rope, head_dim: int):
     f, m = (c_double * max(head_dim, 2))(), c_double(0)
     _check(LIB.spg_rope_freqs(ctypes.byref(rope), int(head_dim), f, ctypes.byref(m)), "spg_rope_freqs")
     return list(f)[: (rope.rot_dim or head_dim) // 2], m.value
+
+
+def spg_set_chunk_parts(parts: int):
+    """16-bit values (2, the default, or 1) in whose sum a probability of chunk attention enters the P V product."""
+    _check(LIB.spg_set_chunk_parts(int(parts)), "spg_set_chunk_parts")
 
 
 def paged_rope_append(p, rope, q, k, v, q_start, page_table, seq_lens, k_pool, v_pool, k_scale=None,

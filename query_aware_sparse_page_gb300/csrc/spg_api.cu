@@ -125,6 +125,10 @@ spg_status check_meta_inputs(const spg_params* p, const void* minmax, const uint
 // (spg_set_step_kernel): 0 automatic, 1 cluster kernel, 2 scheduled kernel.
 std::atomic<int> g_step_pref{0};
 
+// 16-bit parts of a weight in chunk attention's P V product, process-wide
+// (spg_set_chunk_parts).
+std::atomic<int> g_chunk_parts{2};
+
 bool use_fused(const spg_params& p, int append) {
   return g_step_pref.load() != 2 && spg::fused_supported(p, append);
 }
@@ -478,7 +482,8 @@ spg_status paged_chunk_attention(const spg_params* p, int32_t total_q, const voi
     return SPG_EINVAL;
   if ((s = check_kv(p, k_pool, v_pool, k_scale, v_scale)) != SPG_OK) return s;
   const spg::ChunkRows r{q, q_start, page_table, seq_lens, total_q};
-  return cuda_status(spg::launch_chunk(*p, r, k_pool, v_pool, k_scale, v_scale, out, lse, ws,
+  return cuda_status(spg::launch_chunk(*p, r, k_pool, v_pool, k_scale, v_scale, out, lse,
+                                       g_chunk_parts.load(), ws,
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -546,6 +551,12 @@ int32_t spg_step_launches(const spg_params* p) {
   // append (none for the probe selector), scoring (+ a separate selection
   // kernel past 8192 pages), attention
   return (p->selector == SPG_SEL_PROBE ? 2 : 3) + (p->max_pages_per_seq > 8192 ? 1 : 0);
+}
+
+spg_status spg_set_chunk_parts(int32_t parts) {
+  if (parts != 1 && parts != 2) return SPG_EINVAL;
+  g_chunk_parts.store(parts);
+  return SPG_OK;
 }
 
 spg_status spg_set_step_kernel(int32_t kernel) {

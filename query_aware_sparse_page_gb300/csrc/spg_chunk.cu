@@ -6,10 +6,12 @@
 // cache position pos0 + r / G, and sees the tokens up to there.  A step is
 // 128 tokens of an item:
 //   S = Q K^T      both from shared memory, S in TMEM
-//   P = exp2(scale S - m)  by the softmax warps, written back over S as
-//                  16-bit pairs
+//   P = exp2(scale S - m)  by the softmax warps, written back over S as the
+//                  sum of two 16-bit values: 16 logits become 8 columns of
+//                  the first and 8 of what its rounding left
 //   O += P V       A from TMEM, V from shared memory (its rows are the
-//                  contraction: MN-major), O in TMEM
+//                  contraction: MN-major), a product for each of the two
+//                  values, O in TMEM
 // with the running maximum m and sum l of the softmax per row.  m is only
 // raised when a (base 2) logit exceeds it by more than kTop, and then set
 // kHead below that logit: p stays at most 2^kTop, O is rescaled in the rare
@@ -23,14 +25,16 @@
 // stream has an issuing warp and two softmax warpgroups: a thread has one row
 // and half of the step's tokens, and the two threads of a row agree on its
 // maximum through shared memory (one thread per row: 302 against 284 us for
-// a ragged batch to 16K).
+// a ragged batch to 16K, with P as one value).
 //
 // Measured (GB300): 2048 tokens at the end of 32K, MHA-32 fp16, 16-token
-// pages: 0.91 to 0.96 ms, 1.11 to 1.18 PFLOP/s of 1.90 measured.  Products alone take 0.53
-// ms; the rest is the hand-over between the streams (a chain of softmax,
-// issue and products of 3400 cycles per step against 2048 of products) and
-// the copies into shared memory beside them.  Few rows over long caches: 8
-// sequences of 4K to 32K with up to 8 drafted tokens 140 us, 5.1 TB/s.
+// pages: 1.24 to 1.26 ms.  With P as one value (spg_set_chunk_parts) 0.93 to
+// 0.97 ms, 1.10 to 1.14 PFLOP/s of 1.90 measured: products alone take 0.53 ms
+// (0.80 with the second part's); the rest is the hand-over between the streams
+// (with one value a chain of softmax, issue and products of 3400 cycles per
+// step against 2048 of products) and the copies into shared memory beside
+// them.  Few rows over long caches: 8 sequences of 4K to 32K with up to 8
+// drafted tokens 161 us, 4.5 TB/s (one value: 141).
 //
 // The steps of all items, in the order (sequence, kv-head, rows), are dealt
 // out to the CTAs in equal contiguous shares, whatever the lengths: an item
@@ -50,10 +54,10 @@
 // scales are, and the sum of p (larger or smaller by what the scales are)
 // needs no more than fp32's range.
 //
-// Roundings: P (int8: times the value scale) to the 16-bit type, as the
-// products take it, and the result; everything else is fp32.  P as the sum of
-// two 16-bit values, in a first form with some spills, took 2.01 against 0.96
-// ms for the piece at 32K and 228 against 140 us for the drafts.
+// Roundings: P (int8: times the value scale) to two values of the 16-bit type,
+// 2^-16 (bf16) or 2^-22 of it, and the result; everything else is fp32.  The
+// caller may ask for one value, and then has the error of 16-bit weights, 1.4
+// times that of the result's rounding alone.
 #include <algorithm>
 #include <cmath>
 
@@ -162,7 +166,8 @@ struct Misc {
   alignas(16) float scales[I8 ? VST : 1][3][I8 ? kTile : 1];
 };
 
-template <typename T, typename TQ, int D>
+// PARTS: 16-bit values in whose sum a weight enters the P V product
+template <typename T, typename TQ, int D, int PARTS>
 struct Kernel {
   static constexpr bool I8 = sizeof(T) == 1;
   using Lay = Layout<D, I8>;
@@ -184,8 +189,8 @@ struct Kernel {
   // products.  The streams' batches (P V of a step, S of the next) go to the
   // tensor cores strictly in turn: left to themselves the two fall into step,
   // both in their softmax while the tensor cores idle, then both in line
-  // (976 against 925 us for a prompt piece at 32K; with int8 pages, whose
-  // widening sets the pace, the turns only cost: 545 against 474 us).
+  // (1478 against 1257 us for a prompt piece at 32K; with int8 pages, whose
+  // widening sets the pace, the turns only cost: 747 against 656 us).
   static __device__ bool issue(const ChunkArgs& a, M& m, uint32_t smem, uint32_t tmem, int t) {
     const auto wait = [&](uint64_t* bar, uint32_t phase) {  // the whole warp goes on, or none of it
       return __all_sync(0xffffffffu, Waiter{a.err}(bar, phase)) != 0;
@@ -224,7 +229,8 @@ struct Kernel {
 #pragma unroll
       for (int i = 0; i < kTile / 32; ++i) {
         const int ks = half * (kTile / 32) + i;
-        mma_ts(tO, tS + 64 * half + 8 * i, v + ks * (16 * 128 >> 4), idO, acc || ks > 0);
+        mma_ts(tO, tS + 64 * half + 16 * i, v + ks * (16 * 128 >> 4), idO, acc || ks > 0);
+        if (PARTS == 2) mma_ts(tO, tS + 64 * half + 16 * i + 8, v + ks * (16 * 128 >> 4), idO, true);
       }
     };
     SegIter it(a.sh, m.plan);
@@ -578,28 +584,33 @@ struct Kernel {
         uint64_t l0 = f32x2(0.f, 0.f), l1 = l0;
         if (masked) tmem_wait_st();
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (q == 1) tmem_wait_ld();
-          uint32_t w[16];
+        for (int q = 0; q < 4; ++q) {
+          // 16 logits at a time: the parts of their P go over them, the upper
+          // 32 are read again meanwhile
+          uint32_t w[8 * PARTS];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t z = f32x2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+          for (int i = 0; i < 8; ++i) {
+            const int e0 = 16 * (q & 1) + 2 * i;
+            const uint64_t z = f32x2(__uint_as_float(x[e0]), __uint_as_float(x[e0 + 1]));
             uint64_t mul = sc2;
-            if constexpr (I8) mul = *reinterpret_cast<const uint64_t*>(ks + 32 * q + 2 * i);
+            if constexpr (I8) mul = *reinterpret_cast<const uint64_t*>(ks + 16 * q + 2 * i);
             const float2 e = unpack_f32x2(fma_f32x2(z, mul, nm));
             float2 p = make_float2(ex2(e.x), ex2(e.y));
             if (i & 1) l1 = add_f32x2(l1, f32x2(p.x, p.y)); else l0 = add_f32x2(l0, f32x2(p.x, p.y));
             if constexpr (I8) {
-              const float2 vs = *reinterpret_cast<const float2*>(&m.scales[stage][1][h * kHalf + 32 * q + 2 * i]);
+              const float2 vs = *reinterpret_cast<const float2*>(&m.scales[stage][1][h * kHalf + 16 * q + 2 * i]);
               p.x *= vs.x;
               p.y *= vs.y;
             }
             w[i] = pack2<TQ>(p.x, p.y);
+            if constexpr (PARTS == 2) {  // what the rounding left
+              const float2 hi = unpack2f<TQ>(w[i]);
+              w[8 + i] = pack2<TQ>(p.x - hi.x, p.y - hi.y);
+            }
           }
-          // P of the half goes over its own first 32 logits: these are in
-          // registers, and the others are read before the second store
-          if (q == 0) tmem_ld32(x, tS + 32);
-          tmem_st16(tS + 16 * q, w);
+          if (q == 1 || q == 2) tmem_wait_ld();
+          if constexpr (PARTS == 2) tmem_st16(tS + 16 * q, w); else tmem_st8(tS + 16 * q, w);
+          if (q < 2) tmem_ld16(x + 16 * q, tS + 32 + 16 * q);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -738,9 +749,9 @@ struct Kernel {
   }
 };
 
-template <typename T, typename TQ, int D>
+template <typename T, typename TQ, int D, int PARTS>
 __global__ void __launch_bounds__(768, 1) k_chunk(const __grid_constant__ ChunkArgs a) {
-  using K = Kernel<T, TQ, D>;
+  using K = Kernel<T, TQ, D, PARTS>;
   using Lay = typename K::Lay;
   using M = typename K::M;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -817,11 +828,11 @@ int part_rows(const spg_params& p, int total_q) {
   return static_cast<int>(std::min<long long>(kItemRows, rows));
 }
 
-template <typename T, typename TQ, int D>
+template <typename T, typename TQ, int D, int PARTS>
 cudaError_t chunk_typed(const spg_params& p, ChunkArgs& a, const void* q, cudaStream_t st) {
-  using K = Kernel<T, TQ, D>;
+  using K = Kernel<T, TQ, D, PARTS>;
   if (!make_q_tmap(&a.tmq, q, p, a.sh.total_q, kTile)) return cudaErrorNotSupported;
-  const auto kern = k_chunk<T, TQ, D>;
+  const auto kern = k_chunk<T, TQ, D, PARTS>;
   const size_t smem = 1024 + K::Lay::misc + sizeof(typename K::M);
   const cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
@@ -836,8 +847,8 @@ size_t chunk_workspace_bytes(const spg_params& p, int total_q) {
 }
 
 cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_pool, const void* v_pool,
-                         const void* k_scale, const void* v_scale, void* out, float* lse, void* ws,
-                         cudaStream_t stream) {
+                         const void* k_scale, const void* v_scale, void* out, float* lse, int parts,
+                         void* ws, cudaStream_t stream) {
   ChunkArgs a{};
   a.k_pool = k_pool;
   a.v_pool = v_pool;
@@ -864,8 +875,14 @@ cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_
   a.n_phys = p.num_phys_pages;
   a.part_rows = part_rows(p, r.total_q);
   a.scale_log2 = (p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.head_dim))) * kLog2e;
-#define SPG_CHUNK(T, TQ) \
-  return p.head_dim == 128 ? chunk_typed<T, TQ, 128>(p, a, r.q, stream) : chunk_typed<T, TQ, 64>(p, a, r.q, stream)
+#define SPG_CHUNK(T, TQ)                                                     \
+  do {                                                                       \
+    if (parts == 1)                                                          \
+      return p.head_dim == 128 ? chunk_typed<T, TQ, 128, 1>(p, a, r.q, stream) \
+                               : chunk_typed<T, TQ, 64, 1>(p, a, r.q, stream); \
+    return p.head_dim == 128 ? chunk_typed<T, TQ, 128, 2>(p, a, r.q, stream) \
+                             : chunk_typed<T, TQ, 64, 2>(p, a, r.q, stream); \
+  } while (0)
   if (p.kv_dtype == SPG_F16) SPG_CHUNK(__half, __half);
   if (p.kv_dtype == SPG_BF16) SPG_CHUNK(__nv_bfloat16, __nv_bfloat16);
   if (p.q_dtype == SPG_F16) SPG_CHUNK(int8_t, __half);

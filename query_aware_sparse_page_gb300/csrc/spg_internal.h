@@ -132,7 +132,7 @@ cudaError_t launch_rope_append(const spg_params& p, const spg_rope* rope, const 
                                int32_t* err, cudaStream_t stream);
 cudaError_t launch_chunk(const spg_params& p, const ChunkRows& r, const void* k_pool,
                          const void* v_pool, const void* k_scale, const void* v_scale, void* out,
-                         float* lse, void* ws, cudaStream_t stream);
+                         float* lse, int parts, void* ws, cudaStream_t stream);
 // the whole workspace of a chunk of total_q rows: the common one, then launch_chunk's
 size_t chunk_workspace_bytes(const spg_params& p, int total_q);
 cudaError_t launch_mass(const spg_params& p, const ChunkRows& r, const void* k_pool,

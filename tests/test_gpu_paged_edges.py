@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import paged_ref as R
-from test_gpu_paged import Run, check_chunk, close, dev, host
+from test_gpu_paged import RAGGED, SHAPES, Run, check_chunk, close, dev, host
 
 pytestmark = pytest.mark.gpu
 
@@ -144,6 +144,62 @@ def test_chunk_one_token_above_a_long_cache(spg, kv, gap):
     assert r.err() == 0
     out, tol = wide_tolerance(c)
     close(r.out, out, tol, "out")
+
+
+# ---- chunk attention: the parts of a weight -------------------------------------------------------
+
+
+@pytest.fixture
+def one_part(spg):
+    spg.spg_set_chunk_parts(1)
+    yield
+    spg.spg_set_chunk_parts(2)
+
+
+def equal_tail(kv, q, gap, new, hq, d):
+    """One token `gap` above 499 of exactly equal logits: every weight of the tail is rounded in the same direction."""
+    c, first = sink_chunk(kv, q, gap, lambda n, g: torch.full((n,), 0.01), new=new, L=500, S=16, hq=hq, d=d)
+    c.q[..., 1:] = 0
+    return c
+
+
+@pytest.mark.parametrize("new, hq, d", [(1, 2, 128), (3, 8, 64), (140, 2, 128)])
+@pytest.mark.parametrize("kv, q", [("f16", "f16"), ("bf16", "bf16"), ("i8", "f16"), ("i8", "bf16")])
+def test_chunk_weights_are_not_rounded_to_16_bits(spg, kv, q, new, hq, d):
+    """Off by the output's rounding e |o|, that of a weight's second part e e A, and sums of L terms in 32 bits."""
+    e = torch.finfo(R.DT[q]).eps / 2
+    for gap in (1.7, 1.9, 2.0, 2.1, 2.2, 2.35):
+        c = equal_tail(kv, q, gap, new, hq, d)
+        r = Run(spg, c)
+        r.chunk()
+        assert r.err() == 0
+        out = wide_tolerance(c)[0]
+        _, size = c.logits(0, 0, 0)
+        dz = float(d * 2.0 ** -24 * size.max() + 8 * 2.0 ** -24 * 4)
+        v = c.tokens(c.v_pool, c.v_scale, 0, 0)
+        assert bool((v >= 0).all())  # A = o
+        tol = (e + e * e + 2 * dz + 2 * 500 * 2.0 ** -24) * out.abs() + (2.0 ** -25 if q == "f16" else 0.0)
+        close(r.out, out, tol, f"out at {gap}")
+
+
+@pytest.mark.parametrize("lens, new, pad", RAGGED)
+@pytest.mark.parametrize("hq, hkv, d, S, kv, q", SHAPES)
+def test_chunk_attention_with_one_part(spg, one_part, hq, hkv, d, S, kv, q, lens, new, pad):
+    r = Run(spg, R.Chunk(hq, hkv, d, S, kv, q, lens, new, pad_rows=pad))
+    r.chunk()
+    assert r.err() == 0
+    check_chunk(r)
+
+
+@pytest.mark.parametrize("q", ["f16", "bf16"])
+@pytest.mark.parametrize("gap", [0.0, 12.0])
+@pytest.mark.parametrize("scales", list(SCALES))
+def test_chunk_int8_value_scales_with_one_part(spg, one_part, scales, gap, q):
+    test_chunk_int8_value_scales(spg, scales, gap, q)
+
+
+def test_chunk_nan_rows_with_one_part(spg, one_part):
+    test_chunk_nan_rows(spg, "f16")
 
 
 # ---- rows that hold a NaN ------------------------------------------------------------------------

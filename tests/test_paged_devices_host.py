@@ -75,3 +75,11 @@ def test_a_workspace_on_the_host_is_refused(spg, call):
     for ws, dev in ((On(-1, torch.uint8, 1), 0), (On(-1, torch.uint8, 1), -1), (None, 0)):
         with pytest.raises(ValueError):
             getattr(spg, call)(**MORE.get(call, {}), p=p, ws=ws, **{n: On(dev, *s) for n, s in CALLS[call].items()})
+
+
+def test_chunk_parts_are_one_or_two(spg):
+    for bad in (0, 3, -1):
+        with pytest.raises(spg.SpgError):
+            spg.spg_set_chunk_parts(bad)
+    spg.spg_set_chunk_parts(1)
+    spg.spg_set_chunk_parts(2)
