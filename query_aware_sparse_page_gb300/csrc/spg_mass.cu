@@ -16,7 +16,7 @@
 // item leaves its 256 sums in the workspace, and the part that arrives last
 // adds them in order.
 //
-// Measured (GB300): 2048 rows over 32K, GQA 32/8, 577 to 609 us, 0.9 PFLOP/s
+// Measured (GB300): 2048 rows over 32K, GQA 32/8, 606 to 618 us, 0.87 PFLOP/s
 // of 1.90.  A summing warp takes 1770 cycles for its 128 columns and 600 to hand
 // the accumulator back, against 1024 of products for both tiles.  Four
 // summing warpgroups instead of two, half the columns each, took 913 us (the
