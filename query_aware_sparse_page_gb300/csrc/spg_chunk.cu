@@ -46,6 +46,7 @@
 // into the swizzled tiles: pages of 16 tokens are too small for TMA (24 tile
 // copies per step kept its unit busy for 3200 cycles, 1.5 times what the
 // products take), and tokens that are not there become zeros on the way.
+// Larger pages take the same path; TMA was not timed with them.
 // int8 codes land in the upper half of their tile's own space and are widened
 // in place to exact 16-bit values; the key scales then multiply the logits
 // and the value scales the probabilities.  What enters the product is p times

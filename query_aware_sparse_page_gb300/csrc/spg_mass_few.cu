@@ -289,7 +289,8 @@ cudaError_t few_typed(const spg_params& p, FewArgs& a, const void* k_pool, cudaS
   if (!make_kv_tmap(&a.tmk, k_pool, p.kv_dtype, rows, D, p.page_size, &whole)) return cudaErrorNotSupported;
   a.whole_page = whole ? 1 : 0;
   const size_t page = static_cast<size_t>(p.page_size) * D * sizeof(T);
-  // a multiple of the summing warps: each slot has one owner
+  // a multiple of the summing warps: each slot has one owner (pages of 8 KB and
+  // more leave it one slot, whose next page is on its way only after the sums)
   a.slots = std::max(kWarps, std::min<int>(kMaxSlots, static_cast<int>(kRingBytes / page)) / kWarps * kWarps);
   const size_t smem = 1024 + a.slots * (page + (sizeof(T) == 1 ? 2 * p.page_size : 0));
   const auto kern = k_mass_few<T, TQ, D>;
