@@ -47,9 +47,9 @@ STEP_SOURCES = ("spg_append.cuh", "spg_attn_core.cuh", "spg_common.cuh", "spg_fu
                 "spg_select_core.cuh", "spg_tma.cu")
 NCU_TRAFFIC = {
     # workload: (DRAM bytes of one launch, code hash, kernel)
-    "llama2-7b-mha-32k": (67_619_840, "f4e51227135ce389a840a687fe5a684070612805dcffdd0ea03c4fb0d0ba8bc8", "k_fused"),
-    "long-scan-b4-128k": (204_981_760, "f4e51227135ce389a840a687fe5a684070612805dcffdd0ea03c4fb0d0ba8bc8", "k_fused"),
-    "sals-int8-b16-10k-4x": (100_395_264, "f4e51227135ce389a840a687fe5a684070612805dcffdd0ea03c4fb0d0ba8bc8", "k_fused"),
+    "llama2-7b-mha-32k": (67_643_136, "12213080c09be11eb4c9bb6ec5fab787dca4f695b378f79d23cb60e97be57597", "k_fused"),
+    "long-scan-b4-128k": (205_023_488, "12213080c09be11eb4c9bb6ec5fab787dca4f695b378f79d23cb60e97be57597", "k_fused"),
+    "sals-int8-b16-10k-4x": (100_351_232, "12213080c09be11eb4c9bb6ec5fab787dca4f695b378f79d23cb60e97be57597", "k_fused"),
 }
 
 
