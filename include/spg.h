@@ -428,6 +428,98 @@ spg_status paged_cache_evict(const spg_params* p, const float* mass, int32_t kee
                              int32_t* new_lens, float* mass_out, void* ws, size_t ws_bytes,
                              spg_stream_t stream);
 
+/* ---- attention over a paged cache of latent vectors -------------------------
+ *
+ * Every cached token is one vector of latent_dim channels, from which each
+ * head's keys and values would come by that head's own matrices, and one
+ * rotary key shared by all heads (r = latent_dim, dr = rope_dim, dn = nope_dim,
+ * dv = v_dim, H = num_heads):
+ *   key of head h   [ W_uk[h] c_t | k_t ],   W_uk[h] [dn][r]
+ *   value of head h   W_uv[h] c_t,           W_uv[h] [dv][r]
+ * Nothing is expanded: W_uk goes over to the query (latent_absorb), attention
+ * runs on the cached vectors themselves (paged_latent_attention) and W_uv is
+ * applied to its result (latent_project).  The chunk of new tokens is ragged
+ * as in paged_chunk_attention, with the same q_start, seq_lens, page_table and
+ * device-detected faults.
+ *   pool         [P_phys][S][r + dr]   dtype: the latent vector, then the
+ *                                      rotary key
+ *   q            [total_q][H][dn + dr] dtype: the projected queries
+ *   q_lat        [total_q][H][r + dr]  dtype: the absorbed queries, then the
+ *                                      rotated ones
+ *   w_kv         [H][dn + dv][r]       dtype: W_uk[h], then W_uv[h]
+ *   o_lat        [total_q][H][r]       dtype
+ *   out          [total_q][H][dv]      dtype
+ * All inputs must be finite; slots of the pool past seq_lens may hold anything. */
+typedef struct spg_latent_params {
+  int32_t batch;             /* B >= 1 */
+  int32_t num_heads;         /* H: 1 to 1024 */
+  int32_t latent_dim;        /* r: a multiple of 64; 256 and 512 are built */
+  int32_t rope_dim;          /* dr: a multiple of 16; 64 is built */
+  int32_t nope_dim;          /* dn: a multiple of 16; 64 and 128 are built */
+  int32_t v_dim;             /* dv: a multiple of 16; 64 and 128 are built */
+  int32_t page_size;         /* S: 16, 32, 64 or 128 tokens (8 is valid, not built) */
+  int32_t num_phys_pages;    /* P_phys */
+  int32_t max_pages_per_seq; /* MP: columns of page_table */
+  int32_t dtype;             /* SPG_F16 or SPG_BF16, of every 16-bit tensor here (SPG_I8 is
+                                valid, not built) */
+  float softmax_scale;       /* 0 => 1/sqrt(nope_dim + rope_dim) */
+} spg_latent_params;
+
+/* Host-only check of a parameter block: SPG_OK, SPG_EINVAL or SPG_EUNSUPPORTED. */
+spg_status spg_latent_validate(const spg_latent_params* p);
+
+/* Workspace bytes for the two paged_latent_* entry points with these
+ * parameters and chunks of up to total_q rows.  The workspace keeps nothing
+ * between calls but the error word (see spg_read_device_error), so one that is
+ * large enough serves any parameters.  Host only. */
+spg_status spg_latent_workspace_size(const spg_latent_params* p, int32_t total_q, size_t* bytes);
+
+/* A chunk's latent vectors and rotary keys into the cache, and the rotated part
+ * of its queries beside the absorbed one.  Per row t, in fp32 and rounded once:
+ *   pool row  [ c / sqrt(mean(c^2) + eps) * norm_weight | k_pe rotated ]
+ *   q_lat[t][h][r:] = q[t][h][dn:] rotated
+ *   c, k_pe      [total_q] rows of r and dr channels, c_stride and kpe_stride
+ *                elements apart (multiples of 8: they may be slices of one
+ *                projection's output)
+ *   norm_weight  [r] dtype, or NULL: c is written as it is
+ *   eps          >= 0, finite
+ *   q            rows q_stride elements apart (a multiple of 8); q and q_lat
+ *                may both be NULL, and must not overlap
+ *   rope, positions  as in paged_rope_append, over the dr channels (rot_dim 0
+ *                or a multiple of 16 up to dr; NULL leaves k_pe and q as they are)
+ * Channels [0, r) of q_lat are left to latent_absorb. */
+spg_status paged_latent_append(const spg_latent_params* p, const spg_rope* rope, int32_t total_q,
+                               const void* c, int64_t c_stride, const void* k_pe,
+                               int64_t kpe_stride, const void* norm_weight, float eps,
+                               const void* q, int64_t q_stride, const int32_t* q_start,
+                               const int32_t* positions, const int32_t* page_table,
+                               const int32_t* seq_lens, void* pool, void* q_lat, void* ws,
+                               size_t ws_bytes, spg_stream_t stream);
+
+/* q_lat[t][h][0:r] = W_uk[h]^T q[t][h][0:dn] for every row t < total_q, sums in
+ * fp32 and rounded once; channels [r, r + dr) of q_lat are left as they are.
+ *   q            rows q_stride elements apart (a multiple of 8); must not overlap q_lat */
+spg_status latent_absorb(const spg_latent_params* p, int32_t total_q, const void* q,
+                         int64_t q_stride, const void* w_kv, void* q_lat, spg_stream_t stream);
+
+/* out[t][h] = W_uv[h] o_lat[t][h] for every row t < total_q, sums in fp32 and
+ * rounded once.  out must not overlap o_lat. */
+spg_status latent_project(const spg_latent_params* p, int32_t total_q, const void* o_lat,
+                          const void* w_kv, void* out, spg_stream_t stream);
+
+/* Causal attention of a chunk over the cache its tokens are already in: row i
+ * of sequence b attends the tokens t <= seq_lens[b] - n_b + i,
+ *   z = softmax_scale * q_lat[i][h] . pool[t],  o_lat[i][h] = sum softmax(z)_t c_t
+ *   lse          [total_q][H] fp32 natural-log log-sum-exp (may be NULL)
+ * A row that sees no token (its pages are bad) gets o_lat = 0 and lse = -inf.
+ * Rows past q_start[B] are neither read for a result nor written.  Logits,
+ * softmax statistics and sums in fp32; probabilities enter the second product
+ * as in paged_chunk_attention (spg_set_chunk_parts). */
+spg_status paged_latent_attention(const spg_latent_params* p, int32_t total_q, const void* q_lat,
+                                  const int32_t* q_start, const void* pool,
+                                  const int32_t* page_table, const int32_t* seq_lens, void* o_lat,
+                                  float* lse, void* ws, size_t ws_bytes, spg_stream_t stream);
+
 /* Bytes of the library-owned scratch array behind
  * sparse_decode_attention_noalloc (16 MiB).  A call needs
  * 256 + 4 * units + 512 * rows * (head_dim + 2) bytes (each region rounded

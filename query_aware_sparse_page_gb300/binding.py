@@ -95,13 +95,39 @@ def make_rope(rot_dim=0, layout="half", base=10000.0, scaling="none", factor=1.0
     return spg_rope(int(rot_dim), lay, sc, int(orig_len), float(base), float(factor))
 
 
+class spg_latent_params(ctypes.Structure):
+    _fields_ = [
+        ("batch", c_int32),
+        ("num_heads", c_int32),
+        ("latent_dim", c_int32),
+        ("rope_dim", c_int32),
+        ("nope_dim", c_int32),
+        ("v_dim", c_int32),
+        ("page_size", c_int32),
+        ("num_phys_pages", c_int32),
+        ("max_pages_per_seq", c_int32),
+        ("dtype", c_int32),
+        ("softmax_scale", c_float),
+    ]
+
+    def __repr__(self):
+        return "spg_latent_params(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+def make_latent_params(batch, num_heads, latent_dim, page_size, num_phys_pages, max_pages_per_seq, rope_dim=64,
+                       nope_dim=128, v_dim=128, dtype="bf16", softmax_scale=0.0) -> spg_latent_params:
+    dt = _DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    return spg_latent_params(batch, num_heads, latent_dim, rope_dim, nope_dim, v_dim, page_size, num_phys_pages,
+                             max_pages_per_seq, dt, softmax_scale)
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
             f"{LIB_PATH} is not built; run query_aware_sparse_page_gb300._build.build() "
             "(nvcc for sm_103a).  There is no fallback implementation.")
     lib = ctypes.CDLL(LIB_PATH)
-    P = POINTER(spg_params)
+    P, PL = POINTER(spg_params), POINTER(spg_latent_params)
     v = c_void_p
     sigs = {
         "spg_abi_version": ([], c_int32),
@@ -129,6 +155,14 @@ def _load():
             [P, c_int32, v, v, v, v, v, v, v, v, v, c_float, v, c_size_t, v], c_int32),
         "paged_cache_evict": (
             [P, v, c_int32, c_int32, c_int32, v, v, v, v, v, v, v, v, v, v, v, c_size_t, v], c_int32),
+        "spg_latent_validate": ([PL], c_int32),
+        "spg_latent_workspace_size": ([PL, c_int32, POINTER(c_size_t)], c_int32),
+        "paged_latent_append": (
+            [PL, POINTER(spg_rope), c_int32, v, c_int64, v, c_int64, v, c_float, v, c_int64, v, v, v, v, v, v, v,
+             c_size_t, v], c_int32),
+        "latent_absorb": ([PL, c_int32, v, c_int64, v, v, v], c_int32),
+        "latent_project": ([PL, c_int32, v, v, v, v], c_int32),
+        "paged_latent_attention": ([PL, c_int32, v, v, v, v, v, v, v, v, c_size_t, v], c_int32),
         "spg_step_kernel": ([P], c_char_p),
         "spg_prefer_dense": ([P, c_int32, c_float], c_int32),
         "spg_step_launches": ([P], c_int32),
@@ -428,6 +462,88 @@ def paged_cache_evict(p, mass, keep, n_sink, n_recent, k_pool, v_pool, k_scale, 
     nl = _take(dev, "new_lens", new_lens, (p.batch,), torch.int32)
     _call(dev, LIB.paged_cache_evict, "paged_cache_evict", ws, stream, ctypes.byref(p), mi, keep, int(n_sink),
           int(n_recent), kpool, vpool, ksc, vsc, pt, dst, sl, kp, nl, mo)
+
+
+# ---- attention over a paged cache of latent vectors ----------------------------------
+def spg_latent_validate(p: spg_latent_params) -> int:
+    return LIB.spg_latent_validate(ctypes.byref(p))
+
+
+def spg_latent_workspace_size(p: spg_latent_params, total_q: int) -> int:
+    n = c_size_t(0)
+    _check(LIB.spg_latent_workspace_size(ctypes.byref(p), int(total_q), ctypes.byref(n)), "spg_latent_workspace_size")
+    return n.value
+
+
+def _take_latent(dev, p, pool, page_table, seq_lens, q_start):
+    return (_take(dev, "pool", pool, (p.num_phys_pages, p.page_size, p.latent_dim + p.rope_dim), _ELEM[p.dtype]),
+            _take(dev, "page_table", page_table, (p.batch, p.max_pages_per_seq), torch.int32),
+            _take(dev, "seq_lens", seq_lens, (p.batch,), torch.int32),
+            _take(dev, "q_start", q_start, (p.batch + 1,), torch.int32))
+
+
+def _take_2d(dev, name, t, shape, dtype):
+    """Pointer and row stride of a matrix whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(name, t, shape, dtype, dev)
+    row, one = t.stride()
+    if t.numel() and one != 1:
+        raise ValueError(f"{name}: the channels of one token have to be contiguous")
+    return t.data_ptr(), row if shape[0] > 1 else shape[1]
+
+
+def _call_rows(dev, fn, where, stream, *args):
+    """fn(*args, stream) with device `dev` current, for entry points without a workspace."""
+    if dev < 0:
+        raise ValueError("libspg takes device tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev == torch.cuda.current_device():
+        _check(fn(*args, stream), where)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream), where)
+
+
+def paged_latent_append(p, rope, c, k_pe, norm_weight, eps, q, q_start, page_table, seq_lens, pool, q_lat=None,
+                        positions=None, ws=None, stream=None):
+    dev, T, r, dr, dt = _device(ws), c.shape[0], p.latent_dim, p.rope_dim, _ELEM[p.dtype]
+    cp, cs = _take_2d(dev, "c", c, (T, r), dt)
+    kp, ks = _take_2d(dev, "k_pe", k_pe, (T, dr), dt)
+    wp = _take(dev, "norm_weight", norm_weight, (r,), dt)
+    qp, qs = _take_rows(dev, "q", q, (T, p.num_heads, p.nope_dim + dr), dt)
+    lp = _take(dev, "q_lat", q_lat, (T, p.num_heads, r + dr), dt)
+    pos = _take(dev, "positions", positions, (T,), torch.int32)
+    pl, pt, sl, st = _take_latent(dev, p, pool, page_table, seq_lens, q_start)
+    _call(dev, LIB.paged_latent_append, "paged_latent_append", ws, stream, ctypes.byref(p),
+          None if rope is None else ctypes.byref(rope), T, cp, cs, kp, ks, wp, float(eps), qp, qs, st, pos, pt, sl, pl, lp)
+
+
+def latent_absorb(p, q, w_kv, q_lat, stream=None):
+    dev, T, H, r, dt = q_lat.get_device(), q.shape[0], p.num_heads, p.latent_dim, _ELEM[p.dtype]
+    qp, qs = _take_rows(dev, "q", q, (T, H, p.nope_dim + p.rope_dim), dt)
+    wp = _take(dev, "w_kv", w_kv, (H, p.nope_dim + p.v_dim, r), dt)
+    lp = _take(dev, "q_lat", q_lat, (T, H, r + p.rope_dim), dt)
+    _call_rows(dev, LIB.latent_absorb, "latent_absorb", stream, ctypes.byref(p), T, qp, qs, wp, lp)
+
+
+def paged_latent_attention(p, q_lat, q_start, pool, page_table, seq_lens, o_lat, lse=None, ws=None, stream=None):
+    dev, T, H, r, dt = _device(ws), q_lat.shape[0], p.num_heads, p.latent_dim, _ELEM[p.dtype]
+    qp = _take(dev, "q_lat", q_lat, (T, H, r + p.rope_dim), dt)
+    op, lp = _take(dev, "o_lat", o_lat, (T, H, r), dt), _take(dev, "lse", lse, (T, H), torch.float32)
+    pl, pt, sl, st = _take_latent(dev, p, pool, page_table, seq_lens, q_start)
+    _call(dev, LIB.paged_latent_attention, "paged_latent_attention", ws, stream, ctypes.byref(p), T, qp, st, pl, pt, sl,
+          op, lp)
+
+
+def latent_project(p, o_lat, w_kv, out, stream=None):
+    dev, T, H, r, dt = out.get_device(), o_lat.shape[0], p.num_heads, p.latent_dim, _ELEM[p.dtype]
+    ip = _take(dev, "o_lat", o_lat, (T, H, r), dt)
+    wp = _take(dev, "w_kv", w_kv, (H, p.nope_dim + p.v_dim, r), dt)
+    op = _take(dev, "out", out, (T, H, p.v_dim), dt)
+    _call_rows(dev, LIB.latent_project, "latent_project", stream, ctypes.byref(p), T, ip, wp, op)
 
 
 def spg_read_device_error(ws, stream=None) -> int:

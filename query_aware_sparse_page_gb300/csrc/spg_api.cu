@@ -8,6 +8,7 @@
 
 #include "spg_common.cuh"
 #include "spg_internal.h"
+#include "spg_latent.h"
 
 namespace spg {
 
@@ -552,6 +553,12 @@ int32_t spg_step_launches(const spg_params* p) {
   // kernel past 8192 pages), attention
   return (p->selector == SPG_SEL_PROBE ? 2 : 3) + (p->max_pages_per_seq > 8192 ? 1 : 0);
 }
+
+}  // extern "C"
+
+int spg::chunk_parts() { return g_chunk_parts.load(); }
+
+extern "C" {
 
 spg_status spg_set_chunk_parts(int32_t parts) {
   if (parts != 1 && parts != 2) return SPG_EINVAL;

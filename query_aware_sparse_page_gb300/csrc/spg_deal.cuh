@@ -10,6 +10,7 @@
 //   Shape::item_steps(s, i)  steps of item i alone (every role asks at every
 //                        item's start: kept to a few instructions)
 //   Shape::kLeast        fewest steps worth a CTA of their own
+//   Shape::kMostParts   most parts an average item is split into
 //   Shape::kExtra        what an item costs beside its steps, in steps: it
 //                        follows them in the count (steps() holds it)
 // An item that crosses a border is worked on in parts; the CTAs of the parts
@@ -22,9 +23,9 @@
 namespace spg {
 
 constexpr int kMaxCtas = 160;   // shares of a plan (one per SM)
-constexpr int kMaxParts = 32;   // most parts an average item is split into
 
 struct ChunkShape {
+  static constexpr int kMostParts = 32;
   const int32_t *q_start, *seq_lens;
   int B, Hkv, g_log2, total_q, max_tokens;  // 2^g_log2 query heads per kv-head
   __device__ ChunkSeq seq(int b, int32_t& bad) const { return chunk_seq(q_start, seq_lens, b, total_q, max_tokens, bad); }
@@ -36,9 +37,10 @@ struct Plan {
   int ctas, b, h, item;
 };
 
-// one whole warp
+// one whole warp; the share of CTA c of n_ctas
 template <typename Shape>
-__device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane) {
+__device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, int c = static_cast<int>(blockIdx.x),
+                          int n_ctas = static_cast<int>(gridDim.x)) {
   long long total = 0, items = 0;
   int32_t bad = 0;
   for (int b = lane; b < sh.B; b += 32) {
@@ -55,10 +57,9 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane) {
   if (bad && blockIdx.x == 0) record_error(err, bad);
   Plan p{};
   p.total = total;
-  long long n = min(static_cast<long long>(gridDim.x), (total + Shape::kLeast - 1) / Shape::kLeast);
-  n = min(n, items * kMaxParts);
+  long long n = min(static_cast<long long>(n_ctas), (total + Shape::kLeast - 1) / Shape::kLeast);
+  n = min(n, items * Shape::kMostParts);
   p.ctas = static_cast<int>(n);
-  const int c = blockIdx.x;
   if (c >= n) {
     if (lane == 0) *out = p;  // lo = hi = 0: nothing to do
     return;

@@ -1,0 +1,196 @@
+// A chunk's latent vectors and rotary keys into the pages of the cache, and
+// the rotated part of its queries beside the absorbed one, one launch
+// (paged_latent_append).
+//
+//   pool row = [ c * (mean(c^2) + eps)^-1/2 * w | k_pe turned ]
+//   q_lat[h][r:] = q[h][dn:] turned
+//
+// The turn is that of paged_rope_append: the angle as a 64-bit fraction of a
+// turn, its upper 32 bits to sincospif.
+//
+// Bound by bytes, and for one token per sequence by latency: nothing here
+// waits for another warp.  A CTA takes a token; its first warp has the latent
+// vector (two or four 16-byte pieces of it a lane, one shuffle sum), the
+// others 16 channels of a head at a time.  Every warp finds the token's page
+// by itself and has the 32 pairs' cos and sin in its lanes.
+#include <cmath>
+
+#include "spg_chunk_common.cuh"
+#include "spg_latent.h"
+
+namespace spg {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRope = 64, kPairs = kRope / 2;
+
+struct AppendArgs {
+  unsigned long long turns[kPairs];  // angle per position, 64-bit fraction of a turn
+  const void *c, *k_pe, *w, *q;
+  int64_t c_stride, kpe_stride, q_stride;
+  const int32_t *q_start, *positions, *page_table, *seq_lens;
+  void *pool, *q_lat;
+  int32_t* err;
+  float mscale, eps;
+  int B, H, S, MP, n_phys, total_q, rot, nope;
+};
+
+template <typename T, int R, bool HALF>
+__global__ void __launch_bounds__(kThreads) k_latent_append(const __grid_constant__ AppendArgs a) {
+  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  // the sequence with q_start[b] <= t < q_start[b + 1]; an unsorted q_start ends at some b, checked below
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.q_start[mid] <= t) lo = mid; else hi = mid;
+  }
+  int32_t bad = 0;
+  // empty sequences before the row's own share its start: the last of them is the one found
+  const ChunkSeq s = chunk_seq(a.q_start, a.seq_lens, lo, a.total_q, a.MP * a.S, bad);
+  int pos = -1, page = -1;
+  if (t >= s.start && t < s.start + s.n) {
+    pos = s.pos0 + t - s.start;
+    page = a.page_table[static_cast<size_t>(lo) * a.MP + pos / a.S];
+    if (page < 0 || page >= a.n_phys) {
+      bad |= SPG_DEVERR_PAGE_ID;
+      page = -1;
+    }
+  }
+  if (bad && threadIdx.x == 0) record_error(a.err, bad);
+  pdl_trigger();
+  if (pos < 0) return;  // a row of no sequence
+  T* const row = page < 0 ? nullptr : static_cast<T*>(a.pool) + (static_cast<size_t>(page) * a.S + pos % a.S) * (R + kRope);
+
+  if (warp == 0) {
+    // ---- the latent vector ----
+    constexpr int kPieces = R / 256;  // 16-byte pieces of a lane
+    const T* src = static_cast<const T*>(a.c) + t * a.c_stride;
+    uint4 u[kPieces];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) u[i] = *reinterpret_cast<const uint4*>(src + 8 * (lane + 32 * i));
+    if (a.w) {
+      float x[8], g[8];
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        unpack8<T>(u[i], x);
+        float q = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
+        sum += q;
+      }
+      const float f = rsqrtf(warp_sum(sum) * (1.f / R) + a.eps);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        unpack8<T>(u[i], x);
+        unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.w) + 8 * (lane + 32 * i)), g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * f * g[e];
+        u[i] = pack8<T>(x);
+      }
+    }
+    if (row) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint4*>(row + 8 * (lane + 32 * i)) = u[i];
+    }
+    return;
+  }
+
+  // ---- the rotary key and the queries' rotated parts: four items of 16 channels a row ----
+  const unsigned long long at = static_cast<unsigned long long>(static_cast<long long>(a.positions ? a.positions[t] : pos));
+  const unsigned long long f = at * a.turns[lane];
+  // nearest 2^-32 of a turn, as half-turns in [-1, 1)
+  const int w = static_cast<int>(static_cast<uint32_t>((f + 0x80000000ull) >> 32));
+  float sn, cs;
+  sincospif(static_cast<float>(w) * 4.656612873077393e-10f, &sn, &cs);
+  sn *= a.mscale;
+  cs *= a.mscale;
+  const int items = 4 * (a.q ? a.H + 1 : 1), rot_items = a.rot / 16;
+  for (int i0 = threadIdx.x - 32; i0 - lane < items; i0 += kThreads - 32) {
+    const bool live = i0 < items;
+    const int i = live ? i0 : 0, h = (i >> 2) - 1, j = i & 3;  // h = -1: the key
+    int c0 = 2 * j, c1 = 2 * j + 1;  // the item's two 16-byte pieces
+    if (HALF && j < rot_items) {
+      c0 = j;
+      c1 = j + rot_items;
+    }
+    const T* src = h < 0 ? static_cast<const T*>(a.k_pe) + t * a.kpe_stride
+                         : static_cast<const T*>(a.q) + t * a.q_stride + static_cast<size_t>(h) * (a.nope + kRope) + a.nope;
+    uint4 w0 = *reinterpret_cast<const uint4*>(src + 8 * c0), w1 = *reinterpret_cast<const uint4*>(src + 8 * c1);
+    float x[8], y[8];
+    unpack8<T>(w0, x);
+    unpack8<T>(w1, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float c = __shfl_sync(0xffffffffu, cs, 8 * j + e), n = __shfl_sync(0xffffffffu, sn, 8 * j + e);
+      if (j < rot_items) {
+        // half: (x[e], y[e]); interleaved: neighbours within a piece
+        float& p = HALF ? x[e] : (e < 4 ? x[2 * e] : y[2 * e - 8]);
+        float& q = HALF ? y[e] : (e < 4 ? x[2 * e + 1] : y[2 * e - 7]);
+        const float u = p * c - q * n, v = q * c + p * n;
+        p = u;
+        q = v;
+      }
+    }
+    T* dst = h < 0 ? (row ? row + R : nullptr)
+                   : static_cast<T*>(a.q_lat) + (static_cast<size_t>(t) * a.H + h) * (R + kRope) + R;
+    if (live && dst) {
+      *reinterpret_cast<uint4*>(dst + 8 * c0) = pack8<T>(x);
+      *reinterpret_cast<uint4*>(dst + 8 * c1) = pack8<T>(y);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t append_typed(const spg_latent_params& p, const AppendArgs& a, bool half, cudaStream_t st) {
+  const dim3 grid(a.total_q), block(kThreads);
+  if (p.latent_dim == 512)
+    return half ? launch_pdl(k_latent_append<T, 512, true>, grid, block, 0, st, a)
+                : launch_pdl(k_latent_append<T, 512, false>, grid, block, 0, st, a);
+  return half ? launch_pdl(k_latent_append<T, 256, true>, grid, block, 0, st, a)
+              : launch_pdl(k_latent_append<T, 256, false>, grid, block, 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const spg_latent_params& p, const spg_rope* rope, const LatentAppend& r, int32_t* err,
+                                 cudaStream_t stream) {
+  AppendArgs a{};
+  a.mscale = 1.f;
+  bool half = true;
+  if (rope) {
+    double inv[kPairs], m = 1.0;
+    if (!rope_freqs(*rope, kRope, inv, &m)) return cudaErrorInvalidValue;
+    a.rot = rope->rot_dim == 0 ? kRope : rope->rot_dim;
+    for (int i = 0; i < a.rot / 2; ++i)
+      a.turns[i] = static_cast<unsigned long long>(std::ldexp(inv[i] / 6.283185307179586476925, 64));
+    a.mscale = static_cast<float>(m);
+    half = rope->layout == SPG_ROPE_HALF;
+  }
+  a.c = r.c;
+  a.k_pe = r.k_pe;
+  a.w = r.norm_weight;
+  a.q = r.q;
+  a.c_stride = r.c_stride;
+  a.kpe_stride = r.kpe_stride;
+  a.q_stride = r.q_stride;
+  a.q_start = r.q_start;
+  a.positions = r.positions;
+  a.page_table = r.page_table;
+  a.seq_lens = r.seq_lens;
+  a.pool = r.pool;
+  a.q_lat = r.q_lat;
+  a.err = err;
+  a.eps = r.eps;
+  a.B = p.batch;
+  a.H = p.num_heads;
+  a.S = p.page_size;
+  a.MP = p.max_pages_per_seq;
+  a.n_phys = p.num_phys_pages;
+  a.total_q = r.total_q;
+  a.nope = p.nope_dim;
+  return p.dtype == SPG_F16 ? append_typed<__half>(p, a, half, stream) : append_typed<__nv_bfloat16>(p, a, half, stream);
+}
+
+}  // namespace spg

@@ -1,0 +1,772 @@
+// Attention over a paged cache of latent vectors (paged_latent_attention), on
+// the tcgen05 tensor cores.
+//
+// Keys and values of all heads are the cached rows themselves: row t of the
+// pool is [c_t | k_t], a key in its whole length and a value in its first R
+// channels.  So a row (new token, head) of the queries is one of up to 64 that
+// share every cached row, and a step of 64 tokens is read once for both
+// products, both transposed:
+//   S^T = KV Q^T     64 tokens (M) x up to 64 rows (N), K = R + 64
+//   P^T = exp2(scale S^T - m)   by the softmax warps
+//   O^T += C^T P^T   R / 128 times 128 channels (M) x rows (N), K = 64 tokens
+// N follows the rows there are (one head's token: 16), which is what makes few
+// heads cheap: with the rows as M every step would take the time of 64 or 128
+// of them, and 128 rows' O alone would fill TMEM.
+//
+// A step lies in shared memory as groups of 8 tokens, [group][64-channel
+// block][8 rows of 128 bytes]: one TMA copy per page (of any size) brings it
+// in, and the same bytes are the K-major operand of the first product and the
+// MN-major one of the second.  The rotary block is no value; once S is done
+// P^T takes its place, and what P's rounding to 16 bits left (chunk_parts 2)
+// stands in a buffer of its own, as a second operand.
+//
+// The running maximum m of a row is only raised when a (base 2) logit exceeds
+// it by more than kTop, and then set kHead below that logit (as in the chunk
+// attention): a step only asks whether any logit does, all tokens' threads
+// together, and the sums l stay apart per thread until the end.
+//
+// Steps of all items (up to 64 rows of a sequence) are dealt out to the CTAs
+// in equal contiguous shares.  Items that cross a border leave (m, l, O) of
+// their parts in the workspace, and a second launch joins them, the work shared
+// out to the CTAs that had the parts.  With more than 64 rows per sequence
+// neighbouring CTAs take the two halves of 128 rows over the same steps, so
+// that the second reads them from L2.
+#include <algorithm>
+#include <cmath>
+
+#include "spg_deal.cuh"
+#include "spg_latent.h"
+#include "spg_tcgen05.cuh"
+
+namespace spg {
+namespace {
+
+constexpr int kRows = 64;   // rows of a CTA: columns of S^T and O^T
+constexpr int kStep = 64;   // tokens of a step
+constexpr int kRope = 64;
+constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O^T: R / 128 times 64 columns, then two S^T of 64
+constexpr float kUnset = -1e30f;  // m of a row that has seen nothing
+constexpr float kHead = 7.f, kTop = 15.f;  // the weights of a row are at most 2^15, under fp16's 65504
+
+// sum of floor((a i + b) / m) over 0 <= i < n, by the steps of Euclid's algorithm
+__device__ inline unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a, unsigned long long b) {
+  unsigned long long sum = 0;
+  while (n > 0) {
+    if (a >= m) {
+      sum += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const unsigned long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const unsigned long long t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// ---- the plan: items of 64 rows (128 for a pair of CTAs) -------------------------------
+struct LatentItems : ChunkShape {
+  static constexpr int kLeast = 2, kExtra = 3, kMostParts = kMaxCtas;
+  int H, rows_log2;
+  __device__ int items(const ChunkSeq& s) const {
+    return static_cast<int>((static_cast<unsigned>(s.n) * H + (1u << rows_log2) - 1) >> rows_log2);
+  }
+  // one past the last token that item i sees
+  __device__ int seen(const ChunkSeq& s, int i) const {
+    const unsigned last = (static_cast<unsigned>(i + 1) << rows_log2) - 1;
+    return s.pos0 + min(s.n, static_cast<int>(last / H) + 1);
+  }
+  __device__ int item_steps(const ChunkSeq& s, int i) const { return (seen(s, i) + kStep - 1) / kStep; }
+  // Item i but the last sees pos0 + floor((rows (i + 1) - 1) / H) + 1 tokens,
+  // floor((rows i + H (pos0 + 64) + rows - 1) / (64 H)) steps; the last ends with the sequence.
+  __device__ long long steps(const ChunkSeq& s, int m) const {
+    const int n = items(s);
+    long long sum = static_cast<long long>(m) * kExtra;
+    const int full = min(m, n - 1);
+    const unsigned long long rows = 1u << rows_log2;
+    if (full > 0)
+      sum += floor_sum(full, static_cast<unsigned long long>(kStep) * H, rows,
+                       static_cast<unsigned long long>(H) * (s.pos0 + kStep) + rows - 1);
+    if (m == n && n > 0) sum += (s.L + kStep - 1) / kStep;
+    return sum;
+  }
+};
+
+// A CTA's part of an item: its rows and steps.  A pair of CTAs takes the two
+// halves of the rows; an item of at most 64 rows is taken whole by one of them,
+// or, when other pairs have parts of it too, in two halves of the steps.
+struct Seg : Part {
+  int row0, n_rows, half, k0_of_pair;
+  bool split;  // the result is left as a part
+};
+struct SegIter : PartIter<LatentItems> {
+  int pair, rank;
+  __device__ SegIter(const LatentItems& shape, const Plan& p, int pair_, int rank_) : PartIter(shape, p), pair(pair_), rank(rank_) {}
+  __device__ bool next(Seg& s) {
+    while (PartIter::next(s)) {
+      s.row0 = s.item << sh.rows_log2;
+      s.n_rows = min(1 << sh.rows_log2, s.sq.n * sh.H - s.row0);
+      s.split = !s.whole();
+      s.half = rank;
+      s.k0_of_pair = s.k0;
+      if (pair && s.n_rows > kRows) {
+        s.row0 += rank * kRows;
+        s.n_rows = rank == 0 ? kRows : s.n_rows - kRows;
+      } else if (pair && !s.split) {
+        if (((s.b ^ s.item) & 1) != rank) continue;
+      } else if (pair) {
+        const int mid = (s.k0 + s.k1 + 1) / 2;
+        if (rank == 0) s.k1 = mid; else s.k0 = mid;  // may leave rank 1 nothing: a part without weight
+      }
+      return true;
+    }
+    return false;
+  }
+};
+
+struct LatentArgs {
+  LatentItems sh;
+  CUtensorMap tmq, tmkv;
+  const uint8_t* pool;
+  const int32_t* page_table;
+  void* out;
+  float* lse;
+  int32_t* err;
+  float *part, *part_m, *part_l;  // [2 * CTAs][part_rows][R], [2 * CTAs][64] twice
+  int S, s_log2, MP, n_phys, part_rows, pair;
+  float scale_log2;
+};
+
+__device__ __forceinline__ int slot_of(const LatentArgs& a, int c, bool first, int half) {
+  return ((2 * c + (first ? 1 : 0)) << a.pair) + half;
+}
+
+template <int R>
+struct Layout {
+  static constexpr int NA = R / 64 + 1;              // 64-channel blocks of a cached row
+  static constexpr uint32_t kGroup = NA * 1024;      // 8 tokens (or query rows)
+  static constexpr uint32_t kStage = kStep / 8 * kGroup;
+  static constexpr int ST = R == 512 ? 2 : 4;
+  static constexpr uint32_t q_off = 0, kv_off = kRows / 8 * kGroup, lo_off = kv_off + ST * kStage, misc = lo_off + kStep * 128;
+};
+template <int ST>
+struct Misc {
+  uint64_t q_full, q_empty, full[ST], empty[ST], s_full[2], p_full[2], drain[2];
+  uint64_t live[ST];  // tokens of a step that are there
+  Plan plan;
+  uint32_t tmem;
+  int lim[kRows];             // last token a row sees
+  float top[4][kRows];        // largest logit of a step, per warp; at the end the sums
+  float factor[kRows];
+  float inv[kRows];
+};
+
+template <typename T, int R, int PARTS>
+struct Kernel {
+  using Lay = Layout<R>;
+  static constexpr int ST = Lay::ST, NA = Lay::NA;
+  using M = Misc<ST>;
+  static constexpr int kThreads = 256, kSoftmax = 128, kLoadWarp = 4, kSWarp = 5, kPvWarp = 6, kQWarp = 7;
+  static constexpr int kAhead = 2;  // steps brought into L2 before their copies
+
+  static __device__ __forceinline__ int columns(const Seg& s) { return (s.n_rows + 15) & ~15; }
+  static __device__ __forceinline__ uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
+    return instr_desc<T>(0, 0, b_mn) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+  }
+  static __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+  // ---- S^T, one warp (an elected lane issues) ----------------------------------------------
+  static __device__ bool issue_s(const LatentArgs& a, M& m, uint8_t* smem, uint32_t tmem, int rank, int lane) {
+    const auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, Waiter{a.err}(bar, phase)) != 0; };
+    const uint32_t sm = smem_u32(smem), dq = desc_k_major(sm + Lay::q_off), dk = desc_k_major(sm + Lay::kv_off);
+    uint32_t c = 0, qc = 0;
+    SegIter it(a.sh, m.plan, a.pair, rank);
+    Seg s;
+    while (uniform(it.next(s))) {
+      const int n = uniform(s.k1 - s.k0);
+      if (n == 0) continue;
+      const uint32_t id = uniform(idesc(64, columns(s), false, false));
+      if (!wait(&m.q_full, qc++)) return false;
+      for (int i = 0; i < n; ++i, ++c) {
+        const uint32_t stage = c % ST;
+        if (!wait(&m.full[stage], c / ST)) return false;
+        const uint64_t live = m.live[stage];
+        if (~live != 0) {
+          // tokens that are not there: as keys they are masked, as values they have to be finite
+          uint8_t* base = smem + Lay::kv_off + stage * Lay::kStage;
+          for (int t = 0; t < kStep; ++t) {
+            if ((live >> t) & 1) continue;
+            uint8_t* row = base + (t >> 3) * Lay::kGroup + (t & 7) * 128;
+            for (int x = lane; x < NA * 8; x += 32)
+              *reinterpret_cast<uint4*>(row + (x >> 3) * 1024 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        if (c >= 2 && !wait(&m.p_full[c & 1], (c >> 1) - 1)) return false;  // S of two steps ago has been read
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t d = tmem + kTmemS + (c & 1) * kRows, k = dk + stage * (Lay::kStage >> 4);
+#pragma unroll
+          for (int ks = 0; ks < NA * 4; ++ks) {
+            const uint32_t off = ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4;
+            mma_ss_groups<Lay::kGroup, Lay::kGroup>(d, k + off, dq + off, id, ks > 0);
+          }
+          mma_commit(&m.s_full[c & 1]);
+          if (i + 1 == n) mma_commit(&m.q_empty);
+        }
+        __syncwarp();
+      }
+    }
+    return true;
+  }
+
+  // ---- O^T, another ----------------------------------------------------------------------------
+  static __device__ bool issue_pv(const LatentArgs& a, M& m, uint8_t* smem, uint32_t tmem, int rank) {
+    const auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, Waiter{a.err}(bar, phase)) != 0; };
+    const uint32_t sm = smem_u32(smem), dv = desc_mn_major(sm + Lay::kv_off, 1024);
+    const uint32_t dlo = desc_mn_major(sm + Lay::lo_off, 1024);
+    uint32_t c = 0;
+    SegIter it(a.sh, m.plan, a.pair, rank);
+    Seg s;
+    while (uniform(it.next(s))) {
+      const int n = uniform(s.k1 - s.k0);
+      const uint32_t id = uniform(idesc(128, columns(s), true, true));
+      for (int i = 0; i < n; ++i, ++c) {
+        const uint32_t stage = c % ST;
+        if (!wait(&m.p_full[c & 1], c >> 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t v = dv + stage * (Lay::kStage >> 4), hi = v + ((NA - 1) * 1024 >> 4);
+#pragma unroll
+          for (int mt = 0; mt < R / 128; ++mt)
+#pragma unroll
+            for (int ks = 0; ks < kStep / 16; ++ks) {
+              const uint32_t off = 2 * ks * Lay::kGroup >> 4;
+              mma_ss_groups<Lay::kGroup, Lay::kGroup>(tmem + mt * kRows, v + off + (mt * 2048 >> 4), hi + off, id, i > 0 || ks > 0);
+              if (PARTS == 2)
+                mma_ss_groups<Lay::kGroup, 1024>(tmem + mt * kRows, v + off + (mt * 2048 >> 4), dlo + (ks * 2048 >> 4), id, true);
+            }
+          mma_commit(&m.empty[stage]);
+        }
+        __syncwarp();
+      }
+    }
+    return true;
+  }
+
+  // ---- query rows, 8 to a copy (one thread) ----------------------------------------------------
+  static __device__ void load_q(const LatentArgs& a, M& m, uint8_t* smem, int rank) {
+    const Waiter wait{a.err};
+    uint32_t c = 0;
+    SegIter it(a.sh, m.plan, a.pair, rank);
+    Seg s;
+    while (it.next(s)) {
+      if (s.k0 == s.k1) continue;
+      if (c > 0 && !wait(&m.q_empty, c - 1)) break;
+      const int groups = columns(s) / 8, row = s.sq.start * a.sh.H + s.row0;
+      mbar_arrive_expect_tx(&m.q_full, groups * Lay::kGroup);
+      for (int g = 0; g < groups; ++g) {
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                smem_u32(smem + Lay::q_off + g * Lay::kGroup)),
+            "l"(reinterpret_cast<uint64_t>(&a.tmq)), "r"(0), "r"(row + 8 * g), "r"(0), "r"(smem_u32(&m.q_full))
+            : "memory");
+      }
+      ++c;
+    }
+    if (c > 0) wait(&m.q_full, c - 1);  // nothing is in flight when the CTA leaves
+  }
+
+  // ---- steps (one warp) --------------------------------------------------------------------------
+  static __device__ void load_kv(const LatentArgs& a, M& m, uint8_t* smem, int rank, int lane) {
+    const Waiter wait{a.err};
+    const int per = min(a.S, kStep), copies = kStep / per;  // tokens of a copy
+    const uint32_t bytes = per * (R + kRope) * 2;
+    uint32_t c = 0;
+    bool ok = true;
+    SegIter it(a.sh, m.plan, a.pair, rank);
+    Seg s;
+    while (ok && it.next(s)) {
+      const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
+      const auto page_at = [&](int k) {  // of this lane's copy: -1 none, -2 a bad one
+        const int t = k * kStep + lane * per;
+        if (k >= s.k1 || lane >= copies || t >= s.sq.L) return -1;
+        const int page = pt[t >> a.s_log2];
+        return page >= 0 && page < a.n_phys ? page : -2;
+      };
+      const auto ahead = [&](int k, int page) {
+        const int t = k * kStep + lane * per;
+        if (page >= 0)
+          bulk_prefetch_l2(a.pool + (static_cast<size_t>(page) * a.S + (t & (a.S - 1))) * ((R + kRope) * 2),
+                           min(per, s.sq.L - t) * ((R + kRope) * 2));
+      };
+      int pages[kAhead + 1];
+#pragma unroll
+      for (int i = 0; i <= kAhead; ++i) {
+        pages[i] = page_at(s.k0 + i);
+        if (i > 0) ahead(s.k0 + i, pages[i]);
+      }
+      for (int k = s.k0; k < s.k1; ++k, ++c) {
+        const uint32_t stage = c % ST;
+        const int page = pages[0], t = k * kStep + lane * per;
+        const int far = page_at(k + kAhead + 1);
+        if (page == -2) record_error(a.err, SPG_DEVERR_PAGE_ID);
+        uint64_t live = 0;
+        if (page >= 0) {
+          const int cnt = min(per, s.sq.L - t);
+          live = (cnt == 64 ? ~0ull : (1ull << cnt) - 1) << (lane * per);
+        }
+        const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(live));
+        const uint32_t up = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(live >> 32));
+        const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+        if (c >= ST && !__all_sync(0xffffffffu, wait(&m.empty[stage], c / ST - 1))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          m.live[stage] = static_cast<uint64_t>(up) << 32 | lo;
+          mbar_arrive_expect_tx(&m.full[stage], n * bytes);
+        }
+        __syncwarp();
+        if (page >= 0)
+          tma_tile_4d(smem + Lay::kv_off + stage * Lay::kStage + lane * (per / 8) * Lay::kGroup, &a.tmkv, 0, 0, 0,
+                      page * (a.S / 8) + (t & (a.S - 1)) / 8, &m.full[stage]);
+        ahead(k + kAhead + 1, far);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) pages[i] = pages[i + 1];
+        pages[kAhead] = far;
+      }
+    }
+    // nothing is in flight when the CTA leaves
+    for (uint32_t i = c > ST ? c - ST : 0; i < c; ++i) wait(&m.full[i % ST], i / ST);
+  }
+
+  // ---- softmax ---------------------------------------------------------------------------------------
+  // Warp w has tokens 16 w to 16 w + 15 of a step; a thread two of them (lane /
+  // 4 and 8 more) over the rows 8 j + 2 (lane % 4) and the next.
+  static __device__ void softmax(const LatentArgs& a, M& m, uint8_t* smem, uint32_t tmem, int rank, int warp, int lane) {
+    bool dead = false;  // after a wait that ran out the others are skipped, and every barrier is still reached
+    const auto wait = [&](uint64_t* bar, uint32_t phase) {
+      if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
+    };
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int tok = 16 * warp + (lane >> 2), cl = 2 * (lane & 3);
+    const uint32_t sm = smem_u32(smem);
+    // this lane's row of the matrices it addresses: block j (of a pair), token half, row r
+    const int st_r = lane & 7, st_half = (lane >> 3) & 1, st_j = lane >> 4;
+    const uint32_t st_hi = sm + Lay::kv_off + (NA - 1) * 1024 + (2 * warp + st_half) * Lay::kGroup + st_r * 128;
+    const uint32_t st_lo = sm + Lay::lo_off + (2 * warp + st_half) * 1024 + st_r * 128;
+    uint32_t c = 0;
+    SegIter it(a.sh, m.plan, a.pair, rank);
+    Seg s;
+    while (it.next(s)) {
+      const int n = s.k1 - s.k0, nj = columns(s) / 8;
+      const int pos_first = s.sq.pos0 + s.row0 / a.sh.H;
+      if (threadIdx.x < kRows)
+        m.lim[threadIdx.x] = threadIdx.x < s.n_rows ? s.sq.pos0 + (s.row0 + static_cast<int>(threadIdx.x)) / a.sh.H : -1;
+      bar_sync(1, kSoftmax);
+      float nm[16], l[16];  // -m and the thread's sums
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        nm[i] = -kUnset;
+        l[i] = 0.f;
+      }
+      for (int i = 0; i < n; ++i, ++c) {
+        const uint32_t stage = c % ST;
+        wait(&m.s_full[c & 1], c >> 1);
+        tc_fence_after();
+        uint32_t v[32];
+        tmem_ld_frag64(v, lanes + kTmemS + (c & 1) * kRows);
+        tmem_wait_ld();
+        const int t0 = (s.k0 + i) * kStep;
+        const uint64_t live = m.live[stage];
+        if (~live != 0 || t0 + kStep - 1 > pos_first) {
+          const bool la = (live >> tok) & 1, lb = (live >> (tok + 8)) & 1;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int lim = m.lim[8 * j + cl + e] - t0;
+              if (!la || tok > lim) v[4 * j + e] = 0xff800000u;  // -inf
+              if (!lb || tok + 8 > lim) v[4 * j + 2 + e] = 0xff800000u;
+            }
+        }
+        const auto f = [&](int x) { return __uint_as_float(v[x]); };
+        bool over = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < nj) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float z = fmaf(fmaxf(f(4 * j + e), f(4 * j + 2 + e)), a.scale_log2, nm[2 * j + e]);
+              over |= z > kTop;
+            }
+          }
+        if (bar_any(1, kSoftmax, over)) {
+          // some row's maximum is raised: the maxima of all rows over the step
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < nj) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(f(4 * j + e), f(4 * j + 2 + e)) * a.scale_log2;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                if (lane < 4) m.top[warp][8 * j + cl + e] = x;
+              }
+            }
+          bar_sync(1, kSoftmax);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < nj) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int col = 8 * j + cl + e, x = 2 * j + e;
+                const float top = fmaxf(fmaxf(m.top[0][col], m.top[1][col]), fmaxf(m.top[2][col], m.top[3][col]));
+                float fac = 1.f;
+                if (top + nm[x] > kTop) {
+                  fac = ex2(kHead - top - nm[x]);  // 0 for a row that has seen nothing
+                  nm[x] = kHead - top;
+                  l[x] *= fac;
+                }
+                if (warp == 0 && lane < 4) m.factor[col] = fac;
+              }
+            }
+          bar_sync(1, kSoftmax);
+          if (i > 0) {
+            wait(&m.empty[(c - 1) % ST], (c - 1) / ST);  // O holds earlier steps, all done
+            tc_fence_after();
+#pragma unroll 1
+            for (int mt = 0; mt < R / 128; ++mt)
+#pragma unroll 1
+              for (int c0 = 0; c0 < 8 * nj; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(o, lanes + mt * kRows + c0);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * m.factor[c0 + x]);
+                tmem_st16(lanes + mt * kRows + c0, o);
+              }
+            tmem_wait_st();
+          }
+        }
+        uint32_t hi[16], lo[16];  // of block j: first token's pair, the second's
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < nj) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float p0 = ex2(fmaf(f(4 * j + 2 * r), a.scale_log2, nm[2 * j]));
+              const float p1 = ex2(fmaf(f(4 * j + 2 * r + 1), a.scale_log2, nm[2 * j + 1]));
+              l[2 * j] += p0;
+              l[2 * j + 1] += p1;
+              hi[2 * j + r] = pack2<T>(p0, p1);
+              if constexpr (PARTS == 2) {  // what the rounding left
+                const float2 h = unpack2f<T>(hi[2 * j + r]);
+                lo[2 * j + r] = pack2<T>(p0 - h.x, p1 - h.y);
+              }
+            }
+          }
+        if (PARTS == 2 && c > 0) wait(&m.empty[(c - 1) % ST], (c - 1) / ST);  // the second values' buffer is free
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (2 * q < nj) {
+            const uint32_t sw = ((2 * q + st_j) ^ st_r) << 4;
+            stmatrix_x4(st_hi + stage * Lay::kStage + sw, hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+            if constexpr (PARTS == 2) stmatrix_x4(st_lo + sw, lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+          }
+        fence_proxy_async();
+        tc_fence_before();
+        mbar_arrive(&m.p_full[c & 1]);
+      }
+
+      // ---- the segment's end: sums over the tokens' threads, then O^T by channels ----
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int col = 8 * (x >> 1) + cl + (x & 1);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
+        if (lane < 4) {
+          m.top[warp][col] = l[x];
+          if (warp == 0) m.factor[col] = -nm[x];
+        }
+      }
+      if (n > 0) wait(&m.empty[(c - 1) % ST], (c - 1) / ST);
+      bar_sync(1, kSoftmax);
+      const int col = threadIdx.x;
+      const size_t grow = static_cast<size_t>(s.sq.start) * a.sh.H + s.row0;
+      const int slot = slot_of(a, static_cast<int>(blockIdx.x) >> a.pair, s.k0_of_pair == 0, s.half);
+      if (col < s.n_rows) {
+        const float sum = (m.top[0][col] + m.top[1][col]) + (m.top[2][col] + m.top[3][col]), mx = m.factor[col];
+        m.inv[col] = sum == 0.f ? 0.f : 1.f / sum;
+        if (s.split) {
+          __stcg(a.part_m + slot * kRows + col, mx);
+          __stcg(a.part_l + slot * kRows + col, sum);
+        } else if (a.lse) {
+          a.lse[grow + col] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+        }
+      }
+      bar_sync(1, kSoftmax);
+      tc_fence_after();
+      if (n > 0) {
+#pragma unroll 1
+        for (int mt = 0; mt < R / 128; ++mt) {
+          const int ch = mt * 128 + warp * 32 + lane;
+#pragma unroll 1
+          for (int c0 = 0; c0 < s.n_rows; c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(o, lanes + mt * kRows + c0);
+            tmem_wait_ld();
+            if (s.split) {
+              float* dst = a.part + (static_cast<size_t>(slot) * a.part_rows + c0) * R + ch;
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                if (c0 + x < s.n_rows) __stcg(dst + x * R, __uint_as_float(o[x]));
+            } else {
+              T* dst = static_cast<T*>(a.out) + (grow + c0) * R + ch;
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                if (c0 + x < s.n_rows) {
+                  const float inv = m.inv[c0 + x];
+                  // inv = 0: a row that saw nothing
+                  dst[x * R] = static_cast<T>(inv == 0.f ? 0.f : __uint_as_float(o[x]) * inv);
+                }
+            }
+          }
+        }
+      }
+      tc_fence_before();     // the reads of O come before the next segment's first product
+      bar_sync(1, kSoftmax);  // lim, top, factor and inv are read
+    }
+  }
+};
+
+template <typename T, int R, int PARTS>
+__global__ void __launch_bounds__(256, 1) k_latent(const __grid_constant__ LatentArgs a) {
+  using K = Kernel<T, R, PARTS>;
+  using Lay = typename K::Lay;
+  using M = typename K::M;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  M& m = *reinterpret_cast<M*>(smem + Lay::misc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = a.pair ? static_cast<int>(blockIdx.x) & 1 : 0;
+  if (threadIdx.x == 0) {
+    mbar_init(&m.q_full, 1);
+    mbar_init(&m.q_empty, 1);
+    for (int i = 0; i < K::ST; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.s_full[i], 1);
+      mbar_init(&m.p_full[i], K::kSoftmax);
+      mbar_init(&m.drain[i], 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == K::kSWarp) tmem_alloc(&m.tmem, kTmemCols);
+  pdl_wait();
+  if (warp == 0) make_plan(a.sh, &m.plan, a.err, lane, static_cast<int>(blockIdx.x) >> a.pair, static_cast<int>(gridDim.x) >> a.pair);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = m.tmem;
+
+  if (warp < 4) {
+    K::softmax(a, m, smem, tmem, rank, warp, lane);
+  } else if (warp == K::kLoadWarp) {
+    K::load_kv(a, m, smem, rank, lane);
+  } else if (warp == K::kQWarp) {
+    if (lane == 0) K::load_q(a, m, smem, rank);
+    __syncwarp();
+  } else {
+    const bool ok = warp == K::kSWarp ? K::issue_s(a, m, smem, tmem, rank, lane) : K::issue_pv(a, m, smem, tmem, rank);
+    if (!ok) {  // products in flight end before TMEM goes back
+      uint64_t* bar = &m.drain[warp - K::kSWarp];
+      if (elect_one()) mma_commit(bar);
+      __syncwarp();
+      mbar_wait_bounded(bar, 0);
+    }
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == K::kSWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---- the parts of an item joined ------------------------------------------------------------
+// CTA (c, y) takes, of each item that CTA c had a part of, its share of
+// (row, 128 channels) units; the parts of a unit are shared out to 1 to 8 warps.
+constexpr int kJoinWarps = 8, kJoinY = 2;
+
+template <typename T, int R>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_constant__ LatentArgs a) {
+  __shared__ Plan plan;
+  __shared__ float4 acc_s[kJoinWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  const int c = blockIdx.x;
+  if (warp == 0) make_plan(a.sh, &plan, a.err, lane, c, gridDim.x);
+  __syncthreads();
+  pdl_trigger();
+  PartIter<LatentItems> it(a.sh, plan);
+  Part s;
+  while (it.next(s)) {
+    if (s.whole()) continue;
+    const PartRange pr(plan, s);
+    const int row0 = s.item << a.sh.rows_log2, n_rows = min(1 << a.sh.rows_log2, s.sq.n * a.sh.H - row0);
+    const bool by_half = a.pair && n_rows <= kRows;  // the pair's CTAs had halves of the steps
+    const int parts = (pr.c1 - pr.c0 + 1) << (by_half ? 1 : 0);
+    const int wlog = parts >= 32 ? 3 : parts >= 16 ? 2 : parts >= 8 ? 1 : 0;  // warps to a unit
+    const int sub = warp & ((1 << wlog) - 1), per_round = kJoinWarps >> wlog;
+    const int units = n_rows * (R / 128), shares = (pr.c1 - pr.c0 + 1) * kJoinY;
+    for (int u0 = ((c - pr.c0) * kJoinY + static_cast<int>(blockIdx.y)) * per_round; u0 < units; u0 += shares * per_round) {
+      const int u = u0 + (warp >> wlog);
+      const bool live = u < units;
+      const int row = live ? u / (R / 128) : 0, ch = (u % (R / 128)) * 128 + lane * 4;
+      const auto slot = [&](int i) {
+        const int cc = pr.c0 + (by_half ? i >> 1 : i);
+        return slot_of(a, cc, cc == pr.c0, by_half ? i & 1 : row >> 6);
+      };
+      float mm = kUnset, sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int base = 0; base < parts; base += 32) {
+        const int i = base + lane;
+        if (i < parts && __ldcg(a.part_l + slot(i) * kRows + (row & 63)) != 0.f)
+          mm = fmaxf(mm, __ldcg(a.part_m + slot(i) * kRows + (row & 63)));
+      }
+      mm = warp_max(mm);
+      for (int base = 0; base < parts; base += 32) {
+        const int i = base + lane;
+        float w = 0.f;
+        if (i < parts) {
+          const float l = __ldcg(a.part_l + slot(i) * kRows + (row & 63));
+          if (l != 0.f) {  // else the part saw nothing, and may not have written its O
+            w = ex2(__ldcg(a.part_m + slot(i) * kRows + (row & 63)) - mm);
+            sum += w * l;
+          }
+        }
+        const int end = min(32, parts - base);
+#pragma unroll 4
+        for (int q = sub; q < end; q += 1 << wlog) {
+          const float wq = __shfl_sync(0xffffffffu, w, q);
+          const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(slot(base + q)) * a.part_rows + (row & 63)) * R + ch));
+          if (wq != 0.f) {
+            acc.x = fmaf(wq, o.x, acc.x);
+            acc.y = fmaf(wq, o.y, acc.y);
+            acc.z = fmaf(wq, o.z, acc.z);
+            acc.w = fmaf(wq, o.w, acc.w);
+          }
+        }
+      }
+      sum = warp_sum(sum);
+      acc_s[warp][lane] = acc;
+      __syncthreads();
+      if (live && sub == 0) {
+        for (int q = 1; q < 1 << wlog; ++q) {
+          const float4 o = acc_s[warp + q][lane];
+          acc.x += o.x;
+          acc.y += o.y;
+          acc.z += o.z;
+          acc.w += o.w;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const size_t grow = static_cast<size_t>(s.sq.start) * a.sh.H + row0 + row;
+        const uint2 w = make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + grow * R + ch) = w;
+        if (a.lse && ch < 4 && lane == 0) a.lse[grow] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------------------------
+
+size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+int part_rows(const spg_latent_params& p, int total_q) {
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(kRows, static_cast<long long>(total_q) * p.num_heads)));
+}
+constexpr int kSlots = 2 * kMaxCtas;
+
+template <typename T, int R, int PARTS>
+cudaError_t latent_typed(const spg_latent_params& p, LatentArgs& a, const void* q_lat, const void* pool, cudaStream_t st) {
+  using K = Kernel<T, R, PARTS>;
+  const uint64_t row = 2 * (R + kRope);
+  const uint64_t qd[3] = {64, static_cast<uint64_t>(a.sh.total_q) * p.num_heads, K::NA}, qs[2] = {row, 128};
+  const uint32_t qb[3] = {64, 8, K::NA};
+  const uint64_t kd[4] = {64, 8, K::NA, static_cast<uint64_t>(p.num_phys_pages) * (p.page_size / 8)}, ks[3] = {row, 128, 8 * row};
+  const uint32_t kb[4] = {64, 8, K::NA, static_cast<uint32_t>(std::min(p.page_size, kStep) / 8)};
+  if (!make_tmap16(&a.tmq, p.dtype, q_lat, 3, qd, qs, qb) || !make_tmap16(&a.tmkv, p.dtype, pool, 4, kd, ks, kb))
+    return cudaErrorNotSupported;
+  const auto kern = k_latent<T, R, PARTS>;
+  const size_t smem = 1024 + K::Lay::misc + sizeof(typename K::M);
+  static_assert(1024 + K::Lay::misc + sizeof(typename K::M) <= 232448, "shared memory of a CTA");
+  cudaError_t e = ensure_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  const int ctas = std::min(device_sm_count(), kMaxCtas) >> a.pair;
+  e = launch_pdl(kern, dim3(ctas << a.pair), dim3(K::kThreads), smem, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_latent_join<T, R>, dim3(ctas, kJoinY), dim3(32 * kJoinWarps), 0, st, a);
+}
+
+}  // namespace
+
+size_t latent_workspace_bytes(const spg_latent_params& p, int total_q) {
+  return 256 + 2 * round256(sizeof(float) * kSlots * kRows) + sizeof(float) * kSlots * part_rows(p, total_q) * p.latent_dim;
+}
+
+cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows& r, const void* q_lat, const void* pool,
+                                    void* o_lat, float* lse, int parts, void* ws, cudaStream_t stream) {
+  LatentArgs a{};
+  a.sh.q_start = r.q_start;
+  a.sh.seq_lens = r.seq_lens;
+  a.sh.B = p.batch;
+  a.sh.Hkv = 1;
+  a.sh.total_q = r.total_q;
+  a.sh.max_tokens = p.max_pages_per_seq * p.page_size;
+  a.sh.H = p.num_heads;
+  // two CTAs over the same steps where sequences have more than 64 rows (on average)
+  a.pair = static_cast<long long>(r.total_q) * p.num_heads > static_cast<long long>(kRows) * p.batch || p.num_heads > kRows ? 1 : 0;
+  a.sh.rows_log2 = 6 + a.pair;
+  a.pool = static_cast<const uint8_t*>(pool);
+  a.page_table = r.page_table;
+  a.out = o_lat;
+  a.lse = lse;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.err = reinterpret_cast<int32_t*>(base);
+  a.part_m = reinterpret_cast<float*>(base + 256);
+  a.part_l = reinterpret_cast<float*>(base + 256 + round256(sizeof(float) * kSlots * kRows));
+  a.part = reinterpret_cast<float*>(base + 256 + 2 * round256(sizeof(float) * kSlots * kRows));
+  a.S = p.page_size;
+  a.s_log2 = log2_of(p.page_size);
+  a.MP = p.max_pages_per_seq;
+  a.n_phys = p.num_phys_pages;
+  a.part_rows = part_rows(p, r.total_q);
+  a.scale_log2 = (p.softmax_scale > 0.f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.nope_dim + p.rope_dim))) * kLog2e;
+#define SPG_LATENT(T)                                                                                             \
+  do {                                                                                                            \
+    if (parts == 1)                                                                                               \
+      return p.latent_dim == 512 ? latent_typed<T, 512, 1>(p, a, q_lat, pool, stream)                             \
+                                 : latent_typed<T, 256, 1>(p, a, q_lat, pool, stream);                            \
+    return p.latent_dim == 512 ? latent_typed<T, 512, 2>(p, a, q_lat, pool, stream)                               \
+                               : latent_typed<T, 256, 2>(p, a, q_lat, pool, stream);                              \
+  } while (0)
+  if (p.dtype == SPG_F16) SPG_LATENT(__half);
+  SPG_LATENT(__nv_bfloat16);
+#undef SPG_LATENT
+}
+
+}  // namespace spg

@@ -41,22 +41,6 @@ struct RopeArgs {
   int B, Hq, Hkv, S, MP, n_phys, total_q, rot, tokens;
 };
 
-// 8 values of a 16-byte piece
-template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2f<T>(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
-}
-
 template <typename T, bool I8, int D, bool HALF>
 __global__ void __launch_bounds__(kThreads) k_rope_append(const __grid_constant__ RopeArgs a) {
   constexpr int IPH = D / 16;  // items of one head
