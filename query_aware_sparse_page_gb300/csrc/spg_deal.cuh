@@ -31,10 +31,18 @@ struct ChunkShape {
   __device__ ChunkSeq seq(int b, int32_t& bad) const { return chunk_seq(q_start, seq_lens, b, total_q, max_tokens, bad); }
 };
 
+// a / b, b > 0, a >= 0: in 32 bits where both fit, a sixth of the time
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  if ((static_cast<unsigned long long>(a) | static_cast<unsigned long long>(b)) >> 32)
+    return a / b;
+  return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 struct Plan {
   long long total, lo, hi;  // steps in all, and this CTA's
   long long item_first;     // first step of the item that lo lies in
-  int ctas, b, h, item;
+  int ctas, b, h, item, n_items;
+  ChunkSeq sq;              // sequence b
 };
 
 // one whole warp; the share of CTA c of n_ctas
@@ -43,10 +51,19 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, in
                           int n_ctas = static_cast<int>(gridDim.x)) {
   long long total = 0, items = 0;
   int32_t bad = 0;
+  ChunkSeq first_sq{};  // of the lane's first sequence, its items and their steps
+  int first_items = 0;
+  long long first_w = 0;
   for (int b = lane; b < sh.B; b += 32) {
     const ChunkSeq s = sh.seq(b, bad);
     const int ni = sh.items(s);
-    total += sh.Hkv * sh.steps(s, ni);
+    const long long w = sh.Hkv * sh.steps(s, ni);
+    if (b == lane) {
+      first_sq = s;
+      first_items = ni;
+      first_w = w;
+    }
+    total += w;
     items += static_cast<long long>(sh.Hkv) * ni;
   }
 #pragma unroll
@@ -64,16 +81,21 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, in
     if (lane == 0) *out = p;  // lo = hi = 0: nothing to do
     return;
   }
-  p.lo = c * total / n;
-  p.hi = (c + 1) * total / n;
+  p.lo = div_pos(c * total, n);
+  p.hi = div_pos((c + 1) * total, n);
   long long base = 0;
   for (int b0 = 0; b0 < sh.B; b0 += 32) {
     const int b = b0 + lane;
-    long long w = 0;
-    ChunkSeq s{};
-    if (b < sh.B) {
-      s = sh.seq(b, bad);
-      w = sh.Hkv * sh.steps(s, sh.items(s));
+    long long w = first_w;
+    ChunkSeq s = first_sq;
+    int ni = first_items;
+    if (b0 > 0) {
+      w = 0;
+      if (b < sh.B) {
+        s = sh.seq(b, bad);
+        ni = sh.items(s);
+        w = sh.Hkv * sh.steps(s, ni);
+      }
     }
     long long incl = w;
 #pragma unroll
@@ -83,16 +105,18 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, in
     }
     const long long first = base + incl - w;
     if (p.lo >= first && p.lo < first + w) {  // one lane
-      const long long per_head = w / sh.Hkv;
+      const long long per_head = div_pos(w, sh.Hkv);
       p.b = b;
-      p.h = static_cast<int>((p.lo - first) / per_head);
-      const long long rest = (p.lo - first) % per_head;
-      int x = 0, y = sh.items(s) - 1;  // the last item that starts at or before rest
+      p.h = static_cast<int>(div_pos(p.lo - first, per_head));
+      const long long rest = p.lo - first - p.h * per_head;
+      int x = 0, y = ni - 1;  // the last item that starts at or before rest
       while (x < y) {
         const int mid = (x + y + 1) >> 1;
         if (sh.steps(s, mid) <= rest) x = mid; else y = mid - 1;
       }
       p.item = x;
+      p.n_items = ni;
+      p.sq = s;
       p.item_first = first + p.h * per_head + sh.steps(s, x);
       *out = p;
     }
@@ -117,9 +141,7 @@ struct PartIter {
   int b, h, item, n_items;
   ChunkSeq sq;
   __device__ PartIter(const Shape& shape, const Plan& p)
-      : sh(shape), pos(p.lo), hi(p.hi), item_first(p.item_first), b(p.b), h(p.h), item(p.item) {
-    if (pos < hi) load();
-  }
+      : sh(shape), pos(p.lo), hi(p.hi), item_first(p.item_first), b(p.b), h(p.h), item(p.item), n_items(p.n_items), sq(p.sq) {}
   __device__ void load() {
     int32_t bad = 0;
     sq = sh.seq(b, bad);
@@ -159,8 +181,8 @@ struct PartIter {
 struct PartRange {
   int c0, c1;
   __device__ PartRange(const Plan& p, const Part& s)
-      : c0(static_cast<int>(((s.item_first + 1) * p.ctas - 1) / p.total)),
-        c1(static_cast<int>(((s.item_first + s.nk) * p.ctas - 1) / p.total)) {}
+      : c0(static_cast<int>(div_pos((s.item_first + 1) * p.ctas - 1, p.total))),
+        c1(static_cast<int>(div_pos((s.item_first + s.nk) * p.ctas - 1, p.total))) {}
   __device__ int slot(int c) const { return c == c0 ? 2 * c + 1 : 2 * c; }
 };
 __device__ __forceinline__ int own_slot(const Part& s) { return 2 * static_cast<int>(blockIdx.x) + (s.k0 > 0 ? 0 : 1); }

@@ -131,40 +131,56 @@ struct SegIter : PartIter<LatentItems> {
   }
 };
 
+// What the second launch has to know of a part: CTA c0 + i, i < n, has part i
+// of the same rows (by_half: its two halves of the steps, parts 2 i and 2 i + 1).
+struct PartRecord {
+  int row, n_rows, c0, n, index, by_half, half, pad;  // first row of the chunk; this part's number
+};
+
 struct LatentArgs {
   LatentItems sh;
-  CUtensorMap tmq, tmkv;
+  CUtensorMap tmq, tmkv, tmkv2;  // query rows; the halves of the cached ones
   const uint8_t* pool;
   const int32_t* page_table;
   void* out;
   float* lse;
   int32_t* err;
   float *part, *part_m, *part_l;  // [2 * CTAs][part_rows][R], [2 * CTAs][64] twice
+  PartRecord* record;             // [2 * CTAs], n = 0 for a slot without a part
   int S, s_log2, MP, n_phys, part_rows, pair;
   float scale_log2;
 };
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ int slot_of(const LatentArgs& a, int c, bool first, int half) {
   return ((2 * c + (first ? 1 : 0)) << a.pair) + half;
 }
 
+// A stage holds a step in two halves, the first R / 2 channels of its tokens
+// and the others with the rotary block, that come and go by themselves: the
+// first's products run while the second is on its way, and the next step's
+// first half comes while the second's products run.
 template <int R>
 struct Layout {
-  static constexpr int NA = R / 64 + 1;              // 64-channel blocks of a cached row
-  static constexpr uint32_t kGroup = NA * 1024;      // 8 tokens (or query rows)
-  static constexpr uint32_t kStage = kStep / 8 * kGroup;
+  static constexpr int NA = R / 64 + 1;      // 64-channel blocks of a cached row
+  static constexpr int kBlocksA = R / 128, kBlocksB = kBlocksA + 1;  // of its halves
+  static constexpr uint32_t kGroupA = kBlocksA * 1024, kGroupB = kBlocksB * 1024, kGroupQ = NA * 1024;  // 8 tokens, 8 query rows
+  static constexpr uint32_t kHalfB = kStep / 8 * kGroupA;  // where the second half begins
+  static constexpr uint32_t kStage = kHalfB + kStep / 8 * kGroupB;
+  static constexpr uint32_t kRopeBlock = kHalfB + kBlocksA * 1024;
   static constexpr int ST = R == 512 ? 2 : 4;
-  static constexpr uint32_t q_off = 0, kv_off = kRows / 8 * kGroup, lo_off = kv_off + ST * kStage, misc = lo_off + kStep * 128;
+  static constexpr uint32_t q_off = 0, kv_off = kRows / 8 * kGroupQ, lo_off = kv_off + ST * kStage, misc = lo_off + kStep * 128;
 };
 template <int ST>
 struct Misc {
-  uint64_t q_full, q_empty, full[ST], empty[ST], s_full[2], p_full[2], drain[2];
+  uint64_t q_full, q_empty, full[ST][2], empty[ST][2], s_full[2], p_full[2], drain[2];
   uint64_t live[ST];  // tokens of a step that are there
   Plan plan;
   uint32_t tmem;
-  int lim[kRows];             // last token a row sees
-  float top[4][kRows];        // largest logit of a step, per warp; at the end the sums
-  float factor[kRows];
+  int lim[kRows];       // last token a row sees
+  float top[4][kRows];  // largest logit of a step, per 16 tokens; at the end the sums
+  float factor[kRows];  // what O is rescaled by; at the end the maxima
   float inv[kRows];
 };
 
@@ -173,10 +189,12 @@ struct Kernel {
   using Lay = Layout<R>;
   static constexpr int ST = Lay::ST, NA = Lay::NA;
   using M = Misc<ST>;
-  static constexpr int kThreads = 256, kSoftmax = 128, kLoadWarp = 4, kSWarp = 5, kPvWarp = 6, kQWarp = 7;
-  static constexpr int kAhead = 2;  // steps brought into L2 before their copies
+  // two softmax warpgroups, then the warps that load the steps, issue S, issue O and load Q
+  static constexpr int kThreads = 384, kSoftmax = 256, kLoadWarp = 8, kSWarp = 9, kQWarp = 11;
 
   static __device__ __forceinline__ int columns(const Seg& s) { return (s.n_rows + 15) & ~15; }
+  // up to 32 rows: both values of P side by side in one operand, O in two parts
+  static __device__ __forceinline__ bool side_by_side(const Seg& s) { return PARTS == 2 && s.n_rows <= kRows / 2; }
   static __device__ __forceinline__ uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
     return instr_desc<T>(0, 0, b_mn) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
   }
@@ -193,36 +211,69 @@ struct Kernel {
       const int n = uniform(s.k1 - s.k0);
       if (n == 0) continue;
       const uint32_t id = uniform(idesc(64, columns(s), false, false));
+      // While a step's products run and its chain goes on, the step that will
+      // take its place comes to L2 (earlier it would hold up the copies on
+      // their way).  Not for sequences of several items, whose steps others
+      // bring there (a prompt piece: 400 us, with it 424).
+      const bool bring = uniform(it.n_items == 1);
+      const int per = min(a.S, kStep), copies = kStep / per;
+      const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
+      const auto page_at = [&](int k) {
+        const int t = k * kStep + lane * per;
+        const bool there = k < s.k1 && lane < copies && t < s.sq.L;
+        const int page = pt[there ? t >> a.s_log2 : s.k0 * kStep >> a.s_log2];
+        return there && page >= 0 && page < a.n_phys ? page : -1;
+      };
+      int ahead = bring ? page_at(s.k0 + ST) : -1;
       if (!wait(&m.q_full, qc++)) return false;
       for (int i = 0; i < n; ++i, ++c) {
         const uint32_t stage = c % ST;
-        if (!wait(&m.full[stage], c / ST)) return false;
-        const uint64_t live = m.live[stage];
-        if (~live != 0) {
-          // tokens that are not there: as keys they are masked, as values they have to be finite
-          uint8_t* base = smem + Lay::kv_off + stage * Lay::kStage;
-          for (int t = 0; t < kStep; ++t) {
-            if ((live >> t) & 1) continue;
-            uint8_t* row = base + (t >> 3) * Lay::kGroup + (t & 7) * 128;
-            for (int x = lane; x < NA * 8; x += 32)
-              *reinterpret_cast<uint4*>(row + (x >> 3) * 1024 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+        const uint32_t d = tmem + kTmemS + (c & 1) * kRows;
+        const auto products = [&](auto which) {
+          constexpr int half = decltype(which)::value;
+          constexpr int kBlocks = half == 0 ? Lay::kBlocksA : Lay::kBlocksB;
+          constexpr uint32_t kGroup = kBlocks * 1024;
+          if (!wait(&m.full[stage][half], c / ST)) return false;
+          const uint64_t live = m.live[stage];
+          if (~live != 0) {
+            // tokens that are not there: as keys they are masked, as values they have to be finite
+            uint8_t* base = smem + Lay::kv_off + stage * Lay::kStage + half * Lay::kHalfB;
+            for (int t = 0; t < kStep; ++t) {
+              if ((live >> t) & 1) continue;
+              uint8_t* row = base + (t >> 3) * kGroup + (t & 7) * 128;
+              for (int x = lane; x < kBlocks * 8; x += 32)
+                *reinterpret_cast<uint4*>(row + (x >> 3) * 1024 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async();
+            __syncwarp();
           }
-          fence_proxy_async();
-          __syncwarp();
-        }
-        if (c >= 2 && !wait(&m.p_full[c & 1], (c >> 1) - 1)) return false;  // S of two steps ago has been read
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t d = tmem + kTmemS + (c & 1) * kRows, k = dk + stage * (Lay::kStage >> 4);
+          // S of two steps ago has been read
+          if (half == 0 && c >= 2 && !wait(&m.p_full[c & 1], (c >> 1) - 1)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t k = dk + ((stage * Lay::kStage + half * Lay::kHalfB) >> 4), q = dq + half * (Lay::kGroupA >> 4);
 #pragma unroll
-          for (int ks = 0; ks < NA * 4; ++ks) {
-            const uint32_t off = ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4;
-            mma_ss_groups<Lay::kGroup, Lay::kGroup>(d, k + off, dq + off, id, ks > 0);
+            for (int ks = 0; ks < kBlocks * 4; ++ks) {
+              const uint32_t off = ((ks >> 2) * 1024 + (ks & 3) * 32) >> 4;
+              mma_ss_groups<kGroup, Lay::kGroupQ>(d, k + off, q + off, id, half > 0 || ks > 0);
+            }
+            if (half == 1) {
+              mma_commit(&m.s_full[c & 1]);
+              if (i + 1 == n) mma_commit(&m.q_empty);
+            }
           }
-          mma_commit(&m.s_full[c & 1]);
-          if (i + 1 == n) mma_commit(&m.q_empty);
+          __syncwarp();
+          return true;
+        };
+        if (!products(std::integral_constant<int, 0>{}) || !products(std::integral_constant<int, 1>{})) return false;
+        if (bring) {
+          if (ahead >= 0) {
+            const int t = (s.k0 + i + ST) * kStep + lane * per;
+            bulk_prefetch_l2(a.pool + (static_cast<size_t>(ahead) * a.S + (t & (a.S - 1))) * ((R + kRope) * 2),
+                             min(per, s.sq.L - t) * ((R + kRope) * 2));
+          }
+          ahead = page_at(s.k0 + i + 1 + ST);
         }
-        __syncwarp();
       }
     }
     return true;
@@ -238,23 +289,32 @@ struct Kernel {
     Seg s;
     while (uniform(it.next(s))) {
       const int n = uniform(s.k1 - s.k0);
-      const uint32_t id = uniform(idesc(128, columns(s), true, true));
+      const bool one = uniform(PARTS == 1 || side_by_side(s));  // one operand
+      const uint32_t id = uniform(idesc(128, side_by_side(s) ? 2 * columns(s) : columns(s), true, true));
       for (int i = 0; i < n; ++i, ++c) {
         const uint32_t stage = c % ST;
         if (!wait(&m.p_full[c & 1], c >> 1)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t v = dv + stage * (Lay::kStage >> 4), hi = v + ((NA - 1) * 1024 >> 4);
+          const uint32_t v = dv + (stage * Lay::kStage >> 4), hi = v + (Lay::kRopeBlock >> 4);
 #pragma unroll
-          for (int mt = 0; mt < R / 128; ++mt)
+          for (int mt = 0; mt < R / 128; ++mt) {
+            constexpr int kMtA = R / 256;  // the first half's
 #pragma unroll
             for (int ks = 0; ks < kStep / 16; ++ks) {
-              const uint32_t off = 2 * ks * Lay::kGroup >> 4;
-              mma_ss_groups<Lay::kGroup, Lay::kGroup>(tmem + mt * kRows, v + off + (mt * 2048 >> 4), hi + off, id, i > 0 || ks > 0);
-              if (PARTS == 2)
-                mma_ss_groups<Lay::kGroup, 1024>(tmem + mt * kRows, v + off + (mt * 2048 >> 4), dlo + (ks * 2048 >> 4), id, true);
+              const auto product = [&](auto b_groups, uint32_t b, bool acc) {
+                constexpr uint32_t SB = decltype(b_groups)::value;
+                if (mt < kMtA)
+                  mma_ss_groups<Lay::kGroupA, SB>(tmem + mt * kRows, v + ((2 * ks * Lay::kGroupA + mt * 2048) >> 4), b, id, acc);
+                else
+                  mma_ss_groups<Lay::kGroupB, SB>(tmem + mt * kRows, v + ((Lay::kHalfB + 2 * ks * Lay::kGroupB + (mt - kMtA) * 2048) >> 4), b, id, acc);
+              };
+              product(std::integral_constant<uint32_t, Lay::kGroupB>{}, hi + (2 * ks * Lay::kGroupB >> 4), i > 0 || ks > 0);
+              if (!one) product(std::integral_constant<uint32_t, 1024>{}, dlo + (ks * 2048 >> 4), true);
             }
-          mma_commit(&m.empty[stage]);
+            if (mt + 1 == kMtA) mma_commit(&m.empty[stage][0]);
+          }
+          mma_commit(&m.empty[stage][1]);
         }
         __syncwarp();
       }
@@ -272,11 +332,11 @@ struct Kernel {
       if (s.k0 == s.k1) continue;
       if (c > 0 && !wait(&m.q_empty, c - 1)) break;
       const int groups = columns(s) / 8, row = s.sq.start * a.sh.H + s.row0;
-      mbar_arrive_expect_tx(&m.q_full, groups * Lay::kGroup);
+      mbar_arrive_expect_tx(&m.q_full, groups * Lay::kGroupQ);
       for (int g = 0; g < groups; ++g) {
         asm volatile(
             "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                smem_u32(smem + Lay::q_off + g * Lay::kGroup)),
+                smem_u32(smem + Lay::q_off + g * Lay::kGroupQ)),
             "l"(reinterpret_cast<uint64_t>(&a.tmq)), "r"(0), "r"(row + 8 * g), "r"(0), "r"(smem_u32(&m.q_full))
             : "memory");
       }
@@ -289,35 +349,24 @@ struct Kernel {
   static __device__ void load_kv(const LatentArgs& a, M& m, uint8_t* smem, int rank, int lane) {
     const Waiter wait{a.err};
     const int per = min(a.S, kStep), copies = kStep / per;  // tokens of a copy
-    const uint32_t bytes = per * (R + kRope) * 2;
     uint32_t c = 0;
     bool ok = true;
     SegIter it(a.sh, m.plan, a.pair, rank);
     Seg s;
     while (ok && it.next(s)) {
+      if (s.k0 == s.k1) continue;
       const int32_t* pt = a.page_table + static_cast<size_t>(s.b) * a.MP;
       const auto page_at = [&](int k) {  // of this lane's copy: -1 none, -2 a bad one
         const int t = k * kStep + lane * per;
-        if (k >= s.k1 || lane >= copies || t >= s.sq.L) return -1;
-        const int page = pt[t >> a.s_log2];
-        return page >= 0 && page < a.n_phys ? page : -2;
+        const bool there = k < s.k1 && lane < copies && t < s.sq.L;
+        const int page = pt[there ? t >> a.s_log2 : s.k0 * kStep >> a.s_log2];
+        return there ? (page >= 0 && page < a.n_phys ? page : -2) : -1;
       };
-      const auto ahead = [&](int k, int page) {
-        const int t = k * kStep + lane * per;
-        if (page >= 0)
-          bulk_prefetch_l2(a.pool + (static_cast<size_t>(page) * a.S + (t & (a.S - 1))) * ((R + kRope) * 2),
-                           min(per, s.sq.L - t) * ((R + kRope) * 2));
-      };
-      int pages[kAhead + 1];
-#pragma unroll
-      for (int i = 0; i <= kAhead; ++i) {
-        pages[i] = page_at(s.k0 + i);
-        if (i > 0) ahead(s.k0 + i, pages[i]);
-      }
+      int next = page_at(s.k0);
       for (int k = s.k0; k < s.k1; ++k, ++c) {
         const uint32_t stage = c % ST;
-        const int page = pages[0], t = k * kStep + lane * per;
-        const int far = page_at(k + kAhead + 1);
+        const int page = next, t = k * kStep + lane * per;
+        next = page_at(k + 1);
         if (page == -2) record_error(a.err, SPG_DEVERR_PAGE_ID);
         uint64_t live = 0;
         if (page >= 0) {
@@ -327,55 +376,67 @@ struct Kernel {
         const uint32_t lo = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(live));
         const uint32_t up = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(live >> 32));
         const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (c >= ST && !__all_sync(0xffffffffu, wait(&m.empty[stage], c / ST - 1))) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          m.live[stage] = static_cast<uint64_t>(up) << 32 | lo;
-          mbar_arrive_expect_tx(&m.full[stage], n * bytes);
-        }
-        __syncwarp();
-        if (page >= 0)
-          tma_tile_4d(smem + Lay::kv_off + stage * Lay::kStage + lane * (per / 8) * Lay::kGroup, &a.tmkv, 0, 0, 0,
-                      page * (a.S / 8) + (t & (a.S - 1)) / 8, &m.full[stage]);
-        ahead(k + kAhead + 1, far);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) pages[i] = pages[i + 1];
-        pages[kAhead] = far;
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t group = half == 0 ? Lay::kGroupA : Lay::kGroupB;
+          if (c >= ST && !__all_sync(0xffffffffu, wait(&m.empty[stage][half], c / ST - 1))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            // (the products that read the last one's are done with both halves' only behind the second wait,
+            // but the softmax warps, who alone look at it later, before the first)
+            if (half == 0) m.live[stage] = static_cast<uint64_t>(up) << 32 | lo;
+            mbar_arrive_expect_tx(&m.full[stage][half], n * (per / 8) * group);
+          }
+          __syncwarp();
+          if (page >= 0)
+            tma_tile_4d(smem + Lay::kv_off + stage * Lay::kStage + half * Lay::kHalfB + lane * (per / 8) * group,
+                        half == 0 ? &a.tmkv : &a.tmkv2, 0, 0, half * Lay::kBlocksA, page * (a.S / 8) + (t & (a.S - 1)) / 8,
+                        &m.full[stage][half]);
+        }
+        if (!ok) break;
       }
     }
     // nothing is in flight when the CTA leaves
-    for (uint32_t i = c > ST ? c - ST : 0; i < c; ++i) wait(&m.full[i % ST], i / ST);
+    for (uint32_t i = c > ST ? c - ST : 0; i < c; ++i)
+      for (int half = 0; half < 2; ++half) wait(&m.full[i % ST][half], i / ST);
   }
 
   // ---- softmax ---------------------------------------------------------------------------------------
-  // Warp w has tokens 16 w to 16 w + 15 of a step; a thread two of them (lane /
-  // 4 and 8 more) over the rows 8 j + 2 (lane % 4) and the next.
+  // Warp w of a warpgroup has tokens 16 w to 16 w + 15 of a step, the
+  // warpgroup half of the rows (in eights): a thread two tokens (lane / 4 and
+  // 8 more) over the rows 8 j + 2 (lane % 4) and the next.  The warpgroups
+  // have nothing to tell one another before the end.
   static __device__ void softmax(const LatentArgs& a, M& m, uint8_t* smem, uint32_t tmem, int rank, int warp, int lane) {
     bool dead = false;  // after a wait that ran out the others are skipped, and every barrier is still reached
     const auto wait = [&](uint64_t* bar, uint32_t phase) {
       if (!dead && !Waiter{a.err}(bar, phase)) dead = true;
     };
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const int tok = 16 * warp + (lane >> 2), cl = 2 * (lane & 3);
+    const int wg = warp >> 2, w4 = warp & 3, own_bar = 2 + wg;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+    const int tok = 16 * w4 + (lane >> 2);
+    // this lane's row of the matrices it addresses (lanes 0 to 15): token half, row r
+    const int st_r = lane & 7, st_g = 2 * w4 + ((lane >> 3) & 1);
     const uint32_t sm = smem_u32(smem);
-    // this lane's row of the matrices it addresses: block j (of a pair), token half, row r
-    const int st_r = lane & 7, st_half = (lane >> 3) & 1, st_j = lane >> 4;
-    const uint32_t st_hi = sm + Lay::kv_off + (NA - 1) * 1024 + (2 * warp + st_half) * Lay::kGroup + st_r * 128;
-    const uint32_t st_lo = sm + Lay::lo_off + (2 * warp + st_half) * 1024 + st_r * 128;
+    const uint32_t st_hi = sm + Lay::kv_off + Lay::kRopeBlock + st_g * Lay::kGroupB + st_r * 128;
+    const uint32_t st_lo = sm + Lay::lo_off + st_g * 1024 + st_r * 128;
+    const int cta = static_cast<int>(blockIdx.x) >> a.pair;
     uint32_t c = 0;
+    if (threadIdx.x < 2) a.record[slot_of(a, cta, threadIdx.x, rank)].n = 0;
     SegIter it(a.sh, m.plan, a.pair, rank);
     Seg s;
     while (it.next(s)) {
-      const int n = s.k1 - s.k0, nj = columns(s) / 8;
+      const int n = s.k1 - s.k0, nb = columns(s) / 16, j0 = wg * nb;  // the warpgroup's eights: j0 to j0 + nb
+      const int cl = 8 * j0 + 2 * (lane & 3);
+      const bool beside = side_by_side(s);
       const int pos_first = s.sq.pos0 + s.row0 / a.sh.H;
       if (threadIdx.x < kRows)
         m.lim[threadIdx.x] = threadIdx.x < s.n_rows ? s.sq.pos0 + (s.row0 + static_cast<int>(threadIdx.x)) / a.sh.H : -1;
       bar_sync(1, kSoftmax);
-      float nm[16], l[16];  // -m and the thread's sums
+      float nm[8], l[8];  // -m and the thread's sums
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      for (int i = 0; i < 8; ++i) {
         nm[i] = -kUnset;
         l[i] = 0.f;
       }
@@ -383,50 +444,50 @@ struct Kernel {
         const uint32_t stage = c % ST;
         wait(&m.s_full[c & 1], c >> 1);
         tc_fence_after();
-        uint32_t v[32];
-        tmem_ld_frag64(v, lanes + kTmemS + (c & 1) * kRows);
-        tmem_wait_ld();
+        uint32_t v[16];
+        tmem_ld_frag32(v, lanes + kTmemS + (c & 1) * kRows + 8 * j0);
         const int t0 = (s.k0 + i) * kStep;
         const uint64_t live = m.live[stage];
+        tmem_wait_ld();
         if (~live != 0 || t0 + kStep - 1 > pos_first) {
           const bool la = (live >> tok) & 1, lb = (live >> (tok + 8)) & 1;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
+          for (int j = 0; j < 4; ++j)
+            if (j < nb) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int lim = m.lim[8 * j + cl + e] - t0;
-              if (!la || tok > lim) v[4 * j + e] = 0xff800000u;  // -inf
-              if (!lb || tok + 8 > lim) v[4 * j + 2 + e] = 0xff800000u;
+              for (int e = 0; e < 2; ++e) {
+                const int lim = m.lim[8 * j + cl + e] - t0;
+                if (!la || tok > lim) v[4 * j + e] = 0xff800000u;  // -inf
+                if (!lb || tok + 8 > lim) v[4 * j + 2 + e] = 0xff800000u;
+              }
             }
         }
         const auto f = [&](int x) { return __uint_as_float(v[x]); };
         bool over = false;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < nj) {
+        for (int j = 0; j < 4; ++j)
+          if (j < nb) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float z = fmaf(fmaxf(f(4 * j + e), f(4 * j + 2 + e)), a.scale_log2, nm[2 * j + e]);
-              over |= z > kTop;
-            }
+            for (int e = 0; e < 2; ++e)
+              over |= fmaf(fmaxf(f(4 * j + e), f(4 * j + 2 + e)), a.scale_log2, nm[2 * j + e]) > kTop;
           }
-        if (bar_any(1, kSoftmax, over)) {
-          // some row's maximum is raised: the maxima of all rows over the step
+        if (bar_any(own_bar, 128, over)) {
+          // some row's maximum is raised: the maxima of the warpgroup's rows over the step
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < nj) {
+          for (int j = 0; j < 4; ++j)
+            if (j < nb) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 float x = fmaxf(f(4 * j + e), f(4 * j + 2 + e)) * a.scale_log2;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                if (lane < 4) m.top[warp][8 * j + cl + e] = x;
+                if (lane < 4) m.top[w4][8 * j + cl + e] = x;
               }
             }
-          bar_sync(1, kSoftmax);
+          bar_sync(own_bar, 128);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < nj) {
+          for (int j = 0; j < 4; ++j)
+            if (j < nb) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int col = 8 * j + cl + e, x = 2 * j + e;
@@ -437,31 +498,34 @@ struct Kernel {
                   nm[x] = kHead - top;
                   l[x] *= fac;
                 }
-                if (warp == 0 && lane < 4) m.factor[col] = fac;
+                if (w4 == 0 && lane < 4) m.factor[col] = fac;
               }
             }
-          bar_sync(1, kSoftmax);
           if (i > 0) {
-            wait(&m.empty[(c - 1) % ST], (c - 1) / ST);  // O holds earlier steps, all done
+            bar_sync(own_bar, 128);
+            wait(&m.empty[(c - 1) % ST][1], (c - 1) / ST);  // O holds earlier steps, all done
             tc_fence_after();
 #pragma unroll 1
-            for (int mt = 0; mt < R / 128; ++mt)
+            for (int x = 0; x < R / 128 * nb; ++x) {
+              const int col = 8 * (j0 + x % nb);
+              const uint32_t at = lanes + x / nb * kRows + col;
 #pragma unroll 1
-              for (int c0 = 0; c0 < 8 * nj; c0 += 16) {
-                uint32_t o[16];
-                tmem_ld16(o, lanes + mt * kRows + c0);
+              for (int side = 0; side <= (beside ? 16 * nb : 0); side += 16 * nb) {  // O's second part
+                uint32_t o[8];
+                tmem_ld8(o, at + side);
                 tmem_wait_ld();
 #pragma unroll
-                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * m.factor[c0 + x]);
-                tmem_st16(lanes + mt * kRows + c0, o);
+                for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * m.factor[col + y]);
+                tmem_st8(at + side, o);
               }
+            }
             tmem_wait_st();
           }
         }
-        uint32_t hi[16], lo[16];  // of block j: first token's pair, the second's
+        uint32_t hi[8], lo[8];  // of eight j: the first token's pair of rows, the second's
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < nj) {
+        for (int j = 0; j < 4; ++j)
+          if (j < nb) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               const float p0 = ex2(fmaf(f(4 * j + 2 * r), a.scale_log2, nm[2 * j]));
@@ -475,35 +539,47 @@ struct Kernel {
               }
             }
           }
-        if (PARTS == 2 && c > 0) wait(&m.empty[(c - 1) % ST], (c - 1) / ST);  // the second values' buffer is free
+        const uint32_t to = st_hi + stage * Lay::kStage;
+        if (PARTS == 2 && !beside && c > 0) wait(&m.empty[(c - 1) % ST][1], (c - 1) / ST);  // the second values' buffer is free
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (2 * q < nj) {
-            const uint32_t sw = ((2 * q + st_j) ^ st_r) << 4;
-            stmatrix_x4(st_hi + stage * Lay::kStage + sw, hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-            if constexpr (PARTS == 2) stmatrix_x4(st_lo + sw, lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+        for (int j = 0; j < 4; ++j)
+          if (j < nb) {
+            stmatrix_x2(to + (((j0 + j) ^ st_r) << 4), hi[2 * j], hi[2 * j + 1]);
+            if constexpr (PARTS == 2)
+              stmatrix_x2(beside ? to + (((2 * nb + j0 + j) ^ st_r) << 4) : st_lo + (((j0 + j) ^ st_r) << 4), lo[2 * j], lo[2 * j + 1]);
           }
         fence_proxy_async();
         tc_fence_before();
-        mbar_arrive(&m.p_full[c & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.p_full[c & 1]);
       }
 
       // ---- the segment's end: sums over the tokens' threads, then O^T by channels ----
+      bar_sync(own_bar, 128);  // the last raise's top and factor are read
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const int col = 8 * (x >> 1) + cl + (x & 1);
+      for (int j = 0; j < 4; ++j)
+        if (j < nb) {
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], o);
-        if (lane < 4) {
-          m.top[warp][col] = l[x];
-          if (warp == 0) m.factor[col] = -nm[x];
+          for (int e = 0; e < 2; ++e) {
+            float x = l[2 * j + e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane < 4) {
+              m.top[w4][8 * j + cl + e] = x;
+              if (w4 == 0) m.factor[8 * j + cl + e] = -nm[2 * j + e];
+            }
+          }
         }
-      }
-      if (n > 0) wait(&m.empty[(c - 1) % ST], (c - 1) / ST);
       bar_sync(1, kSoftmax);
       const int col = threadIdx.x;
       const size_t grow = static_cast<size_t>(s.sq.start) * a.sh.H + s.row0;
-      const int slot = slot_of(a, static_cast<int>(blockIdx.x) >> a.pair, s.k0_of_pair == 0, s.half);
+      const int slot = slot_of(a, cta, s.k0_of_pair == 0, s.half);
+      if (s.split && threadIdx.x == 128) {
+        const PartRange pr(m.plan, s);
+        const int parts = pr.c1 - pr.c0 + 1, x = cta - pr.c0;
+        const bool by_half = a.pair && min(1 << a.sh.rows_log2, s.sq.n * a.sh.H - (s.item << a.sh.rows_log2)) <= kRows;
+        a.record[slot] = {static_cast<int>(grow), s.n_rows, pr.c0, by_half ? 2 * parts : parts, by_half ? 2 * x + rank : x, by_half, rank, 0};
+      }
       if (col < s.n_rows) {
         const float sum = (m.top[0][col] + m.top[1][col]) + (m.top[2][col] + m.top[3][col]), mx = m.factor[col];
         m.inv[col] = sum == 0.f ? 0.f : 1.f / sum;
@@ -514,16 +590,25 @@ struct Kernel {
           a.lse[grow + col] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
         }
       }
+      if (n > 0) wait(&m.empty[(c - 1) % ST][1], (c - 1) / ST);
       bar_sync(1, kSoftmax);
       tc_fence_after();
       if (n > 0) {
+        // a warpgroup takes every other 128 channels
 #pragma unroll 1
-        for (int mt = 0; mt < R / 128; ++mt) {
-          const int ch = mt * 128 + warp * 32 + lane;
+        for (int mt = wg; mt < R / 128; mt += 2) {
+          const int ch = mt * 128 + w4 * 32 + lane;
 #pragma unroll 1
           for (int c0 = 0; c0 < s.n_rows; c0 += 16) {
             uint32_t o[16];
             tmem_ld16(o, lanes + mt * kRows + c0);
+            if (beside) {
+              uint32_t o2[16];
+              tmem_ld16(o2, lanes + mt * kRows + 16 * nb + c0);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(o2[x]));
+            }
             tmem_wait_ld();
             if (s.split) {
               float* dst = a.part + (static_cast<size_t>(slot) * a.part_rows + c0) * R + ch;
@@ -543,14 +628,14 @@ struct Kernel {
           }
         }
       }
-      tc_fence_before();     // the reads of O come before the next segment's first product
+      tc_fence_before();      // the reads of O come before the next segment's first product
       bar_sync(1, kSoftmax);  // lim, top, factor and inv are read
     }
   }
 };
 
 template <typename T, int R, int PARTS>
-__global__ void __launch_bounds__(256, 1) k_latent(const __grid_constant__ LatentArgs a) {
+__global__ void __launch_bounds__(384, 1) k_latent(const __grid_constant__ LatentArgs a) {
   using K = Kernel<T, R, PARTS>;
   using Lay = typename K::Lay;
   using M = typename K::M;
@@ -563,17 +648,32 @@ __global__ void __launch_bounds__(256, 1) k_latent(const __grid_constant__ Laten
     mbar_init(&m.q_full, 1);
     mbar_init(&m.q_empty, 1);
     for (int i = 0; i < K::ST; ++i) {
-      mbar_init(&m.full[i], 1);
-      mbar_init(&m.empty[i], 1);
+      for (int half = 0; half < 2; ++half) {
+        mbar_init(&m.full[i][half], 1);
+        mbar_init(&m.empty[i][half], 1);
+      }
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.s_full[i], 1);
-      mbar_init(&m.p_full[i], K::kSoftmax);
+      mbar_init(&m.p_full[i], K::kSoftmax / 32);
       mbar_init(&m.drain[i], 1);
     }
     mbar_fence_init();
   }
   if (warp == K::kSWarp) tmem_alloc(&m.tmem, kTmemCols);
+  if (threadIdx.x == 32 * K::kLoadWarp) {
+    tma_prefetch_desc(&a.tmkv);
+    tma_prefetch_desc(&a.tmkv2);
+  }
+  if (threadIdx.x == 32 * K::kQWarp) tma_prefetch_desc(&a.tmq);
+  {
+    // the chain before the first copy is lengths, plan, pages: what they are
+    // read from (whatever it will hold) comes to L2 meanwhile
+    const long long at = (static_cast<long long>(blockIdx.x) * K::kThreads + threadIdx.x) * 128;
+    if (at < static_cast<long long>(a.sh.B) * a.MP * 4) prefetch_l2(reinterpret_cast<const uint8_t*>(a.page_table) + at);
+    if (threadIdx.x * 32 <= a.sh.B) prefetch_l2(a.sh.q_start + threadIdx.x * 32);
+    if (threadIdx.x * 32 < a.sh.B) prefetch_l2(a.sh.seq_lens + threadIdx.x * 32);
+  }
   pdl_wait();
   if (warp == 0) make_plan(a.sh, &m.plan, a.err, lane, static_cast<int>(blockIdx.x) >> a.pair, static_cast<int>(gridDim.x) >> a.pair);
   tc_fence_before();
@@ -581,7 +681,7 @@ __global__ void __launch_bounds__(256, 1) k_latent(const __grid_constant__ Laten
   tc_fence_after();
   const uint32_t tmem = m.tmem;
 
-  if (warp < 4) {
+  if (warp < K::kLoadWarp) {
     K::softmax(a, m, smem, tmem, rank, warp, lane);
   } else if (warp == K::kLoadWarp) {
     K::load_kv(a, m, smem, rank, lane);
@@ -607,74 +707,77 @@ __global__ void __launch_bounds__(256, 1) k_latent(const __grid_constant__ Laten
 }
 
 // ---- the parts of an item joined ------------------------------------------------------------
-// CTA (c, y) takes, of each item that CTA c had a part of, its share of
-// (row, 128 channels) units; the parts of a unit are shared out to 1 to 8 warps.
-constexpr int kJoinWarps = 8, kJoinY = 2;
+// CTA (slot, y) takes its share of the (row, 128 channels) units of the rows
+// that the slot's part is of; a unit's parts are shared out to 1 to 16 warps.
+constexpr int kJoinWarps = 16, kJoinY = 4;
 
 template <typename T, int R>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_constant__ LatentArgs a) {
-  __shared__ Plan plan;
+  constexpr int kPieces = R / 128, kWeights = kMaxCtas / 32;
   __shared__ float4 acc_s[kJoinWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const int c = blockIdx.x;
-  if (warp == 0) make_plan(a.sh, &plan, a.err, lane, c, gridDim.x);
-  __syncthreads();
+  const int4 r0 = __ldcg(reinterpret_cast<const int4*>(a.record + blockIdx.x)), r1 = __ldcg(reinterpret_cast<const int4*>(a.record + blockIdx.x) + 1);
   pdl_trigger();
-  PartIter<LatentItems> it(a.sh, plan);
-  Part s;
-  while (it.next(s)) {
-    if (s.whole()) continue;
-    const PartRange pr(plan, s);
-    const int row0 = s.item << a.sh.rows_log2, n_rows = min(1 << a.sh.rows_log2, s.sq.n * a.sh.H - row0);
-    const bool by_half = a.pair && n_rows <= kRows;  // the pair's CTAs had halves of the steps
-    const int parts = (pr.c1 - pr.c0 + 1) << (by_half ? 1 : 0);
-    const int wlog = parts >= 32 ? 3 : parts >= 16 ? 2 : parts >= 8 ? 1 : 0;  // warps to a unit
-    const int sub = warp & ((1 << wlog) - 1), per_round = kJoinWarps >> wlog;
-    const int units = n_rows * (R / 128), shares = (pr.c1 - pr.c0 + 1) * kJoinY;
-    for (int u0 = ((c - pr.c0) * kJoinY + static_cast<int>(blockIdx.y)) * per_round; u0 < units; u0 += shares * per_round) {
-      const int u = u0 + (warp >> wlog);
-      const bool live = u < units;
-      const int row = live ? u / (R / 128) : 0, ch = (u % (R / 128)) * 128 + lane * 4;
-      const auto slot = [&](int i) {
-        const int cc = pr.c0 + (by_half ? i >> 1 : i);
-        return slot_of(a, cc, cc == pr.c0, by_half ? i & 1 : row >> 6);
-      };
-      float mm = kUnset, sum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int base = 0; base < parts; base += 32) {
-        const int i = base + lane;
-        if (i < parts && __ldcg(a.part_l + slot(i) * kRows + (row & 63)) != 0.f)
-          mm = fmaxf(mm, __ldcg(a.part_m + slot(i) * kRows + (row & 63)));
+  const int row0 = r0.x, n_rows = r0.y, c0 = r0.z, parts = r0.w, by_half = r1.y, half = r1.z;
+  if (parts == 0) return;
+  // warps to a unit: at most ten parts a warp with 16, four with fewer
+  const int wlog = parts > 32 ? 4 : parts > 16 ? 3 : parts > 8 ? 2 : parts > 4 ? 1 : 0;
+  const int sub = warp & ((1 << wlog) - 1), per_round = kJoinWarps >> wlog, units = n_rows * kPieces;
+  const auto slot = [&](int i) {
+    const int c = by_half ? i >> 1 : i;
+    return slot_of(a, c0 + c, c == 0, by_half ? i & 1 : half);
+  };
+  for (int u0 = (r1.x * kJoinY + static_cast<int>(blockIdx.y)) * per_round; u0 < units; u0 += parts * kJoinY * per_round) {
+    const int u = u0 + (warp >> wlog);
+    const bool live = u < units;
+    const int row = live ? u / kPieces : 0, ch = (u % kPieces) * 128 + lane * 4;
+    // a lane has the weights of every 32nd part
+    float w[kWeights], l[kWeights], mm = kUnset, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWeights; ++k) {
+      const int i = 32 * k + lane, at = slot(min(i, parts - 1)) * kRows + row;
+      w[k] = l[k] = 0.f;
+      if (32 * k < parts) {
+        l[k] = i < parts ? __ldcg(a.part_l + at) : 0.f;
+        w[k] = __ldcg(a.part_m + at);
       }
-      mm = warp_max(mm);
-      for (int base = 0; base < parts; base += 32) {
-        const int i = base + lane;
-        float w = 0.f;
-        if (i < parts) {
-          const float l = __ldcg(a.part_l + slot(i) * kRows + (row & 63));
-          if (l != 0.f) {  // else the part saw nothing, and may not have written its O
-            w = ex2(__ldcg(a.part_m + slot(i) * kRows + (row & 63)) - mm);
-            sum += w * l;
-          }
-        }
-        const int end = min(32, parts - base);
-#pragma unroll 4
-        for (int q = sub; q < end; q += 1 << wlog) {
-          const float wq = __shfl_sync(0xffffffffu, w, q);
-          const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(slot(base + q)) * a.part_rows + (row & 63)) * R + ch));
-          if (wq != 0.f) {
-            acc.x = fmaf(wq, o.x, acc.x);
-            acc.y = fmaf(wq, o.y, acc.y);
-            acc.z = fmaf(wq, o.z, acc.z);
-            acc.w = fmaf(wq, o.w, acc.w);
-          }
-        }
+    }
+#pragma unroll
+    for (int k = 0; k < kWeights; ++k)
+      if (l[k] != 0.f) mm = fmaxf(mm, w[k]);  // else the part saw nothing, and may not have written its O
+    mm = warp_max(mm);
+#pragma unroll
+    for (int k = 0; k < kWeights; ++k) {
+      w[k] = l[k] != 0.f ? ex2(w[k] - mm) : 0.f;
+      sum = fmaf(w[k], l[k], sum);
+    }
+    sum = warp_sum(sum);
+    // this warp's parts sub + (q << wlog): all of them on their way at once
+    float4 o[2 * kWeights];
+#pragma unroll
+    for (int q = 0; q < 2 * kWeights; ++q) {
+      const int i = sub + (q << wlog);
+      o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if ((q < 4 || wlog == 4) && i < parts)
+        o[q] = __ldcg(reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(slot(i)) * a.part_rows + row) * R + ch));
+    }
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int q = 0; q < 2 * kWeights; ++q) {
+      if (q >= 4 && wlog != 4) break;
+      const float wq = __shfl_sync(0xffffffffu, q < 2 || wlog == 4 ? w[q >> 1] : w[0], (sub + (q << wlog)) & 31);
+      if (wq != 0.f) {
+        acc.x = fmaf(wq, o[q].x, acc.x);
+        acc.y = fmaf(wq, o[q].y, acc.y);
+        acc.z = fmaf(wq, o[q].z, acc.z);
+        acc.w = fmaf(wq, o[q].w, acc.w);
       }
-      sum = warp_sum(sum);
+    }
+    if (wlog > 0) {  // the same in the whole CTA
       acc_s[warp][lane] = acc;
       __syncthreads();
-      if (live && sub == 0) {
+      if (sub == 0)
         for (int q = 1; q < 1 << wlog; ++q) {
           const float4 o = acc_s[warp + q][lane];
           acc.x += o.x;
@@ -682,24 +785,25 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_co
           acc.z += o.z;
           acc.w += o.w;
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const size_t grow = static_cast<size_t>(s.sq.start) * a.sh.H + row0 + row;
-        const uint2 w = make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + grow * R + ch) = w;
-        if (a.lse && ch < 4 && lane == 0) a.lse[grow] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
-      }
       __syncthreads();
+    }
+    if (live && sub == 0) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t grow = static_cast<size_t>(row0) + row;
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + grow * R + ch) =
+          make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+      if (a.lse && ch == 0) a.lse[grow] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
     }
   }
 }
 
 // ---- host ------------------------------------------------------------------------------------
 
-size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 int part_rows(const spg_latent_params& p, int total_q) {
   return static_cast<int>(std::max<long long>(1, std::min<long long>(kRows, static_cast<long long>(total_q) * p.num_heads)));
 }
 constexpr int kSlots = 2 * kMaxCtas;
+static_assert(sizeof(PartRecord) == 32, "two 16-byte loads");
 
 template <typename T, int R, int PARTS>
 cudaError_t latent_typed(const spg_latent_params& p, LatentArgs& a, const void* q_lat, const void* pool, cudaStream_t st) {
@@ -708,9 +812,11 @@ cudaError_t latent_typed(const spg_latent_params& p, LatentArgs& a, const void* 
   const uint64_t qd[3] = {64, static_cast<uint64_t>(a.sh.total_q) * p.num_heads, K::NA}, qs[2] = {row, 128};
   const uint32_t qb[3] = {64, 8, K::NA};
   const uint64_t kd[4] = {64, 8, K::NA, static_cast<uint64_t>(p.num_phys_pages) * (p.page_size / 8)}, ks[3] = {row, 128, 8 * row};
-  const uint32_t kb[4] = {64, 8, K::NA, static_cast<uint32_t>(std::min(p.page_size, kStep) / 8)};
+  uint32_t kb[4] = {64, 8, Layout<R>::kBlocksA, static_cast<uint32_t>(std::min(p.page_size, kStep) / 8)};
   if (!make_tmap16(&a.tmq, p.dtype, q_lat, 3, qd, qs, qb) || !make_tmap16(&a.tmkv, p.dtype, pool, 4, kd, ks, kb))
     return cudaErrorNotSupported;
+  kb[2] = Layout<R>::kBlocksB;
+  if (!make_tmap16(&a.tmkv2, p.dtype, pool, 4, kd, ks, kb)) return cudaErrorNotSupported;
   const auto kern = k_latent<T, R, PARTS>;
   const size_t smem = 1024 + K::Lay::misc + sizeof(typename K::M);
   static_assert(1024 + K::Lay::misc + sizeof(typename K::M) <= 232448, "shared memory of a CTA");
@@ -719,13 +825,13 @@ cudaError_t latent_typed(const spg_latent_params& p, LatentArgs& a, const void* 
   const int ctas = std::min(device_sm_count(), kMaxCtas) >> a.pair;
   e = launch_pdl(kern, dim3(ctas << a.pair), dim3(K::kThreads), smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_latent_join<T, R>, dim3(ctas, kJoinY), dim3(32 * kJoinWarps), 0, st, a);
+  return launch_pdl(k_latent_join<T, R>, dim3(2 * ctas << a.pair, kJoinY), dim3(32 * kJoinWarps), 0, st, a);
 }
 
 }  // namespace
 
 size_t latent_workspace_bytes(const spg_latent_params& p, int total_q) {
-  return 256 + 2 * round256(sizeof(float) * kSlots * kRows) + sizeof(float) * kSlots * part_rows(p, total_q) * p.latent_dim;
+  return 256 + sizeof(PartRecord) * kSlots + 2 * sizeof(float) * kSlots * kRows + sizeof(float) * kSlots * part_rows(p, total_q) * p.latent_dim;
 }
 
 cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows& r, const void* q_lat, const void* pool,
@@ -741,15 +847,16 @@ cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows
   // two CTAs over the same steps where sequences have more than 64 rows (on average)
   a.pair = static_cast<long long>(r.total_q) * p.num_heads > static_cast<long long>(kRows) * p.batch || p.num_heads > kRows ? 1 : 0;
   a.sh.rows_log2 = 6 + a.pair;
-  a.pool = static_cast<const uint8_t*>(pool);
   a.page_table = r.page_table;
+  a.pool = static_cast<const uint8_t*>(pool);
   a.out = o_lat;
   a.lse = lse;
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.err = reinterpret_cast<int32_t*>(base);
-  a.part_m = reinterpret_cast<float*>(base + 256);
-  a.part_l = reinterpret_cast<float*>(base + 256 + round256(sizeof(float) * kSlots * kRows));
-  a.part = reinterpret_cast<float*>(base + 256 + 2 * round256(sizeof(float) * kSlots * kRows));
+  a.record = reinterpret_cast<PartRecord*>(base + 256);
+  a.part_m = reinterpret_cast<float*>(a.record + kSlots);
+  a.part_l = a.part_m + kSlots * kRows;
+  a.part = a.part_l + kSlots * kRows;
   a.S = p.page_size;
   a.s_log2 = log2_of(p.page_size);
   a.MP = p.max_pages_per_seq;
