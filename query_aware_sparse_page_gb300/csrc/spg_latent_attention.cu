@@ -49,7 +49,7 @@ constexpr float kUnset = -1e30f;  // m of a row that has seen nothing
 constexpr float kHead = 7.f, kTop = 15.f;  // the weights of a row are at most 2^15, under fp16's 65504
 
 // sum of floor((a i + b) / m) over 0 <= i < n, by the steps of Euclid's algorithm
-__device__ inline unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a, unsigned long long b) {
+__device__ __noinline__ unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a, unsigned long long b) {
   unsigned long long sum = 0;
   while (n > 0) {
     if (a >= m) {
@@ -136,6 +136,8 @@ struct SegIter : PartIter<LatentItems> {
 struct PartRecord {
   int row, n_rows, c0, n, index, by_half, half, pad;  // first row of the chunk; this part's number
 };
+static_assert(sizeof(PartRecord) == 32, "two 16-byte loads");
+constexpr int kSlots = 2 * kMaxCtas;
 
 struct LatentArgs {
   LatentItems sh;
@@ -145,8 +147,9 @@ struct LatentArgs {
   void* out;
   float* lse;
   int32_t* err;
-  float *part, *part_m, *part_l;  // [2 * CTAs][part_rows][R], [2 * CTAs][64] twice
-  PartRecord* record;             // [2 * CTAs], n = 0 for a slot without a part
+  float* part;        // [2 * CTAs][part_rows][R]
+  float2* part_ml;    // m and l, [64][2 * CTAs]: a row's parts are neighbours
+  PartRecord* record;  // [2 * CTAs], n = 0 for a slot without a part
   int S, s_log2, MP, n_phys, part_rows, pair;
   float scale_log2;
 };
@@ -178,10 +181,12 @@ struct Misc {
   uint64_t live[ST];  // tokens of a step that are there
   Plan plan;
   uint32_t tmem;
-  int lim[kRows];       // last token a row sees
+  union {
+    int lim[kRows];     // last token a row sees
+    float inv[kRows];   // at the end
+  };
   float top[4][kRows];  // largest logit of a step, per 16 tokens; at the end the sums
   float factor[kRows];  // what O is rescaled by; at the end the maxima
-  float inv[kRows];
 };
 
 template <typename T, int R, int PARTS>
@@ -584,8 +589,7 @@ struct Kernel {
         const float sum = (m.top[0][col] + m.top[1][col]) + (m.top[2][col] + m.top[3][col]), mx = m.factor[col];
         m.inv[col] = sum == 0.f ? 0.f : 1.f / sum;
         if (s.split) {
-          __stcg(a.part_m + slot * kRows + col, mx);
-          __stcg(a.part_l + slot * kRows + col, sum);
+          __stcg(a.part_ml + col * kSlots + slot, make_float2(mx, sum));
         } else if (a.lse) {
           a.lse[grow + col] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
         }
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(384, 1) k_latent(const __grid_constant__ Laten
   } else if (warp == K::kQWarp) {
     if (lane == 0) K::load_q(a, m, smem, rank);
     __syncwarp();
-  } else {
+  } else if (warp != K::kLoadWarp) {
     const bool ok = warp == K::kSWarp ? K::issue_s(a, m, smem, tmem, rank, lane) : K::issue_pv(a, m, smem, tmem, rank);
     if (!ok) {  // products in flight end before TMEM goes back
       uint64_t* bar = &m.drain[warp - K::kSWarp];
@@ -707,28 +711,22 @@ __global__ void __launch_bounds__(384, 1) k_latent(const __grid_constant__ Laten
 }
 
 // ---- the parts of an item joined ------------------------------------------------------------
-// CTA (slot, y) takes its share of the (row, 128 channels) units of the rows
-// that the slot's part is of; a unit's parts are shared out to 1 to 16 warps.
+// CTA (x, y) takes, for each part that CTA x of the first launch left, its
+// share of the (row, 128 channels) units of that part's rows; a unit's parts
+// are shared out to 1 to 16 warps.
 constexpr int kJoinWarps = 16, kJoinY = 4;
 
 template <typename T, int R>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_constant__ LatentArgs a) {
+__device__ __forceinline__ void join_part(const LatentArgs& a, const PartRecord& rec, float4 (*acc_s)[32], int warp, int lane) {
   constexpr int kPieces = R / 128, kWeights = kMaxCtas / 32;
-  __shared__ float4 acc_s[kJoinWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  const int4 r0 = __ldcg(reinterpret_cast<const int4*>(a.record + blockIdx.x)), r1 = __ldcg(reinterpret_cast<const int4*>(a.record + blockIdx.x) + 1);
-  pdl_trigger();
-  const int row0 = r0.x, n_rows = r0.y, c0 = r0.z, parts = r0.w, by_half = r1.y, half = r1.z;
-  if (parts == 0) return;
   // warps to a unit: at most ten parts a warp with 16, four with fewer
-  const int wlog = parts > 32 ? 4 : parts > 16 ? 3 : parts > 8 ? 2 : parts > 4 ? 1 : 0;
-  const int sub = warp & ((1 << wlog) - 1), per_round = kJoinWarps >> wlog, units = n_rows * kPieces;
+  const int wlog = rec.n > 32 ? 4 : rec.n > 16 ? 3 : rec.n > 8 ? 2 : rec.n > 4 ? 1 : 0;
+  const int sub = warp & ((1 << wlog) - 1), per_round = kJoinWarps >> wlog, units = rec.n_rows * kPieces;
   const auto slot = [&](int i) {
-    const int c = by_half ? i >> 1 : i;
-    return slot_of(a, c0 + c, c == 0, by_half ? i & 1 : half);
+    const int c = rec.by_half ? i >> 1 : i;
+    return slot_of(a, rec.c0 + c, c == 0, rec.by_half ? i & 1 : rec.half);
   };
-  for (int u0 = (r1.x * kJoinY + static_cast<int>(blockIdx.y)) * per_round; u0 < units; u0 += parts * kJoinY * per_round) {
+  for (int u0 = (rec.index * kJoinY + static_cast<int>(blockIdx.y)) * per_round; u0 < units; u0 += rec.n * kJoinY * per_round) {
     const int u = u0 + (warp >> wlog);
     const bool live = u < units;
     const int row = live ? u / kPieces : 0, ch = (u % kPieces) * 128 + lane * 4;
@@ -736,12 +734,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_co
     float w[kWeights], l[kWeights], mm = kUnset, sum = 0.f;
 #pragma unroll
     for (int k = 0; k < kWeights; ++k) {
-      const int i = 32 * k + lane, at = slot(min(i, parts - 1)) * kRows + row;
-      w[k] = l[k] = 0.f;
-      if (32 * k < parts) {
-        l[k] = i < parts ? __ldcg(a.part_l + at) : 0.f;
-        w[k] = __ldcg(a.part_m + at);
-      }
+      const float2 ml = 32 * k < rec.n ? __ldcg(a.part_ml + row * kSlots + slot(min(32 * k + lane, rec.n - 1))) : make_float2(0.f, 0.f);
+      w[k] = ml.x;
+      l[k] = 32 * k + lane < rec.n ? ml.y : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < kWeights; ++k)
@@ -753,13 +748,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_co
       sum = fmaf(w[k], l[k], sum);
     }
     sum = warp_sum(sum);
-    // this warp's parts sub + (q << wlog): all of them on their way at once
+    // this warp's rec.n sub + (q << wlog): all of them on their way at once
     float4 o[2 * kWeights];
 #pragma unroll
     for (int q = 0; q < 2 * kWeights; ++q) {
       const int i = sub + (q << wlog);
       o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if ((q < 4 || wlog == 4) && i < parts)
+      if ((q < 4 || wlog == 4) && i < rec.n)
         o[q] = __ldcg(reinterpret_cast<const float4*>(a.part + (static_cast<size_t>(slot(i)) * a.part_rows + row) * R + ch));
     }
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -789,11 +784,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_co
     }
     if (live && sub == 0) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const size_t grow = static_cast<size_t>(row0) + row;
+      const size_t grow = static_cast<size_t>(rec.row) + row;
       *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + grow * R + ch) =
           make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
       if (a.lse && ch == 0) a.lse[grow] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * kLn2;
     }
+  }
+}
+
+template <typename T, int R>
+__global__ void __launch_bounds__(32 * kJoinWarps, 2) k_latent_join(const __grid_constant__ LatentArgs a) {
+  __shared__ float4 acc_s[kJoinWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  // the two slots of a CTA of the first launch
+  const PartRecord* rec = a.record + slot_of(a, static_cast<int>(blockIdx.x) >> a.pair, false, blockIdx.x & a.pair);
+  const int4 r0[2] = {__ldcg(reinterpret_cast<const int4*>(rec)), __ldcg(reinterpret_cast<const int4*>(rec + (1 << a.pair)))};
+  const int4 r1[2] = {__ldcg(reinterpret_cast<const int4*>(rec) + 1), __ldcg(reinterpret_cast<const int4*>(rec + (1 << a.pair)) + 1)};
+  pdl_trigger();
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int4 ra = which == 0 ? r0[0] : r0[1], rb = which == 0 ? r1[0] : r1[1];
+    if (ra.w > 0) join_part<T, R>(a, {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, 0}, acc_s, warp, lane);
   }
 }
 
@@ -802,8 +814,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_latent_join(const __grid_co
 int part_rows(const spg_latent_params& p, int total_q) {
   return static_cast<int>(std::max<long long>(1, std::min<long long>(kRows, static_cast<long long>(total_q) * p.num_heads)));
 }
-constexpr int kSlots = 2 * kMaxCtas;
-static_assert(sizeof(PartRecord) == 32, "two 16-byte loads");
 
 template <typename T, int R, int PARTS>
 cudaError_t latent_typed(const spg_latent_params& p, LatentArgs& a, const void* q_lat, const void* pool, cudaStream_t st) {
@@ -825,13 +835,13 @@ cudaError_t latent_typed(const spg_latent_params& p, LatentArgs& a, const void* 
   const int ctas = std::min(device_sm_count(), kMaxCtas) >> a.pair;
   e = launch_pdl(kern, dim3(ctas << a.pair), dim3(K::kThreads), smem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_latent_join<T, R>, dim3(2 * ctas << a.pair, kJoinY), dim3(32 * kJoinWarps), 0, st, a);
+  return launch_pdl(k_latent_join<T, R>, dim3(ctas << a.pair, kJoinY), dim3(32 * kJoinWarps), 0, st, a);
 }
 
 }  // namespace
 
 size_t latent_workspace_bytes(const spg_latent_params& p, int total_q) {
-  return 256 + sizeof(PartRecord) * kSlots + 2 * sizeof(float) * kSlots * kRows + sizeof(float) * kSlots * part_rows(p, total_q) * p.latent_dim;
+  return 256 + sizeof(PartRecord) * kSlots + sizeof(float2) * kSlots * kRows + sizeof(float) * kSlots * part_rows(p, total_q) * p.latent_dim;
 }
 
 cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows& r, const void* q_lat, const void* pool,
@@ -854,9 +864,8 @@ cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.err = reinterpret_cast<int32_t*>(base);
   a.record = reinterpret_cast<PartRecord*>(base + 256);
-  a.part_m = reinterpret_cast<float*>(a.record + kSlots);
-  a.part_l = a.part_m + kSlots * kRows;
-  a.part = a.part_l + kSlots * kRows;
+  a.part_ml = reinterpret_cast<float2*>(a.record + kSlots);
+  a.part = reinterpret_cast<float*>(a.part_ml + kSlots * kRows);
   a.S = p.page_size;
   a.s_log2 = log2_of(p.page_size);
   a.MP = p.max_pages_per_seq;

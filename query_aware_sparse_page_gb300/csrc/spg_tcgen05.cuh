@@ -169,6 +169,16 @@ __device__ __forceinline__ void tma_tile_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// with an L2 policy
+__device__ __forceinline__ void tma_tile_4d_hint(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar,
+                                                 uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+      "%4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)), "l"(pol)
+      : "memory");
+}
+
 // ---- packed fp32 pairs --------------------------------------------------------------------
 __device__ __forceinline__ uint64_t f32x2(float a, float b) {
   uint64_t r;
