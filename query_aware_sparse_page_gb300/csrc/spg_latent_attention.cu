@@ -748,7 +748,7 @@ __device__ __forceinline__ void join_part(const LatentArgs& a, const PartRecord&
       sum = fmaf(w[k], l[k], sum);
     }
     sum = warp_sum(sum);
-    // this warp's rec.n sub + (q << wlog): all of them on their way at once
+    // this warp's parts sub + (q << wlog): all of them on their way at once
     float4 o[2 * kWeights];
 #pragma unroll
     for (int q = 0; q < 2 * kWeights; ++q) {
