@@ -16,7 +16,8 @@
  *   4. run split-K flash-decoding over the selected pages only and merge the
  *      splits by log-sum-exp (SALS SFAA 四阶段 flow; AICPU Tiling challenge 2).
  * Around the steps, chunks of new tokens: into the cache, attended, and the
- * cache evicted by accumulated attention weight (paged_*, further down).
+ * cache evicted by accumulated attention weight (paged_*, further down); and the
+ * same over a cache of one latent vector per token (*latent*, further down).
  *
  * Conventions for every entry point
  *   - All tensor pointers are DEVICE pointers, 16-byte aligned, contiguous
@@ -510,8 +511,10 @@ spg_status latent_project(const spg_latent_params* p, int32_t total_q, const voi
 /* Causal attention of a chunk over the cache its tokens are already in: row i
  * of sequence b attends the tokens t <= seq_lens[b] - n_b + i,
  *   z = softmax_scale * q_lat[i][h] . pool[t],  o_lat[i][h] = sum softmax(z)_t c_t
+ *   o_lat        must not overlap an input
  *   lse          [total_q][H] fp32 natural-log log-sum-exp (may be NULL)
- * A row that sees no token (its pages are bad) gets o_lat = 0 and lse = -inf.
+ * A row that sees no token (its pages are bad) gets o_lat = 0 and lse = -inf, a
+ * row whose queries hold a NaN NaN in both.
  * Rows past q_start[B] are neither read for a result nor written.  Logits,
  * softmax statistics and sums in fp32; probabilities enter the second product
  * as in paged_chunk_attention (spg_set_chunk_parts). */

@@ -27,8 +27,9 @@ int chunk_parts();
 bool make_tmap16(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                  const uint32_t* box);
 
-cudaError_t launch_latent_append(const spg_latent_params& p, const spg_rope* rope, const LatentAppend& r, int32_t* err,
-                                 cudaStream_t stream);
+// rope (may be NULL) with what rope_freqs gave for it
+cudaError_t launch_latent_append(const spg_latent_params& p, const spg_rope* rope, const double* inv_freq, double mscale,
+                                 const LatentAppend& r, int32_t* err, cudaStream_t stream);
 // project: x = o_lat [total_q][H][r] times W_uv, else x = q (rows q_stride apart) times W_uk
 cudaError_t launch_latent_heads(const spg_latent_params& p, bool project, int total_q, const void* x, int64_t x_stride,
                                 const void* w_kv, void* y, cudaStream_t stream);

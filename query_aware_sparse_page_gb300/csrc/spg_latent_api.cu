@@ -103,8 +103,8 @@ spg_status paged_latent_append(const spg_latent_params* p, const spg_rope* rope,
                                void* q_lat, void* ws, size_t ws_bytes, spg_stream_t stream) {
   spg_status s = check_rows(p, total_q);
   if (s != SPG_OK) return s;
+  double inv[32], m = 1.0;  // rope_dim / 2 pairs
   if (rope) {
-    double inv[32], m;  // rope_dim / 2 pairs
     if (!spg::rope_freqs(*rope, p->rope_dim, inv, &m)) return SPG_EINVAL;
     if (rope->rot_dim % 16) return SPG_EUNSUPPORTED;  // whole 16-byte pieces of both halves
   }
@@ -133,7 +133,7 @@ spg_status paged_latent_append(const spg_latent_params* p, const spg_rope* rope,
   r.eps = eps;
   r.pool = pool;
   r.q_lat = q_lat;
-  return cuda_status(spg::launch_latent_append(*p, rope, r, static_cast<int32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(spg::launch_latent_append(*p, rope, inv, m, r, static_cast<int32_t*>(ws), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 spg_status latent_absorb(const spg_latent_params* p, int32_t total_q, const void* q, int64_t q_stride, const void* w_kv,
@@ -164,7 +164,7 @@ spg_status paged_latent_attention(const spg_latent_params* p, int32_t total_q, c
   if ((s = check_ws(p, total_q, ws, ws_bytes)) != SPG_OK) return s;
   if (total_q == 0) return SPG_OK;
   if (!ok_ptr(q_lat) || !ok_ptr(q_start) || !ok_ptr(pool) || !ok_ptr(page_table) || !ok_ptr(seq_lens) || !ok_ptr(o_lat) ||
-      !aligned16(lse))
+      !aligned16(lse) || q_lat == o_lat)
     return SPG_EINVAL;
   const spg::LatentRows r{q_start, page_table, seq_lens, total_q};
   return cuda_status(spg::launch_latent_attention(*p, r, q_lat, pool, o_lat, lse, spg::chunk_parts(), ws,

@@ -175,18 +175,16 @@ cudaError_t append_typed(const spg_latent_params& p, const AppendArgs& a, bool h
 
 }  // namespace
 
-cudaError_t launch_latent_append(const spg_latent_params& p, const spg_rope* rope, const LatentAppend& r, int32_t* err,
-                                 cudaStream_t stream) {
+cudaError_t launch_latent_append(const spg_latent_params& p, const spg_rope* rope, const double* inv_freq, double mscale,
+                                 const LatentAppend& r, int32_t* err, cudaStream_t stream) {
   AppendArgs a{};
   a.mscale = 1.f;
   bool half = true;
   if (rope) {
-    double inv[kPairs], m = 1.0;
-    if (!rope_freqs(*rope, kRope, inv, &m)) return cudaErrorInvalidValue;
     a.rot = rope->rot_dim == 0 ? kRope : rope->rot_dim;
     for (int i = 0; i < a.rot / 2; ++i)
-      a.turns[i] = static_cast<unsigned long long>(std::ldexp(inv[i] / 6.283185307179586476925, 64));
-    a.mscale = static_cast<float>(m);
+      a.turns[i] = static_cast<unsigned long long>(std::ldexp(inv_freq[i] / 6.283185307179586476925, 64));
+    a.mscale = static_cast<float>(mscale);
     half = rope->layout == SPG_ROPE_HALF;
   }
   a.c = r.c;

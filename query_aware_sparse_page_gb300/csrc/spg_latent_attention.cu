@@ -45,7 +45,7 @@ constexpr int kRows = 64;   // rows of a CTA: columns of S^T and O^T
 constexpr int kStep = 64;   // tokens of a step
 constexpr int kRope = 64;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O^T: R / 128 times 64 columns, then two S^T of 64
-constexpr float kUnset = -1e30f;  // m of a row that has seen nothing
+constexpr float kUnset = -1.7e38f;  // m of a row that has seen nothing: half of the range, so that any logit's distance from it is finite
 constexpr float kHead = 7.f, kTop = 15.f;  // the weights of a row are at most 2^15, under fp16's 65504
 
 // sum of floor((a i + b) / m) over 0 <= i < n, by the steps of Euclid's algorithm
@@ -467,6 +467,10 @@ struct Kernel {
               }
             }
         }
+        // the scaled logits, rounded here once: m is one of them, and what it is
+        // taken from has to be the same however large they are
+#pragma unroll
+        for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * a.scale_log2);
         const auto f = [&](int x) { return __uint_as_float(v[x]); };
         bool over = false;
 #pragma unroll
@@ -474,7 +478,7 @@ struct Kernel {
           if (j < nb) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              over |= fmaf(fmaxf(f(4 * j + e), f(4 * j + 2 + e)), a.scale_log2, nm[2 * j + e]) > kTop;
+              over |= fmaxf(f(4 * j + e), f(4 * j + 2 + e)) + nm[2 * j + e] > kTop;
           }
         if (bar_any(own_bar, 128, over)) {
           // some row's maximum is raised: the maxima of the warpgroup's rows over the step
@@ -483,7 +487,7 @@ struct Kernel {
             if (j < nb) {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float x = fmaxf(f(4 * j + e), f(4 * j + 2 + e)) * a.scale_log2;
+                float x = fmaxf(f(4 * j + e), f(4 * j + 2 + e));
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
                 if (lane < 4) m.top[w4][8 * j + cl + e] = x;
@@ -533,8 +537,8 @@ struct Kernel {
           if (j < nb) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float p0 = ex2(fmaf(f(4 * j + 2 * r), a.scale_log2, nm[2 * j]));
-              const float p1 = ex2(fmaf(f(4 * j + 2 * r + 1), a.scale_log2, nm[2 * j + 1]));
+              const float p0 = ex2(f(4 * j + 2 * r) + nm[2 * j]);
+              const float p1 = ex2(f(4 * j + 2 * r + 1) + nm[2 * j + 1]);
               l[2 * j] += p0;
               l[2 * j + 1] += p1;
               hi[2 * j + r] = pack2<T>(p0, p1);

@@ -423,3 +423,160 @@ def test_one_workspace_for_different_calls(spg):
             x.attend()
             check_attend(x)
     assert a.err() == 0
+
+
+# ---- where these are easily wrong ---------------------------------------------------------------
+
+
+def test_rows_with_nan_queries_stay_to_themselves(spg):
+    c = R.Latent(20, 512, 16, "bf16", [900, 70], [2, 1], poison=0.0)
+    c.q_lat[0, 3, 5] = math.nan
+    c.q_lat[2, 19, 570] = math.nan
+    x = Run(spg, c)
+    x.attend()
+    assert x.err() == 0
+    bad = torch.zeros(3, 20, dtype=torch.bool)
+    bad[0, 3] = bad[2, 19] = True
+    assert torch.equal(torch.isnan(host(x.lse)), bad)
+    assert bool(torch.isnan(x.o_lat[bad.cuda()]).all())
+    c.q_lat = torch.nan_to_num(c.q_lat)
+    out, tol, lse, lse_tol = R.attention(c)
+    close(x.o_lat[(~bad).cuda()], out[~bad], tol[~bad], "o_lat")
+    close(x.lse[(~bad).cuda()], lse[~bad], lse_tol[~bad], "lse")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_one_token_far_above_and_far_below_the_others(spg, dt):
+    """One logit thousands above the rest (all weight on one token), and rows whose logits are all thousands below 0."""
+    c = R.Latent(16, 512, 64, dt, [500, 3000], [1, 1])
+    c.q_lat[:, :8] = 4.0
+    for b, L in enumerate(c.lens):
+        pg = c.page_table[b].long()
+        c.pool[pg[300 // 64], 300 % 64] = 4.0     # 4 * 4 * 576 / 13.9: about 660 above
+    c.q_lat[:, 8:] = -8.0
+    for b, L in enumerate(c.lens):
+        for t0 in range(0, L, 64):
+            n = min(64, L - t0)
+            row = c.pool[int(c.page_table[b, t0 // 64]), :n]
+            row.copy_((row.float().abs() + 1.0).to(row.dtype))
+    x = Run(spg, c)
+    x.attend()
+    assert x.err() == 0
+    check_attend(x)
+
+
+def test_a_logit_of_the_range_s_size(spg):
+    """bf16 reaches logits of -1e36: a row's only token has all of its weight whatever its logit is."""
+    c = R.Latent(4, 256, 16, "bf16", [1], [1])
+    c.q_lat[:] = 1e18
+    c.pool[c.page_table[0, 0].long(), 0] = -1e16
+    x = Run(spg, c)
+    x.attend()
+    assert bool(torch.isfinite(x.lse).all()) and bool((x.lse < -1e35).all())
+    assert torch.equal(x.o_lat, x.pool[x.page_table[0, 0].long(), 0, :256].expand(1, 4, 256))
+
+
+def test_shared_pages(spg):
+    """Sequences with a common prefix in the same physical pages."""
+    c = R.Latent(32, 512, 16, "bf16", [200, 170], [2, 1])
+    c.page_table[1, :8] = c.page_table[0, :8]
+    x = Run(spg, c)
+    x.attend()
+    assert x.err() == 0
+    check_attend(x)
+
+
+@pytest.mark.parametrize("H, lens, new", [(1024, [90, 33], [1, 1]), (1023, [70], [2]), (65, [200, 0, 64], [3, 0, 1]), (63, [130], [5])])
+def test_head_counts(spg, H, lens, new):
+    x = Run(spg, R.Latent(H, 256, 32, "bf16", lens, new, pad_rows=1))
+    x.attend()
+    assert x.err() == 0
+    check_attend(x)
+
+
+@pytest.mark.parametrize("L", [63, 64, 65, 127, 128, 129, 191, 192])
+@pytest.mark.parametrize("S", [16, 128])
+def test_lengths_around_a_step(spg, L, S):
+    x = Run(spg, R.Latent(17, 512, S, "f16", [L, L + 1, L], [1, min(L, 5), L]))
+    x.attend()
+    assert x.err() == 0
+    check_attend(x)
+
+
+def test_more_sequences_than_ctas_of_one_step(spg):
+    """Items of one step each, several to a CTA, with 64 and with 128 rows an item."""
+    for H in (64, 128):
+        x = Run(spg, R.Latent(H, 256, 16, "f16", [1 + i % 60 for i in range(330)], [1] * 330))
+        x.attend()
+        assert x.err() == 0
+        check_attend(x)
+
+
+def test_calls_in_a_row_on_one_stream(spg):
+    """A layer's four calls back to back many times over, each launch free to start while the one before ends."""
+    c = R.Latent(16, 512, 64, "bf16", [700, 130], [1, 3])
+    x, rope = Run(spg, c), spg.make_rope(rot_dim=64)
+    layer(x, rope)
+    want = [t.clone() for t in (x.out, x.o_lat, x.lse, x.q_lat)]
+    for _ in range(50):
+        layer(x, rope)
+    for a, b in zip((x.out, x.o_lat, x.lse, x.q_lat), want):
+        assert torch.equal(a, b)
+    assert x.err() == 0
+
+
+def test_calls_from_a_side_stream(spg):
+    """The binding takes the current stream: work queued on it comes first."""
+    c = R.Latent(16, 512, 64, "bf16", [700, 130], [1, 3])
+    x = Run(spg, c)
+    s = torch.cuda.Stream()
+    q = x.q_lat.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        x.q_lat.zero_()
+        torch.cuda._sleep(2_000_000)
+        x.q_lat.copy_(q)
+        x.attend()
+    s.synchronize()
+    check_attend(x)
+
+
+def test_two_graphs_share_a_workspace(spg):
+    """Two captured calls of different sizes on one workspace, replayed in turn."""
+    a = Run(spg, R.Latent(64, 512, 64, "bf16", [3000, 900], [1, 4], seed=1))
+    b = Run(spg, R.Latent(128, 256, 16, "f16", [2000], [2], seed=2))
+    b.ws = a.ws
+    for x in (a, b):
+        x.attend()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for x in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            x.attend()
+        graphs.append(g)
+    for _ in range(3):
+        for x, g in zip((a, b), graphs):
+            x.o_lat.fill_(7.0)
+            g.replay()
+    torch.cuda.synchronize()
+    for x in (a, b):
+        check_attend(x)
+    assert a.err() == 0
+
+
+def test_append_of_many_rows_in_ragged_sequences(spg):
+    """Rows of 40 sequences, empty ones among them, found by every CTA for itself."""
+    g = torch.Generator().manual_seed(3)
+    lens = [int(v) for v in torch.randint(0, 90, (40,), generator=g)]
+    new = [min(L, int(v)) for L, v in zip(lens, torch.randint(0, 30, (40,), generator=g))]
+    c = R.Latent(5, 256, 16, "bf16", lens, new, pad_rows=3)
+    x = Run(spg, c)
+    x.append(None, norm=False)
+    assert x.err() == 0
+    pool = host(x.pool)
+    for b, L in enumerate(lens):
+        for i in range(new[b]):
+            t = L - new[b] + i
+            assert torch.equal(pool[int(c.page_table[b, t // 16]), t % 16], c.kv[c.starts[b] + i])

@@ -56,13 +56,14 @@ ODD = ctypes.c_void_p((1 << 20) + 8)
 WS = ctypes.c_size_t(1 << 40)
 
 
-def _attend(spg, p, total=4, q=A, st=A, pool=A, pt=A, sl=A, out=A, lse=None, ws=A, wn=WS):
+def _attend(spg, p, total=4, q=A, st=A, pool=A, pt=A, sl=A, out=B, lse=None, ws=A, wn=WS):
     return spg.LIB.paged_latent_attention(ctypes.byref(p), total, q, st, pool, pt, sl, out, lse, ws, wn, None)
 
 
 @pytest.mark.parametrize("kw, status", [
     (dict(total=-1), 1), (dict(q=None), 1), (dict(q=ODD), 1), (dict(st=None), 1), (dict(pool=None), 1), (dict(pool=ODD), 1),
-    (dict(pt=None), 1), (dict(sl=None), 1), (dict(out=None), 1), (dict(lse=ODD), 1), (dict(ws=None), 1), (dict(ws=ODD), 1),
+    (dict(pt=None), 1), (dict(sl=None), 1), (dict(out=None), 1), (dict(out=A), 1), (dict(lse=ODD), 1), (dict(ws=None), 1),
+    (dict(ws=ODD), 1),
     (dict(wn=ctypes.c_size_t(16)), 4), (dict(total=0, q=None, out=None), 0), (dict(total=2 ** 30), 2),
 ])
 def test_attention_refusals(spg, kw, status):
@@ -168,3 +169,33 @@ def test_reference_append_agrees_with_complex_turns():
     assert torch.allclose(row[:, 256:], torch.cat([z.real, z.imag], 1), atol=1e-12)
     y = torch.nn.functional.rms_norm(c.kv[:, :256].to(R.F64), (256,), c.norm.to(R.F64), 1e-6)
     assert torch.allclose(row[:, :256], y, atol=1e-12)
+
+
+# ---- another device --------------------------------------------------------------------------
+
+from test_paged_devices_host import On  # noqa: E402
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+CACHE = dict(pool=(BF, 20, 64, 576), page_table=(I32, 3, 5), seq_lens=(I32, 3), q_start=(I32, 4))
+CALLS = {
+    "paged_latent_append": dict(CACHE, c=(BF, 7, 512), k_pe=(BF, 7, 64), norm_weight=(BF, 512), q=(BF, 7, 8, 192),
+                                q_lat=(BF, 7, 8, 576), positions=(I32, 7)),
+    "paged_latent_attention": dict(CACHE, q_lat=(BF, 7, 8, 576), o_lat=(BF, 7, 8, 512), lse=(F32, 7, 8)),
+    "latent_absorb": dict(q=(BF, 7, 8, 192), w_kv=(BF, 8, 256, 512), q_lat=(BF, 7, 8, 576)),
+    "latent_project": dict(o_lat=(BF, 7, 8, 512), w_kv=(BF, 8, 256, 512), out=(BF, 7, 8, 128)),
+}
+
+
+@pytest.mark.parametrize("fn, name", [(f, n) for f, ts in CALLS.items() for n in ts])
+@pytest.mark.parametrize("dev", [0, -1])
+def test_tensors_of_another_device_are_refused(spg, monkeypatch, fn, name, dev):
+    """Every tensor on device 1 but one: refused, and the library is not called."""
+    p = spg.make_latent_params(batch=3, num_heads=8, latent_dim=512, page_size=64, num_phys_pages=20, max_pages_per_seq=5)
+    monkeypatch.setattr(spg.binding, "LIB", None)
+    args = {n: On(1, *t) for n, t in CALLS[fn].items()}
+    args[name] = On(dev, *CALLS[fn][name])
+    if fn.startswith("paged"):
+        args["ws"] = On(1, torch.uint8, 1 << 30)
+    extra = dict(rope=None, eps=1e-6) if fn == "paged_latent_append" else {}
+    with pytest.raises(ValueError):
+        getattr(spg, fn)(p, **args, **extra)
