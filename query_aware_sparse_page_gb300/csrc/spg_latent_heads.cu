@@ -15,6 +15,10 @@
 // bound it.  So with few rows every tile of columns has a CTA of its own, and
 // with many one CTA walks all columns of its rows, which it reads once; while
 // the tensor cores work on a tile the one before is converted and stored.
+//
+// Measured (GB300, r = 512, dn = dv = 128): absorbing 16 rows of 128 heads 6.5
+// us, projecting them 6.2 (19 MB each); absorbing 2048 rows of 32 heads 23 us,
+// 3.9 TB/s (every tile of columns by itself, stored from the registers: 38).
 #include "spg_latent.h"
 #include "spg_tcgen05.cuh"
 
