@@ -35,6 +35,7 @@ struct HeadsArgs {
   int y_head;
   int n_tiles, walk, w_row;  // tiles of columns, those of one CTA; first row of the head's matrix used
   int few;                   // rows, when they fit one tile: stored from the registers; else 0
+  int rows;                  // of a tile, as copied
 };
 
 __device__ __forceinline__ void tma_tile_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -43,6 +44,12 @@ __device__ __forceinline__ void tma_tile_3d(void* dst, const CUtensorMap* map, i
           smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
+}
+// the tile a copy will bring, into L2
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -54,23 +61,22 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 // KC: chunks of 64 of the contraction.  ABSORB: the rows' chunks stay for all
 // tiles of columns, the matrix's pass through ST buffers; else one tile of
 // columns, and both pass through them.  A single tile leaves through the place
-// of its operands.
-template <int KC, int NT, bool ABSORB>
+// of its operands.  With few rows their chunks have only these (in eights): the
+// product's other rows are whatever lies behind, in rows that nobody stores.
+template <int KC, int NT, int ST, bool ABSORB>
 struct HeadsLayout {
-  static constexpr int ST = ABSORB ? 2 : 3;
-  static constexpr uint32_t kBBytes = NT * 128;
-  static constexpr uint32_t a_off = 0, kAStages = ABSORB ? KC : ST;
-  static constexpr uint32_t b_off = a_off + kAStages * kABytes, end = b_off + ST * kBBytes;
-  static constexpr uint32_t kOutBytes = NT / 64 * kRowsTile * 128;
-  static constexpr uint32_t bytes(int walk) { return end + (walk > 1 ? kOutBytes : 0); }
-  static constexpr int kTmem = ABSORB ? 2 * NT : NT;
-  static_assert(end >= kOutBytes, "room for a tile");
+  static constexpr uint32_t kBBytes = NT * 128, kAStages = ABSORB ? KC : ST, kOutBytes = NT / 64 * kRowsTile * 128;
+  __host__ __device__ static constexpr uint32_t b_off(uint32_t a_bytes) { return kAStages * a_bytes; }
+  __host__ __device__ static constexpr uint32_t end(uint32_t a_bytes) { return b_off(a_bytes) + ST * kBBytes; }
+  static constexpr uint32_t bytes(uint32_t a_bytes, int walk) { return end(a_bytes) + (walk > 1 ? kOutBytes : 0); }
+  static_assert(end(kABytes) >= kOutBytes, "room for a tile");
+  static_assert(end(1024) >= (kAStages - 1) * 1024 + kABytes, "what a product reads of few rows' chunks");
 };
 
-template <typename T, int KC, int NT, bool ABSORB>
+template <typename T, int KC, int NT, int ST, bool ABSORB>
 __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant__ HeadsArgs a) {
-  using Lay = HeadsLayout<KC, NT, ABSORB>;
-  constexpr int ST = Lay::ST;
+  using Lay = HeadsLayout<KC, NT, ST, ABSORB>;
+  const uint32_t a_bytes = a.rows * 128, b_off = Lay::b_off(a_bytes), tmem_cols = a.walk > 1 ? 2 * NT : NT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   // (full: the matrix's chunk, with it the rows' while they come; done, free: a tile's accumulator)
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
     s_failed = 0;
     mbar_fence_init();
   }
-  if (warp == 5) tmem_alloc(&s_tmem, Lay::kTmem);
+  if (warp == 5) tmem_alloc(&s_tmem, tmem_cols);
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&a.tmx);
     tma_prefetch_desc(&a.tmw);
@@ -106,21 +112,33 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
 
   if (warp == 4) {
     if (lane == 0) {
-      // the matrices are the caller's weights, but nothing says that the launch before did not write them
+      // The matrices are the caller's weights, but nothing says that the launch
+      // before did not write them: until it is done they only come to L2.
+      if (a.walk == 1) {
+#pragma unroll
+        for (int k = 0; k < KC; ++k) {
+          if (ABSORB) {
+#pragma unroll
+            for (int i = 0; i < NT / 64; ++i) tma_prefetch_3d(&a.tmw, n_first * NT + 64 * i, a.w_row + 64 * k, h);
+          } else {
+            tma_prefetch_3d(&a.tmw, 64 * k, a.w_row + n_first * NT, h);
+          }
+        }
+      }
       pdl_wait();
       for (int c = 0; c < chunks; ++c) {
         const int st = c % ST, k = c % KC, n0 = (n_first + c / KC) * NT;
         if (c >= ST && !mbar_wait_bounded(&empty[st], (c / ST - 1) & 1)) break;
         const bool rows = !ABSORB || c < KC;
-        uint8_t* b = smem + Lay::b_off + st * Lay::kBBytes;
-        mbar_arrive_expect_tx(&full[st], Lay::kBBytes + (rows ? kABytes : 0));
+        uint8_t* b = smem + b_off + st * Lay::kBBytes;
+        mbar_arrive_expect_tx(&full[st], Lay::kBBytes + (rows ? a_bytes : 0));
         if (ABSORB) {
 #pragma unroll
           for (int i = 0; i < NT / 64; ++i) tma_tile_3d(b + i * 8192, &a.tmw, n0 + 64 * i, a.w_row + 64 * k, h, &full[st]);
         } else {
           tma_tile_3d(b, &a.tmw, 64 * k, a.w_row + n0, h, &full[st]);
         }
-        if (rows) tma_tile_3d(smem + Lay::a_off + (ABSORB ? k : st) * kABytes, &a.tmx, 64 * k, h, t0, &full[st]);
+        if (rows) tma_tile_3d(smem + (ABSORB ? k : st) * a_bytes, &a.tmx, 64 * k, h, t0, &full[st]);
       }
     }
     __syncwarp();
@@ -144,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
       }
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t at = base + Lay::a_off + (ABSORB ? k : st) * kABytes, bt = base + Lay::b_off + st * Lay::kBBytes;
+        const uint32_t at = base + (ABSORB ? k : st) * a_bytes, bt = base + b_off + st * Lay::kBBytes;
         const uint32_t da = desc_k_major(at), db = ABSORB ? desc_mn_major(bt, 8192) : desc_k_major(bt);
 #pragma unroll
         for (int i = 0; i < 4; ++i) mma_ss(tmem + acc * NT, da + 2 * i, db + i * (ABSORB ? 128 : 2), id, k > 0 || i > 0);
@@ -155,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
     }
   } else {
     // ---- a tile's rows, one a thread, to 16 bits and out ----
-    uint8_t* out = smem + (a.walk > 1 ? Lay::end : 0);
+    uint8_t* out = smem + (a.walk > 1 ? Lay::end(a_bytes) : 0);
     const int r = threadIdx.x;
     for (int n = 0; n < a.walk; ++n) {
       const int acc = n & 1;
@@ -213,24 +231,18 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
   __syncthreads();
   if (warp == 5) {
     tc_fence_after();
-    tmem_dealloc(tmem, Lay::kTmem);
+    tmem_dealloc(tmem, tmem_cols);
   }
 }
 
-template <typename T, int KC, int NT, bool ABSORB>
+template <typename T, int KC, int NT, int ST, bool ABSORB>
 cudaError_t heads_typed(const spg_latent_params& p, int total_q, const void* x, int64_t x_stride, const void* w, void* y,
                         cudaStream_t st) {
+  using Lay = HeadsLayout<KC, NT, ST, ABSORB>;
   HeadsArgs a{};
   const uint64_t H = p.num_heads, K = 64 * KC, N = ABSORB ? p.latent_dim : p.v_dim, rows = total_q;
   const uint64_t xh = ABSORB ? p.nope_dim + p.rope_dim : p.latent_dim, wr = p.nope_dim + p.v_dim;
   const uint64_t yh = ABSORB ? p.latent_dim + p.rope_dim : p.v_dim;
-  const uint64_t xd[3] = {K, H, rows}, xs[2] = {2 * xh, 2 * static_cast<uint64_t>(x_stride)};
-  const uint64_t wd[3] = {static_cast<uint64_t>(p.latent_dim), wr, H}, ws[2] = {2 * wd[0], 2 * wd[0] * wr};
-  const uint64_t yd[3] = {N, H, rows}, ys[2] = {2 * yh, 2 * yh * H};
-  const uint32_t rb[3] = {64, 1, kRowsTile}, wb[3] = {64, ABSORB ? 64u : static_cast<uint32_t>(NT), 1};
-  if (!make_tmap16(&a.tmx, p.dtype, x, 3, xd, xs, rb) || !make_tmap16(&a.tmw, p.dtype, w, 3, wd, ws, wb) ||
-      !make_tmap16(&a.tmy, p.dtype, y, 3, yd, ys, rb))
-    return cudaErrorNotSupported;
   a.w_row = ABSORB ? 0 : p.nope_dim;
   a.n_tiles = static_cast<int>(N / NT);
   const long long row_tiles = (static_cast<long long>(total_q) + kRowsTile - 1) / kRowsTile;
@@ -238,28 +250,43 @@ cudaError_t heads_typed(const spg_latent_params& p, int total_q, const void* x, 
   a.walk = ABSORB && row_tiles * p.num_heads >= device_sm_count() ? a.n_tiles : 1;
   // few rows straight from the registers (16 rows of 128 heads: 7.2 against 7.9 us by way of shared memory)
   a.few = a.walk == 1 && total_q <= kRowsTile ? total_q : 0;
+  a.rows = a.few ? (a.few + 7) & ~7 : kRowsTile;
   a.y = y;
   a.y_head = static_cast<int>(yh);
   a.y_row = static_cast<long long>(yh * H);
-  const auto kern = k_latent_heads<T, KC, NT, ABSORB>;
-  const size_t smem = 1024 + HeadsLayout<KC, NT, ABSORB>::bytes(a.walk);
+  const uint64_t xd[3] = {K, H, rows}, xs[2] = {2 * xh, 2 * static_cast<uint64_t>(x_stride)};
+  const uint64_t wd[3] = {static_cast<uint64_t>(p.latent_dim), wr, H}, ws[2] = {2 * wd[0], 2 * wd[0] * wr};
+  const uint64_t yd[3] = {N, H, rows}, ys[2] = {2 * yh, 2 * yh * H};
+  const uint32_t xb[3] = {64, 1, static_cast<uint32_t>(a.rows)}, wb[3] = {64, ABSORB ? 64u : static_cast<uint32_t>(NT), 1};
+  const uint32_t yb[3] = {64, 1, kRowsTile};
+  if (!make_tmap16(&a.tmx, p.dtype, x, 3, xd, xs, xb) || !make_tmap16(&a.tmw, p.dtype, w, 3, wd, ws, wb) ||
+      (!a.few && !make_tmap16(&a.tmy, p.dtype, y, 3, yd, ys, yb)))
+    return cudaErrorNotSupported;
+  const auto kern = k_latent_heads<T, KC, NT, ST, ABSORB>;
+  const size_t smem = 1024 + Lay::bytes(a.rows * 128, a.walk);
   const cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(row_tiles * (a.n_tiles / a.walk)), p.num_heads), dim3(kThreads), smem, st, a);
+}
+
+template <typename T, int KC>
+cudaError_t project_typed(const spg_latent_params& p, int total_q, const void* x, int64_t x_stride, const void* w, void* y,
+                          cudaStream_t st) {
+  // few rows: all chunks on their way at once
+  if (total_q <= 32) return heads_typed<T, KC, 64, KC, false>(p, total_q, x, x_stride, w, y, st);
+  // 64 columns a CTA while one tile has all rows (twice the CTAs for the matrices' bytes)
+  if (p.v_dim == 64 || total_q <= kRowsTile) return heads_typed<T, KC, 64, 3, false>(p, total_q, x, x_stride, w, y, st);
+  return heads_typed<T, KC, 128, 3, false>(p, total_q, x, x_stride, w, y, st);
 }
 
 template <typename T>
 cudaError_t heads(const spg_latent_params& p, bool project, int total_q, const void* x, int64_t x_stride, const void* w, void* y,
                   cudaStream_t st) {
   if (!project)
-    return p.nope_dim == 128 ? heads_typed<T, 2, 128, true>(p, total_q, x, x_stride, w, y, st)
-                             : heads_typed<T, 1, 128, true>(p, total_q, x, x_stride, w, y, st);
-  // 64 columns a CTA while one tile has all rows (twice the CTAs for the matrices' bytes)
-  if (p.v_dim == 64 || total_q <= kRowsTile)
-    return p.latent_dim == 512 ? heads_typed<T, 8, 64, false>(p, total_q, x, x_stride, w, y, st)
-                               : heads_typed<T, 4, 64, false>(p, total_q, x, x_stride, w, y, st);
-  return p.latent_dim == 512 ? heads_typed<T, 8, 128, false>(p, total_q, x, x_stride, w, y, st)
-                             : heads_typed<T, 4, 128, false>(p, total_q, x, x_stride, w, y, st);
+    return p.nope_dim == 128 ? heads_typed<T, 2, 128, 2, true>(p, total_q, x, x_stride, w, y, st)
+                             : heads_typed<T, 1, 128, 2, true>(p, total_q, x, x_stride, w, y, st);
+  return p.latent_dim == 512 ? project_typed<T, 8>(p, total_q, x, x_stride, w, y, st)
+                             : project_typed<T, 4>(p, total_q, x, x_stride, w, y, st);
 }
 
 }  // namespace
