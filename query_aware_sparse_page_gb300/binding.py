@@ -10,6 +10,7 @@ fallback: if the library is missing, importing this module fails.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_void_p
 
@@ -386,6 +387,9 @@ def _take_cache(dev, p, k_pool, v_pool, k_scale, v_scale, page_table, seq_lens, 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+_one_device = functools.lru_cache(None)(lambda: torch.cuda.device_count() == 1)
+
+
 def _call(dev, fn, where, ws, stream, *args):
     """fn(*args, workspace, its bytes, stream) with the workspace's device current."""
     if dev < 0 or not ws.is_contiguous():
@@ -393,7 +397,7 @@ def _call(dev, fn, where, ws, stream, *args):
     if stream is None:
         stream = _raw_stream(dev)
     size = ws.numel() * ws.element_size()
-    if dev == torch.cuda.current_device():
+    if _one_device() or dev == torch.cuda.current_device():
         _check(fn(*args, ws.data_ptr(), size, stream), where)
     else:
         with torch.cuda.device(dev):
@@ -504,7 +508,7 @@ def _call_rows(dev, fn, where, stream, *args):
         raise ValueError("libspg takes device tensors")
     if stream is None:
         stream = _raw_stream(dev)
-    if dev == torch.cuda.current_device():
+    if _one_device() or dev == torch.cuda.current_device():
         _check(fn(*args, stream), where)
     else:
         with torch.cuda.device(dev):

@@ -49,33 +49,47 @@ struct Plan {
 template <typename Shape>
 __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, int c = static_cast<int>(blockIdx.x),
                           int n_ctas = static_cast<int>(gridDim.x)) {
-  long long total = 0, items = 0;
+  // steps up to and with each lane's first sequence, then those of the others
+  long long items = 0;
   int32_t bad = 0;
-  ChunkSeq first_sq{};  // of the lane's first sequence, its items and their steps
+  ChunkSeq first_sq{};
   int first_items = 0;
   long long first_w = 0;
-  for (int b = lane; b < sh.B; b += 32) {
-    const ChunkSeq s = sh.seq(b, bad);
-    const int ni = sh.items(s);
-    const long long w = sh.Hkv * sh.steps(s, ni);
-    if (b == lane) {
-      first_sq = s;
-      first_items = ni;
-      first_w = w;
-    }
-    total += w;
-    items += static_cast<long long>(sh.Hkv) * ni;
+  if (lane < sh.B) {
+    first_sq = sh.seq(lane, bad);
+    first_items = sh.items(first_sq);
+    first_w = sh.Hkv * sh.steps(first_sq, first_items);
   }
+  long long incl = first_w;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    items += __shfl_xor_sync(0xffffffffu, items, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const long long first_incl = incl, first_total = __shfl_sync(0xffffffffu, incl, 31);
+  long long total = first_total;
+  items = static_cast<long long>(sh.Hkv) * first_items;
+  if (sh.B > 32) {
+    long long rest = 0;
+    for (int b = lane + 32; b < sh.B; b += 32) {
+      const ChunkSeq s = sh.seq(b, bad);
+      const int ni = sh.items(s);
+      rest += sh.Hkv * sh.steps(s, ni);
+      items += static_cast<long long>(sh.Hkv) * ni;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
+    total += rest;
+  }
+  if constexpr (Shape::kMostParts < kMaxCtas) {  // else no item can have more parts
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
   }
   if (bad && blockIdx.x == 0) record_error(err, bad);
   Plan p{};
   p.total = total;
   long long n = min(static_cast<long long>(n_ctas), (total + Shape::kLeast - 1) / Shape::kLeast);
-  n = min(n, items * Shape::kMostParts);
+  if constexpr (Shape::kMostParts < kMaxCtas) n = min(n, items * Shape::kMostParts);
   p.ctas = static_cast<int>(n);
   if (c >= n) {
     if (lane == 0) *out = p;  // lo = hi = 0: nothing to do
@@ -86,7 +100,7 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, in
   long long base = 0;
   for (int b0 = 0; b0 < sh.B; b0 += 32) {
     const int b = b0 + lane;
-    long long w = first_w;
+    long long w = first_w, upto = first_incl;
     ChunkSeq s = first_sq;
     int ni = first_items;
     if (b0 > 0) {
@@ -96,14 +110,14 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, in
         ni = sh.items(s);
         w = sh.Hkv * sh.steps(s, ni);
       }
-    }
-    long long incl = w;
+      upto = w;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
     }
-    const long long first = base + incl - w;
+    const long long first = base + upto - w;
     if (p.lo >= first && p.lo < first + w) {  // one lane
       const long long per_head = div_pos(w, sh.Hkv);
       p.b = b;
@@ -120,7 +134,7 @@ __device__ void make_plan(const Shape& sh, Plan* out, int32_t* err, int lane, in
       p.item_first = first + p.h * per_head + sh.steps(s, x);
       *out = p;
     }
-    base += __shfl_sync(0xffffffffu, incl, 31);
+    base += b0 == 0 ? first_total : __shfl_sync(0xffffffffu, upto, 31);
     if (base > p.lo) break;
   }
 }
