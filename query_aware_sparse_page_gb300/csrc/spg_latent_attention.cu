@@ -124,7 +124,7 @@ struct Seg : Part {
 };
 struct SegIter : PartIter<LatentItems> {
   int pair, rank;
-  __device__ SegIter(const LatentItems& shape, const Plan& p, int pair_, int rank_) : PartIter(shape, p), pair(pair_), rank(rank_) {}
+  __device__ SegIter(const LatentItems& shape, const Plan& p, int pair_, int rank_) : PartIter(shape, p, Planned{}), pair(pair_), rank(rank_) {}
   __device__ bool next(Seg& s) {
     while (PartIter::next(s)) {
       s.row0 = s.item << sh.rows_log2;
