@@ -65,11 +65,11 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
 // product's other rows are whatever lies behind, in rows that nobody stores.
 template <int KC, int NT, int ST, bool ABSORB>
 struct HeadsLayout {
-  static constexpr uint32_t kBBytes = NT * 128, kAStages = ABSORB ? KC : ST, kOutBytes = NT / 64 * kRowsTile * 128;
+  static constexpr uint32_t kBBytes = NT * 128, kAStages = ABSORB ? KC : ST, kOutBytes = kRowsTile * 128;
   __host__ __device__ static constexpr uint32_t b_off(uint32_t a_bytes) { return kAStages * a_bytes; }
   __host__ __device__ static constexpr uint32_t end(uint32_t a_bytes) { return b_off(a_bytes) + ST * kBBytes; }
   static constexpr uint32_t bytes(uint32_t a_bytes, int walk) { return end(a_bytes) + (walk > 1 ? kOutBytes : 0); }
-  static_assert(end(kABytes) >= kOutBytes, "room for a tile");
+  static_assert(end(kABytes) >= kOutBytes, "room for 64 columns");
   static_assert(end(1024) >= (kAStages - 1) * 1024 + kABytes, "what a product reads of few rows' chunks");
 };
 
@@ -179,10 +179,6 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
       const int acc = n & 1;
       const bool ok = mbar_wait_bounded(&done[acc], (n >> 1) & 1) && *static_cast<volatile int*>(&s_failed) == 0;
       tc_fence_after();
-      if (n > 0) {
-        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile has left
-        bar_sync(1, kRowsTile);
-      }
       if (a.few && warp * 32 >= a.few) break;
 #pragma unroll
       for (int c = 0; c < NT; c += 32) {
@@ -204,26 +200,33 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
           }
           continue;
         }
-        uint8_t* row = out + (c >> 6) * (kRowsTile * 128) + r * 128;
+        // 64 columns at a time through one buffer
+        if (c % 64 == 0 && n + c > 0) {
+          if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last ones have left
+          bar_sync(1, kRowsTile);
+        }
+        uint8_t* row = out + r * 128;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           const auto f = [&](int e) { return __uint_as_float(x[i + e]); };
           *reinterpret_cast<uint4*>(row + (((((c & 63) + i) >> 3) ^ (r & 7)) << 4)) =
               make_uint4(pack2<T>(f(0), f(1)), pack2<T>(f(2), f(3)), pack2<T>(f(4), f(5)), pack2<T>(f(6), f(7)));
         }
+        if (c + 32 == NT) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&free_[acc]);
+        }
+        if (c % 64 == 32) {
+          fence_proxy_async();
+          bar_sync(1, kRowsTile);
+          if (threadIdx.x == 0) {
+            tma_store_3d(&a.tmy, out, (n_first + n) * NT + c - 32, h, t0);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
       }
       if (a.few) break;  // a single tile
-      tc_fence_before();
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&free_[acc]);
-      bar_sync(1, kRowsTile);
-      if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 0; i < NT / 64; ++i)
-          tma_store_3d(&a.tmy, out + i * (kRowsTile * 128), (n_first + n) * NT + 64 * i, h, t0);
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      }
     }
     if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
@@ -283,8 +286,8 @@ template <typename T>
 cudaError_t heads(const spg_latent_params& p, bool project, int total_q, const void* x, int64_t x_stride, const void* w, void* y,
                   cudaStream_t st) {
   if (!project)
-    return p.nope_dim == 128 ? heads_typed<T, 2, 128, 2, true>(p, total_q, x, x_stride, w, y, st)
-                             : heads_typed<T, 1, 128, 2, true>(p, total_q, x, x_stride, w, y, st);
+    return p.nope_dim == 128 ? heads_typed<T, 2, 128, 3, true>(p, total_q, x, x_stride, w, y, st)
+                             : heads_typed<T, 1, 128, 3, true>(p, total_q, x, x_stride, w, y, st);
   return p.latent_dim == 512 ? project_typed<T, 8>(p, total_q, x, x_stride, w, y, st)
                              : project_typed<T, 4>(p, total_q, x, x_stride, w, y, st);
 }
