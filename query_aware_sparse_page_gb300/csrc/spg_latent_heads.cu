@@ -16,9 +16,10 @@
 // with many one CTA walks all columns of its rows, which it reads once; while
 // the tensor cores work on a tile the one before is converted and stored.
 //
-// Measured (GB300, r = 512, dn = dv = 128): absorbing 16 rows of 128 heads 6.5
-// us, projecting them 6.2 (19 MB each); absorbing 2048 rows of 32 heads 23 us,
-// 3.9 TB/s (every tile of columns by itself, stored from the registers: 38).
+// Measured (GB300, r = 512, dn = dv = 128, back to back): absorbing 16 rows of
+// 128 heads 5.1 us, projecting them 6.0 (19 MB each); absorbing 2048 rows of 32
+// heads 22.3 us, 3.9 TB/s (every tile of columns by itself, stored from the
+// registers: 38).
 #include "spg_latent.h"
 #include "spg_tcgen05.cuh"
 
@@ -275,8 +276,9 @@ cudaError_t heads_typed(const spg_latent_params& p, int total_q, const void* x, 
 template <typename T, int KC>
 cudaError_t project_typed(const spg_latent_params& p, int total_q, const void* x, int64_t x_stride, const void* w, void* y,
                           cudaStream_t st) {
-  // few rows: all chunks on their way at once
-  if (total_q <= 32) return heads_typed<T, KC, 64, KC, false>(p, total_q, x, x_stride, w, y, st);
+  // few rows: all chunks on their way at once (16 rows of 128 heads 6.3 us; with four or three in flight 7.3 and 8.1), 32
+  // columns a CTA (64: 6.3, 32: 6.0)
+  if (total_q <= 32) return heads_typed<T, KC, 32, KC, false>(p, total_q, x, x_stride, w, y, st);
   // 64 columns a CTA while one tile has all rows (twice the CTAs for the matrices' bytes)
   if (p.v_dim == 64 || total_q <= kRowsTile) return heads_typed<T, KC, 64, 3, false>(p, total_q, x, x_stride, w, y, st);
   return heads_typed<T, KC, 128, 3, false>(p, total_q, x, x_stride, w, y, st);
