@@ -378,8 +378,8 @@ spg_status paged_chunk_attention(const spg_params* p, int32_t total_q, const voi
                                  const int32_t* page_table, const int32_t* seq_lens, void* out,
                                  float* lse, void* ws, size_t ws_bytes, spg_stream_t stream);
 
-/* 16-bit values in whose sum a probability enters paged_chunk_attention's P V
- * product, process-wide: 2 (the default: 16 bits of it with bf16, 22 with
+/* 16-bit values in whose sum a probability enters paged_chunk_attention's and
+ * paged_latent_attention's P V product, process-wide: 2 (the default: 16 bits of it with bf16, 22 with
  * fp16, so that the result is off by little more than its own rounding) or 1
  * (half a step per token more, together 1.4 times the error; prompts are 1.3
  * times as fast).  Not thread-safe with respect to calls on other host

@@ -405,8 +405,8 @@ struct Kernel {
             break;
           }
           if (lane == 0) {
-            // (the products that read the last one's are done with both halves' only behind the second wait,
-            // but the softmax warps, who alone look at it later, before the first)
+            // nobody reads the last step's any more: the S warp did before that step's S, the softmax warps
+            // before its P, and the first half's products, waited for above, came after both
             if (half == 0) m.live[stage] = static_cast<uint64_t>(up) << 32 | lo;
             mbar_arrive_expect_tx(&m.full[stage][half], n * (per / 8) * group);
           }
