@@ -20,8 +20,9 @@
 // once S is done P^T takes its place.  P enters as two 16-bit values
 // (spg_set_chunk_parts), the second what the first's rounding left: up to 32
 // rows both lie side by side in that block as one operand of twice the columns
-// (a product's time is its A operand's, 4 KB of shared memory, whatever N is),
-// beyond it the second stands in a buffer of its own and is a second operand.
+// (a product's time is mostly its A operand's, 4 KB of shared memory: 32 cycles
+// with 32 columns, 41 with 64), beyond it the second stands in a buffer of its
+// own and is a second operand.
 //
 // The running maximum m of a row is only raised when a (base 2) logit exceeds
 // it by more than kTop, and then set kHead below that logit (as in the chunk
@@ -43,10 +44,13 @@
 // one token of 32 heads of 8 sequences of 4K to 64K 60 us, 4.4 TB/s over all
 // and 6.2 in the middle (copies alone 6.45); of one sequence at 32K 23 us; of
 // 128 heads of 16 sequences at 10K 90 us; 500 tokens of 16 heads over 16K 407
-// us, 690 TFLOP/s.  With 64 rows a CTA shared memory bounds it: a step's
-// products read 336 KB and its copies write 74 KB, 3300 cycles at 128 bytes
-// each, of 3900 that a step takes.  With few rows it is the bytes, and about 7
-// us of start (lengths, plan, pages, first copy) and 5 of the second launch.
+// us, 690 TFLOP/s.  With 64 rows a CTA it is the chain of a step: copy 2200
+// cycles, S 2000 (beside the other step's O), softmax 2000, O 1800, and only
+// two steps find room in shared memory beside the queries, so that one ends
+// every 3900 to 4000 cycles.  The products alone are 2200 of them (a product of
+// 64 tokens by 64 rows 25, one of 128 channels 41).  With few rows it is the
+// bytes, and about 7 us of start (lengths, plan, pages, first copy) and 5 of the
+// second launch.
 #include <algorithm>
 #include <cmath>
 
