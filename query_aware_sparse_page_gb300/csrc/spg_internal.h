@@ -33,6 +33,12 @@ size_t mass_workspace_bytes();
 
 size_t workspace_bytes(const spg_params& p);
 
+// Tensor map of a 2- to 4-dimensional tensor, 128-byte swizzle, elements past
+// the end zeros.  dims and box innermost first, strides in bytes of all but the
+// innermost.  False when it cannot be described or the encoder is unavailable.
+// For any host thread, one without a context among them.
+bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box);
 // Tensor map of a K or V pool (rows = num_phys_pages * num_kv_heads *
 // page_size rows of head_dim elements) through which one page of one kv-head
 // lands in shared memory as head_dim * elem_bytes / 128 tiles of [page_size

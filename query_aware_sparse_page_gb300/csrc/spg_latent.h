@@ -21,9 +21,7 @@ struct LatentAppend : LatentRows {
 // 16-bit values in whose sum a probability enters the second product (spg_set_chunk_parts)
 int chunk_parts();
 
-// Tensor map of 16-bit elements, 128-byte swizzle, elements past the end
-// zeros.  dims and box innermost first, strides in bytes of all but the
-// innermost.  False when it cannot be described.
+// encode_tmap of 16-bit elements
 bool make_tmap16(CUtensorMap* map, int dtype, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
                  const uint32_t* box);
 

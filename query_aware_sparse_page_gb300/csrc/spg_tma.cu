@@ -1,5 +1,5 @@
-// Host side of the TMA tensor tiles: encodes the tensor map through which the
-// attention producers copy K/V page tiles.  cuTensorMapEncodeTiled comes from
+// Host side of the TMA tensor tiles: encodes the tensor maps through which the
+// kernels copy tiles of pools, queries and matrices.  cuTensorMapEncodeTiled comes from
 // the runtime's driver entry-point lookup, so the library does not link
 // against the driver library itself.
 #include <cudaTypedefs.h>
@@ -27,6 +27,32 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 }  // namespace
 
+bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box) {
+  const auto fn = encode_fn();
+  if (!fn || rank < 2 || rank > 4) return false;
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  const auto encode = [&] {
+    return fn(map, dtype, rank, const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  if (r != CUDA_SUCCESS && r != CUDA_ERROR_INVALID_VALUE) {
+    // The encoder is a driver call and wants a context, which a host thread only
+    // gets with its first work in the runtime: a thread whose first work is this
+    // call takes the current device's.
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
+  }
+  return r == CUDA_SUCCESS;
+}
+
 bool make_kv_tmap(CUtensorMap* map, const void* pool, int kv_dtype, long long rows, int head_dim,
                   int page_size, bool* whole_page) {
   const int esz = kv_dtype == SPG_I8 ? 1 : 2;
@@ -34,52 +60,38 @@ bool make_kv_tmap(CUtensorMap* map, const void* pool, int kv_dtype, long long ro
   if ((head_dim * esz) % 128 != 0 || page_size < 8 || page_size > 256) return false;
   if (rows < 1 || rows > 0x7fffffffLL) return false;  // int32 row coordinates
   if ((reinterpret_cast<uintptr_t>(pool) & 15u) != 0) return false;
-  const auto fn = encode_fn();
-  if (!fn) return false;
   const CUtensorMapDataType dt = kv_dtype == SPG_F16    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : kv_dtype == SPG_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                         : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  const cuuint64_t row_bytes = static_cast<cuuint64_t>(head_dim) * esz;
-  const cuuint32_t nt = static_cast<cuuint32_t>(row_bytes / 128);  // 128-byte slices of a row
+  const uint64_t row_bytes = static_cast<uint64_t>(head_dim) * esz;
+  const uint32_t nt = static_cast<uint32_t>(row_bytes / 128);  // 128-byte slices of a row
+  const uint32_t slice = 128u / static_cast<uint32_t>(esz);
   // Whole page in one copy: a 3-D view (x: the 128 bytes of a slice, y: rows,
   // z: slices), so that a box of [128 bytes][page_size rows][nt slices] lands
   // as nt tiles of [page_size rows][128 bytes], the same layout (and 128-byte
   // swizzle) as nt separate 2-D tile copies.
   {
-    const cuuint64_t dims[3] = {128u / static_cast<cuuint64_t>(esz), static_cast<cuuint64_t>(rows), nt};
-    const cuuint64_t strides[2] = {row_bytes, 128u};
-    const cuuint32_t box[3] = {128u / esz, static_cast<cuuint32_t>(page_size), nt};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    if (fn(map, dt, 3, const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS) {
+    const uint64_t dims[3] = {slice, static_cast<uint64_t>(rows), nt}, strides[2] = {row_bytes, 128};
+    const uint32_t box[3] = {slice, static_cast<uint32_t>(page_size), nt};
+    if (encode_tmap(map, dt, 3, pool, dims, strides, box)) {
       *whole_page = true;
       return true;
     }
   }
   // else one 2-D tile of [page_size rows][128 bytes] per slice
   *whole_page = false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {128u / esz, static_cast<cuuint32_t>(page_size)};  // 128-byte rows
-  const cuuint32_t estr[2] = {1u, 1u};
-  const CUresult r = fn(map, dt, 2, const_cast<void*>(pool), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
+  const uint64_t dims[2] = {static_cast<uint64_t>(head_dim), static_cast<uint64_t>(rows)};
+  const uint32_t box[2] = {slice, static_cast<uint32_t>(page_size)};  // 128-byte rows
+  return encode_tmap(map, dt, 2, pool, dims, &row_bytes, box);
 }
 
 bool make_q_tmap(CUtensorMap* map, const void* q, const spg_params& p, int total_q, int rows) {
-  const auto fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t d = p.head_dim, G = p.num_q_heads / p.num_kv_heads, Hkv = p.num_kv_heads;
-  const cuuint64_t dims[4] = {d, G, Hkv, static_cast<cuuint64_t>(total_q)};
-  const cuuint64_t strides[3] = {d * 2, G * d * 2, Hkv * G * d * 2};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(rows / G)};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return fn(map, p.q_dtype == SPG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
-            const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const uint64_t d = p.head_dim, G = p.num_q_heads / p.num_kv_heads, Hkv = p.num_kv_heads;
+  const uint64_t dims[4] = {d, G, Hkv, static_cast<uint64_t>(total_q)};
+  const uint64_t strides[3] = {d * 2, G * d * 2, Hkv * G * d * 2};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(G), 1, static_cast<uint32_t>(rows / G)};
+  return encode_tmap(map, p.q_dtype == SPG_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, q,
+                     dims, strides, box);
 }
 
 }  // namespace spg
