@@ -499,6 +499,9 @@ spg_status paged_latent_append(const spg_latent_params* p, const spg_rope* rope,
 
 /* q_lat[t][h][0:r] = W_uk[h]^T q[t][h][0:dn] for every row t < total_q, sums in
  * fp32 and rounded once; channels [r, r + dr) of q_lat are left as they are.
+ * This call and latent_project have no workspace and so no error word: should a
+ * bounded wait run out (SPG_DEVERR_TIMEOUT elsewhere), the results of that part
+ * of the product are NaN.
  *   q            rows q_stride elements apart (a multiple of 8); must not overlap q_lat */
 spg_status latent_absorb(const spg_latent_params* p, int32_t total_q, const void* q,
                          int64_t q_stride, const void* w_kv, void* q_lat, spg_stream_t stream);

@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   pdl_trigger();
+  // (every role waits for the launch before ahead of its first bounded wait:
+  // however long that launch takes, none of them runs out over it)
 
   if (warp == 4) {
     if (lane == 0) {
@@ -147,6 +149,7 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
     constexpr uint32_t id = instr_desc<T>(kRowsTile, NT, ABSORB);
     const uint32_t base = smem_u32(smem);
     const auto wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase & 1)) != 0; };
+    pdl_wait();
     for (int c = 0; c < chunks; ++c) {
       const int st = c % ST, k = c % KC, n = c / KC, acc = n & 1;
       // (a tile's accumulator has been read)
@@ -176,6 +179,7 @@ __global__ void __launch_bounds__(kThreads) k_latent_heads(const __grid_constant
     // ---- a tile's rows, one a thread, to 16 bits and out ----
     uint8_t* out = smem + (a.walk > 1 ? Lay::end(a_bytes) : 0);
     const int r = threadIdx.x;
+    pdl_wait();
     for (int n = 0; n < a.walk; ++n) {
       const int acc = n & 1;
       const bool ok = mbar_wait_bounded(&done[acc], (n >> 1) & 1) && *static_cast<volatile int*>(&s_failed) == 0;

@@ -1,0 +1,83 @@
+"""Where the latent-cache operators are easily wrong, beside tests/test_gpu_latent.py."""
+
+import ctypes
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import latent_ref as R
+from test_gpu_latent import Run, close
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def spg():
+    import query_aware_sparse_page_gb300 as m
+
+    return m
+
+
+# ---- a launch before that lets the next one start at once, and then takes its time -----------------
+
+LATE_COPY = r"""
+#include <cuda_runtime.h>
+__global__ void k_late_copy(uint4* dst, const uint4* src, long long n, unsigned long long ns) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  unsigned long long t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (int i = 0; i < 1 << 20; ++i) {
+    __nanosleep(10000);
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > ns) break;
+  }
+  for (long long i = threadIdx.x; i < n; i += blockDim.x) dst[i] = src[i];
+}
+extern "C" int late_copy(void* dst, const void* src, long long bytes, unsigned long long ns, void* stream) {
+  k_late_copy<<<1, 256, 0, static_cast<cudaStream_t>(stream)>>>(static_cast<uint4*>(dst), static_cast<const uint4*>(src),
+                                                                bytes / 16, ns);
+  return cudaGetLastError();
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def late_copy(tmp_path_factory):
+    """dst = src, 250 ms later, by a launch whose dependents may start at its beginning."""
+    d = tmp_path_factory.mktemp("late")
+    (d / "late.cu").write_text(LATE_COPY)
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    subprocess.run([nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-Xcompiler", "-fPIC", "-o",
+                    str(d / "late.so"), str(d / "late.cu")], check=True)
+    fn = ctypes.CDLL(str(d / "late.so")).late_copy
+    fn.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_ulonglong, ctypes.c_void_p]
+
+    def copy(dst, src):
+        n = dst.numel() * dst.element_size()
+        assert dst.shape == src.shape and dst.dtype == src.dtype and dst.is_contiguous() and src.is_contiguous() and n % 16 == 0
+        assert fn(dst.data_ptr(), src.data_ptr(), n, 250_000_000, torch.cuda.current_stream().cuda_stream) == 0
+
+    return copy
+
+
+@pytest.mark.parametrize("H, T", [(16, 3), (130, 140)])
+def test_head_products_wait_out_a_long_launch(spg, late_copy, H, T):
+    """2.5 times as long as a bounded wait of theirs: their inputs come from that launch."""
+    c = R.Latent(H, 512, 16, "bf16", [T], [T])
+    x = Run(spg, c)
+    o = (0.1 * torch.randn(T, H, 512, generator=torch.Generator().manual_seed(T))).to(torch.bfloat16)
+    q, oc = x.q.clone(), o.cuda()
+    x.q.zero_()
+    x.o_lat.zero_()
+    torch.cuda.synchronize()
+    late_copy(x.q, q)
+    spg.latent_absorb(x.p, x.q, x.w_kv, x.q_lat)
+    late_copy(x.o_lat, oc)
+    spg.latent_project(x.p, x.o_lat, x.w_kv, x.out)
+    torch.cuda.synchronize()
+    y, tol = R.absorb(c)
+    close(x.q_lat[..., :512], y, tol, "absorb")
+    y, tol = R.project(c, o)
+    close(x.out, y, tol, "project")
