@@ -56,6 +56,7 @@
 
 #include "spg_deal.cuh"
 #include "spg_latent.h"
+#include "spg_ring.cuh"
 #include "spg_tcgen05.cuh"
 
 namespace spg {
@@ -374,7 +375,7 @@ struct Kernel {
   static __device__ void load_kv(const LatentArgs& a, M& m, uint8_t* smem, int rank, int lane) {
     const Waiter wait{a.err};
     const int per = min(a.S, kStep), copies = kStep / per;  // tokens of a copy
-    uint32_t c = 0;
+    PartRing<ST, 2> ring;
     bool ok = true;
     SegIter it(a.sh, m.plan, a.pair, rank);
     Seg s;
@@ -388,8 +389,7 @@ struct Kernel {
         return there ? (page >= 0 && page < a.n_phys ? page : -2) : -1;
       };
       int next = page_at(s.k0);
-      for (int k = s.k0; k < s.k1; ++k, ++c) {
-        const uint32_t stage = c % ST;
+      for (int k = s.k0; ok && k < s.k1; ++k) {
         const int page = next, t = k * kStep + lane * per;
         next = page_at(k + 1);
         if (page == -2) record_error(a.err, SPG_DEVERR_PAGE_ID);
@@ -404,28 +404,27 @@ struct Kernel {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint32_t group = half == 0 ? Lay::kGroupA : Lay::kGroupB;
-          if (c >= ST && !__all_sync(0xffffffffu, wait(&m.empty[stage][half], c / ST - 1))) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            // nobody reads the last step's any more: the S warp did before that step's S, the softmax warps
-            // before its P, and the first half's products, waited for above, came after both
-            if (half == 0) m.live[stage] = static_cast<uint64_t>(up) << 32 | lo;
-            mbar_arrive_expect_tx(&m.full[stage][half], n * (per / 8) * group);
-          }
-          __syncwarp();
-          if (page >= 0)
-            tma_tile_4d(smem + Lay::kv_off + stage * Lay::kStage + half * Lay::kHalfB + lane * (per / 8) * group,
-                        half == 0 ? &a.tmkv : &a.tmkv2, 0, 0, half * Lay::kBlocksA, page * (a.S / 8) + (t & (a.S - 1)) / 8,
-                        &m.full[stage][half]);
+          ok = ok && ring.put(
+              half,
+              [&](uint32_t stage, uint32_t phase) { return __all_sync(0xffffffffu, wait(&m.empty[stage][half], phase)) != 0; },
+              [&](uint32_t stage) {
+                if (lane == 0) {
+                  // nobody reads the last step's any more: the S warp did before that step's S, the softmax warps
+                  // before its P, and the first half's products, waited for above, came after both
+                  if (half == 0) m.live[stage] = static_cast<uint64_t>(up) << 32 | lo;
+                  mbar_arrive_expect_tx(&m.full[stage][half], n * (per / 8) * group);
+                }
+                __syncwarp();
+                if (page >= 0)
+                  tma_tile_4d(smem + Lay::kv_off + stage * Lay::kStage + half * Lay::kHalfB + lane * (per / 8) * group,
+                              half == 0 ? &a.tmkv : &a.tmkv2, 0, 0, half * Lay::kBlocksA, page * (a.S / 8) + (t & (a.S - 1)) / 8,
+                              &m.full[stage][half]);
+              });
         }
-        if (!ok) break;
       }
     }
     // nothing is in flight when the CTA leaves
-    for (uint32_t i = c > ST ? c - ST : 0; i < c; ++i)
-      for (int half = 0; half < 2; ++half) wait(&m.full[i % ST][half], i / ST);
+    ring.drain([&](uint32_t stage, int half, uint32_t phase) { wait(&m.full[stage][half], phase); });
   }
 
   // ---- softmax ---------------------------------------------------------------------------------------
