@@ -52,6 +52,7 @@
 // bytes, and about 7 us of start (lengths, plan, pages, first copy) and 5 of the
 // second launch.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "spg_deal.cuh"
@@ -66,7 +67,10 @@ constexpr int kRows = 64;   // rows of a CTA: columns of S^T and O^T
 constexpr int kStep = 64;   // tokens of a step
 constexpr int kRope = 64;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O^T: R / 128 times 64 columns, then two S^T of 64
-constexpr float kUnset = -1.7e38f;  // m of a row that has seen nothing: half of the range, so that any logit's distance from it is finite
+// m of a row that has seen nothing, the least finite value: any other logit is
+// above it by more than kTop (or overflows, which is above it too), and a token
+// that is not seen, -inf, is not
+constexpr float kUnset = -FLT_MAX;
 constexpr float kHead = 7.f, kTop = 15.f;  // the weights of a row are at most 2^15, under fp16's 65504
 
 // sum of floor((a i + b) / m) over 0 <= i < n, by the steps of Euclid's algorithm

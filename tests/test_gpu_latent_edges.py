@@ -1,6 +1,7 @@
 """Where the latent-cache operators are easily wrong, beside tests/test_gpu_latent.py."""
 
 import ctypes
+import math
 import shutil
 import subprocess
 
@@ -81,3 +82,42 @@ def test_head_products_wait_out_a_long_launch(spg, late_copy, H, T):
     close(x.q_lat[..., :512], y, tol, "absorb")
     y, tol = R.project(c, o)
     close(x.out, y, tol, "project")
+
+
+# ---- logits near the end of the 32-bit range ------------------------------------------------------
+
+
+@pytest.mark.parametrize("dt, q, k, scale", [("bf16", 2.0 ** 60, -(2.0 ** 67), 1.0), ("f16", 2.0 ** 10, -(2.0 ** 10), 2.0 ** 107),
+                                             ("bf16", 2.0 ** 60, 2.0 ** 67, 1.0)])
+@pytest.mark.parametrize("H, lens, new", [(4, [1, 200], [1, 3]), (70, [1, 200], [1, 3]), (4, [3000, 5], [1, 1])])
+def test_logits_near_the_end_of_the_range(spg, H, lens, new, dt, q, k, scale):
+    """Logits of 2^127 (2.5e38 in base 2) of either sign, the same for all tokens: the mean of the tokens seen.  Where they
+    are above 0, a sequence's first token has the opposite one and so no weight.
+
+    TOLERANCE.  The weights are equal and a power of two, so P is exact; the sums of L terms in 32 bits and one inverse
+    cost (2 L + 8) 2^-24 of sum p |c|, the result's rounding e |o| (fp16: and 2^-25)."""
+    c = R.Latent(H, 256, 16, dt, lens, new)
+    c.q_lat.zero_()
+    c.q_lat[..., 0] = q
+    live = ~torch.isnan(c.pool)
+    c.pool[..., 0] = k
+    c.pool[~live] = math.nan
+    first = [(int(c.page_table[b, 0]), 0) for b, L in enumerate(lens) if L > 1 and k > 0]
+    for pg, sl in first:
+        c.pool[pg, sl, 0] = -k
+    x = Run(spg, c, softmax_scale=scale)
+    x.attend()
+    assert x.err() == 0
+    want = torch.zeros((c.T, H, 256), dtype=R.F64)
+    tol = torch.zeros_like(want)
+    e = torch.finfo(R.DT[dt]).eps / 2
+    for b, L in enumerate(lens):
+        kv = c.tokens(b)[:, :256]
+        for i in range(new[b]):
+            seen = kv[1 if L > 1 and k > 0 else 0 : L - new[b] + i + 1]
+            t = c.starts[b] + i
+            want[t] = seen.mean(dim=0)
+            tol[t] = 1.01 * e * want[t].abs() + (2 * len(seen) + 8) * 2.0 ** -24 * seen.abs().mean(dim=0) + 2.0 ** -25
+    close(x.o_lat, want, tol, "o_lat")
+    z = q * k * scale
+    close(x.lse, torch.full((c.T, H), z, dtype=R.F64), torch.full((c.T, H), 2.0 ** -21 * abs(z), dtype=R.F64), "lse")
