@@ -35,7 +35,9 @@
  *     skipped and a bit (SPG_DEVERR_*) is OR-ed into the error word at the
  *     start of the workspace.  spg_read_device_error() fetches it.
  *   - The workspace must be zero-filled once after allocation; the library
- *     leaves its bookkeeping in a reusable state after every call.  After a
+ *     leaves its bookkeeping in a reusable state after every call (for calls
+ *     of which sizes: spg_chunk_workspace_size, and for the calls over latent
+ *     vectors spg_latent_workspace_size).  After a
  *     call that reported SPG_DEVERR_TIMEOUT, zero it again before reuse.
  *     Calls that share a workspace must not overlap on the GPU (order them
  *     on one stream).
@@ -301,8 +303,8 @@ spg_status dense_decode_attention(const spg_params* p, const void* q, const void
  * The selector fields of spg_params play no part here.  Cached values of
  * tokens below seq_lens must be finite; slots past it may hold anything. */
 
-/* Workspace bytes that are enough for every entry point of this header with
- * these parameters and chunks of up to total_q rows (at least
+/* Workspace bytes that are enough for every entry point of this header that
+ * takes an spg_params, with these parameters and chunks of up to total_q rows (at least
  * spg_workspace_size).  A workspace keeps its bookkeeping where the sizes in
  * spg_params put it: total_q and the selector's fields may vary from call to
  * call (on a workspace that is enough for each), but for another batch, head
@@ -470,9 +472,15 @@ typedef struct spg_latent_params {
 spg_status spg_latent_validate(const spg_latent_params* p);
 
 /* Workspace bytes for the two paged_latent_* entry points with these
- * parameters and chunks of up to total_q rows.  The workspace keeps nothing
- * between calls but the error word (see spg_read_device_error), so one that is
- * large enough serves any parameters.  Host only. */
+ * parameters and chunks of up to total_q rows.  These calls use the error word
+ * (see spg_read_device_error) and that many bytes at the END of the workspace
+ * they are given, keep nothing there from call to call and do not leave it
+ * zero.  So a workspace that is large enough serves latent calls of any
+ * parameters.  To share one with the entry points that take an spg_params,
+ * give it spg_chunk_workspace_size + spg_latent_workspace_size bytes (the
+ * largest of each) and pass its whole size to all of them; on a smaller one
+ * latent calls overwrite counters that those calls need, and the workspace has
+ * to be zeroed between a latent call and one of those.  Host only. */
 spg_status spg_latent_workspace_size(const spg_latent_params* p, int32_t total_q, size_t* bytes);
 
 /* A chunk's latent vectors and rotary keys into the cache, and the rotated part

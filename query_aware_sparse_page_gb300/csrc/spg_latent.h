@@ -33,6 +33,6 @@ cudaError_t launch_latent_heads(const spg_latent_params& p, bool project, int to
                                 const void* w_kv, void* y, cudaStream_t stream);
 size_t latent_workspace_bytes(const spg_latent_params& p, int total_q);
 cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows& r, const void* q_lat, const void* pool,
-                                    void* o_lat, float* lse, int parts, void* ws, cudaStream_t stream);
+                                    void* o_lat, float* lse, int parts, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 }  // namespace spg

@@ -138,7 +138,7 @@ spg_status paged_latent_attention(const spg_latent_params* p, int32_t total_q, c
     return SPG_EINVAL;
   const spg::LatentRows r{q_start, page_table, seq_lens, total_q};
   return cuda_status(spg::launch_latent_attention(*p, r, q_lat, pool, o_lat, lse, spg::chunk_parts(), ws,
-                                                  reinterpret_cast<cudaStream_t>(stream)));
+                                                  ws_bytes, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -867,12 +867,16 @@ cudaError_t latent_typed(const spg_latent_params& p, LatentArgs& a, const void* 
 
 }  // namespace
 
-size_t latent_workspace_bytes(const spg_latent_params& p, int total_q) {
-  return 256 + sizeof(PartRecord) * kSlots + sizeof(float2) * kSlots * kRows + sizeof(float) * kSlots * part_rows(p, total_q) * p.latent_dim;
+namespace {
+size_t scratch_bytes(const spg_latent_params& p, int total_q) {
+  return sizeof(PartRecord) * kSlots + sizeof(float2) * kSlots * kRows + sizeof(float) * kSlots * part_rows(p, total_q) * p.latent_dim;
 }
+}  // namespace
+
+size_t latent_workspace_bytes(const spg_latent_params& p, int total_q) { return 256 + scratch_bytes(p, total_q); }
 
 cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows& r, const void* q_lat, const void* pool,
-                                    void* o_lat, float* lse, int parts, void* ws, cudaStream_t stream) {
+                                    void* o_lat, float* lse, int parts, void* ws, size_t ws_bytes, cudaStream_t stream) {
   LatentArgs a{};
   a.sh.q_start = r.q_start;
   a.sh.seq_lens = r.seq_lens;
@@ -890,7 +894,10 @@ cudaError_t launch_latent_attention(const spg_latent_params& p, const LatentRows
   a.lse = lse;
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.err = reinterpret_cast<int32_t*>(base);
-  a.record = reinterpret_cast<PartRecord*>(base + 256);
+  // What is left here is not zero, and other entry points keep counters that
+  // have to be, where their sizes put them from the workspace's start on: so
+  // this stands at its end, behind them where there is room for both.
+  a.record = reinterpret_cast<PartRecord*>(base + ((ws_bytes - scratch_bytes(p, r.total_q)) & ~static_cast<size_t>(255)));
   a.part_ml = reinterpret_cast<float2*>(a.record + kSlots);
   a.part = reinterpret_cast<float*>(a.part_ml + kSlots * kRows);
   a.S = p.page_size;

@@ -9,6 +9,10 @@ import pytest
 import torch
 
 import latent_ref as R
+import paged_ref
+import test_gpu_latent as latent
+import test_gpu_paged as paged
+from synth import get_workload, make_inputs, scaled
 from test_gpu_latent import Run, close
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +125,67 @@ def test_logits_near_the_end_of_the_range(spg, H, lens, new, dt, q, k, scale):
     close(x.o_lat, want, tol, "o_lat")
     z = q * k * scale
     close(x.lse, torch.full((c.T, H), z, dtype=R.F64), torch.full((c.T, H), 2.0 ** -21 * abs(z), dtype=R.F64), "lse")
+
+
+# ---- a workspace that other entry points use as well ----------------------------------------------
+
+
+@pytest.mark.parametrize("slack", [0, 16, 1000 * 16])
+def test_a_workspace_shared_with_the_other_entry_points(spg, slack):
+    """Latent calls in between chunk attention, attention mass and decode steps (each in its kernels), on one workspace of
+    both sizes together: everything as on workspaces of their own, and the other calls' part as they left it."""
+    w = scaled(get_workload("tiny-quest-gqa4-1k"))
+    inp = make_inputs(w, device="cuda")
+    p = spg.params_for(inp)
+    b = spg.alloc_buffers(p, "cuda")
+    ch = paged.Run(spg, paged_ref.Chunk(8, 2, 128, 64, "bf16", "bf16", [3000, 900], [2, 200]))
+    few = latent.Run(spg, R.Latent(64, 512, 64, "bf16", [3000, 900], [1, 4], seed=1))
+    many = latent.Run(spg, R.Latent(128, 256, 16, "f16", [2000], [2], seed=2))
+    mass = torch.zeros((2, 2, ch.page_table.shape[1] * 64), device="cuda")
+    spg.sparse_page_meta_update(p, inp.k_pool, None, inp.page_table, inp.seq_lens, 1, b.minmax, None, None, None, b.ws)
+
+    def step(kernel, ws):
+        spg.spg_set_step_kernel(kernel)
+        try:
+            spg.sparse_decode_select_attend(p, inp.q, inp.k_pool, inp.v_pool, None, None, inp.page_table, inp.seq_lens, b.minmax,
+                                            None, None, None, b.sel, b.sel_cnt, b.out, b.lse, ws)
+        finally:
+            spg.spg_set_step_kernel(0)
+        return b.out.clone(), b.lse.clone(), b.sel.clone()
+
+    def chunk(ws):
+        ch.ws = ws
+        ch.out.fill_(7.0)
+        ch.chunk()
+        ch.mass(ch.lse, None, mass, 1.0)
+        return ch.out.clone(), ch.lse.clone(), mass.clone()
+
+    def attend(x, ws):
+        x.ws = ws
+        x.o_lat.fill_(7.0)
+        x.attend()
+        return x.o_lat.clone(), x.lse.clone()
+
+    # both geometries' calls on their own workspaces, and a workspace per geometry shared with the latent ones
+    calls = [lambda ws: step(1, ws[0]), lambda ws: attend(few, ws[0]), lambda ws: step(2, ws[0]), lambda ws: attend(many, ws[0]),
+             lambda ws: step(1, ws[0]), lambda ws: chunk(ws[1]), lambda ws: attend(few, ws[1]), lambda ws: chunk(ws[1]),
+             lambda ws: attend(many, ws[1]), lambda ws: chunk(ws[1])]
+    zeros = lambda n: torch.zeros(n, dtype=torch.uint8, device="cuda")  # noqa: E731
+    n_step, n_chunk = spg.spg_workspace_size(p), spg.spg_chunk_workspace_size(ch.p, ch.c.T)
+    n_latent = max(spg.spg_latent_workspace_size(x.p, x.c.T) for x in (few, many))
+    want = []
+    for i, f in enumerate(calls):
+        own = [zeros(n_latent if i in (1, 3) else n_step), zeros(n_latent if i in (6, 8) else n_chunk)]
+        want.append(f(own))
+    shared = [zeros(n_step + n_latent + slack), zeros(n_chunk + n_latent + slack)]
+    for _ in range(3):
+        for i, f in enumerate(calls):
+            rest = shared[0 if i < 5 else 1][: n_step if i < 5 else n_chunk]
+            before = rest.clone()
+            got = f(shared)
+            if i in (1, 3, 6, 8):
+                assert torch.equal(rest, before)
+            for x, y in zip(got, want[i]):
+                assert torch.equal(x, y)
+    for ws in shared:
+        assert spg.spg_read_device_error(ws) == 0
