@@ -8,6 +8,7 @@ import subprocess
 import pytest
 import torch
 
+import latent_exact as X
 import latent_ref as R
 import paged_ref
 import test_gpu_latent as latent
@@ -125,6 +126,29 @@ def test_logits_near_the_end_of_the_range(spg, H, lens, new, dt, q, k, scale):
     close(x.o_lat, want, tol, "o_lat")
     z = q * k * scale
     close(x.lse, torch.full((c.T, H), z, dtype=R.F64), torch.full((c.T, H), 2.0 ** -21 * abs(z), dtype=R.F64), "lse")
+
+
+# ---- exact logits ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("H, r, lens, new", X.CASES)
+def test_exact_logits_show_both_values_of_p(spg, H, r, lens, new, dt):
+    """Within a tolerance that one value of P, or a second one of the wrong sign or place, does not keep (the model in
+    tests/test_latent_exact_host.py); with one value within that one's, and not the same."""
+    c = X.chunk(H, r, lens, new, dt)
+    x = Run(spg, c, softmax_scale=X.SCALE)
+    got = {}
+    for parts in (1, 2):
+        try:
+            spg.spg_set_chunk_parts(parts)
+            x.attend()
+        finally:
+            spg.spg_set_chunk_parts(2)
+        assert x.err() == 0
+        close(x.o_lat, *X.attention(c, parts), f"o_lat, {parts}")
+        got[parts] = x.o_lat.clone()
+    assert not torch.equal(got[1], got[2])
 
 
 # ---- a workspace that other entry points use as well ----------------------------------------------
