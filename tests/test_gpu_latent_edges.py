@@ -89,6 +89,32 @@ def test_head_products_wait_out_a_long_launch(spg, late_copy, H, T):
     close(x.out, y, tol, "project")
 
 
+# ---- head products at the borders of their forms -------------------------------------------------
+
+
+@pytest.mark.parametrize("H, r, dn, dv, T", [
+    # 32 columns a CTA up to 32 rows, 64 up to 128, then tiles of 128 rows
+    (4, 512, 128, 128, 31), (4, 256, 64, 64, 32), (4, 512, 128, 128, 33), (3, 256, 128, 128, 64), (3, 512, 64, 128, 257),
+    # absorbing with one CTA for all columns: rows' tiles times heads from as many as there are SMs on
+    (130, 256, 64, 64, 140), (130, 512, 64, 128, 129), (151, 256, 64, 64, 1), (152, 512, 64, 64, 1), (152, 256, 128, 64, 2),
+    (200, 512, 128, 64, 1), (200, 256, 64, 128, 5), (200, 512, 64, 64, 33), (1024, 256, 64, 64, 1), (1024, 256, 64, 64, 3),
+])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_head_products_at_borders(spg, H, r, dn, dv, T, dt):
+    c = R.Latent(H, r, 16, dt, [T], [T], dn=dn, dv=dv, pad_rows=3)
+    x = Run(spg, c)
+    x.q_lat.fill_(5.0)
+    spg.latent_absorb(x.p, x.q[:T], x.w_kv, x.q_lat[:T])
+    y, tol = R.absorb(c)
+    close(x.q_lat[:T, :, :r], y[:T], tol[:T], "absorb")
+    assert bool((x.q_lat[..., r:] == 5.0).all()) and bool((x.q_lat[T:] == 5.0).all())
+    o = (0.1 * torch.randn(T + 3, H, r, generator=torch.Generator().manual_seed(T))).to(R.DT[dt])
+    spg.latent_project(x.p, o.cuda()[:T], x.w_kv, x.out[:T])
+    y, tol = R.project(c, o)
+    close(x.out[:T], y[:T], tol[:T], "project")
+    assert bool((x.out[T:] == 7.0).all())
+
+
 # ---- logits near the end of the 32-bit range ------------------------------------------------------
 
 
