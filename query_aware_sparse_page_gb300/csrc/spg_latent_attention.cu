@@ -363,13 +363,7 @@ struct Kernel {
       if (c > 0 && !wait(&m.q_empty, c - 1)) break;
       const int groups = columns(s) / 8, row = s.sq.start * a.sh.H + s.row0;
       mbar_arrive_expect_tx(&m.q_full, groups * Lay::kGroupQ);
-      for (int g = 0; g < groups; ++g) {
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                smem_u32(smem + Lay::q_off + g * Lay::kGroupQ)),
-            "l"(reinterpret_cast<uint64_t>(&a.tmq)), "r"(0), "r"(row + 8 * g), "r"(0), "r"(smem_u32(&m.q_full))
-            : "memory");
-      }
+      for (int g = 0; g < groups; ++g) tma_tile_3d(smem + Lay::q_off + g * Lay::kGroupQ, &a.tmq, 0, row + 8 * g, 0, &m.q_full);
       ++c;
     }
     if (c > 0) wait(&m.q_full, c - 1);  // nothing is in flight when the CTA leaves
@@ -719,7 +713,7 @@ __global__ void __launch_bounds__(384, 1) k_latent(const __grid_constant__ Laten
   } else if (warp == K::kQWarp) {
     if (lane == 0) K::load_q(a, m, smem, rank);
     __syncwarp();
-  } else if (warp != K::kLoadWarp) {
+  } else {
     const bool ok = warp == K::kSWarp ? K::issue_s(a, m, smem, tmem, rank, lane) : K::issue_pv(a, m, smem, tmem, rank);
     if (!ok) {  // products in flight end before TMEM goes back
       uint64_t* bar = &m.drain[warp - K::kSWarp];
