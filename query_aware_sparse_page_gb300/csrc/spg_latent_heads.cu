@@ -247,9 +247,18 @@ cudaError_t heads_typed(const spg_latent_params& p, int total_q, const void* x, 
   a.w_row = ABSORB ? 0 : p.nope_dim;
   a.n_tiles = static_cast<int>(N / NT);
   const long long row_tiles = (static_cast<long long>(total_q) + kRowsTile - 1) / kRowsTile;
-  // every SM has a CTA of its own without splitting the columns
-  a.walk = ABSORB && row_tiles * p.num_heads >= device_sm_count() ? a.n_tiles : 1;
-  // few rows straight from the registers (16 rows of 128 heads: 7.2 against 7.9 us by way of shared memory)
+  // One CTA for all columns of its rows where every SM has one so, and there
+  // are rows enough for reading them once to pay: up to 16 rows the columns stay
+  // apart (r 512, 1 and 16 rows; apart against walked: 152 heads 5.0 and 5.4
+  // against 7.0 and 7.5 us, 192 heads 7.7 and 8.2 against 7.9 and 8.4, 256 heads
+  // 9.0 and 9.5 against 8.6 and 9.2, 1024 heads 26.4 and 28.8 against 30.4 and
+  // 32.8; 32 rows of 256 heads 11.9 against 10.0, 128 rows of 192 heads 18.9
+  // against 13.3, 640 rows of 32 heads 12.9 against 12.0).
+  constexpr int kApart = 16;
+  a.walk = ABSORB && total_q > kApart && row_tiles * p.num_heads >= device_sm_count() ? a.n_tiles : 1;
+  // rows of one tile straight from the registers, and no more of them copied than there are (16 rows absorbed: 128 heads 5.1
+  // against 8.3 us by way of shared memory with a whole tile, 16 heads 3.0 against 3.4; 33 to 128 rows projected: 16 heads
+  // 4.4 to 5.7 against 4.7 to 5.5, 128 heads 7.8 to 10.2 against 6.7 to 9.5)
   a.few = a.walk == 1 && total_q <= kRowsTile ? total_q : 0;
   a.rows = a.few ? (a.few + 7) & ~7 : kRowsTile;
   a.y = y;
@@ -273,8 +282,10 @@ cudaError_t heads_typed(const spg_latent_params& p, int total_q, const void* x, 
 template <typename T, int KC>
 cudaError_t project_typed(const spg_latent_params& p, int total_q, const void* x, int64_t x_stride, const void* w, void* y,
                           cudaStream_t st) {
-  // few rows: all chunks on their way at once (16 rows of 128 heads 6.3 us; with four or three in flight 7.3 and 8.1), 32
-  // columns a CTA (64: 6.3, 32: 6.0)
+  // few rows: all chunks on their way at once, 32 columns a CTA; else three in flight, 64 columns.  Measured both ways (r 512,
+  // dv 128; first this one): 16 heads 1 row 3.7 / 4.0 us, 32 rows 4.1 / 4.4, 33 rows 4.1 / 4.4, 128 rows 4.5 / 5.7; 32 heads
+  // 4.3 / 4.8, 4.7 / 5.0, 4.7 / 5.1, 4.9 / 6.3; 128 heads (more CTAs than fit at once) 6.4 / 7.8, 16 rows 6.0 / 8.2, 32 rows
+  // 9.0 / 7.6, 33 rows 9.1 / 7.8, 128 rows 18.9 / 10.2: the border is between the two.
   if (total_q <= 32) return heads_typed<T, KC, 32, KC, false>(p, total_q, x, x_stride, w, y, st);
   // 64 columns a CTA while one tile has all rows (twice the CTAs for the matrices' bytes)
   if (p.v_dim == 64 || total_q <= kRowsTile) return heads_typed<T, KC, 64, 3, false>(p, total_q, x, x_stride, w, y, st);

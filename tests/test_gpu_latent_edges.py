@@ -95,8 +95,8 @@ def test_head_products_wait_out_a_long_launch(spg, late_copy, H, T):
 @pytest.mark.parametrize("H, r, dn, dv, T", [
     # 32 columns a CTA up to 32 rows, 64 up to 128, then tiles of 128 rows
     (4, 512, 128, 128, 31), (4, 256, 64, 64, 32), (4, 512, 128, 128, 33), (3, 256, 128, 128, 64), (3, 512, 64, 128, 257),
-    # absorbing with one CTA for all columns: rows' tiles times heads from as many as there are SMs on
-    (130, 256, 64, 64, 140), (130, 512, 64, 128, 129), (151, 256, 64, 64, 1), (152, 512, 64, 64, 1), (152, 256, 128, 64, 2),
+    # absorbing with one CTA for all columns: more than 16 rows, their tiles times heads from as many as there are SMs on
+    (152, 512, 128, 64, 16), (152, 512, 128, 64, 17), (130, 256, 64, 64, 140), (130, 512, 64, 128, 129), (151, 256, 64, 64, 1), (152, 512, 64, 64, 1), (152, 256, 128, 64, 2),
     (200, 512, 128, 64, 1), (200, 256, 64, 128, 5), (200, 512, 64, 64, 33), (1024, 256, 64, 64, 1), (1024, 256, 64, 64, 3),
 ])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
