@@ -47,9 +47,9 @@ STEP_SOURCES = ("spg_append.cuh", "spg_attn_core.cuh", "spg_common.cuh", "spg_fu
                 "spg_select_core.cuh", "spg_tma.cu")
 NCU_TRAFFIC = {
     # workload: (DRAM bytes of one launch, code hash, kernel)
-    "llama2-7b-mha-32k": (67_643_136, "12213080c09be11eb4c9bb6ec5fab787dca4f695b378f79d23cb60e97be57597", "k_fused"),
-    "long-scan-b4-128k": (205_023_488, "12213080c09be11eb4c9bb6ec5fab787dca4f695b378f79d23cb60e97be57597", "k_fused"),
-    "sals-int8-b16-10k-4x": (100_351_232, "12213080c09be11eb4c9bb6ec5fab787dca4f695b378f79d23cb60e97be57597", "k_fused"),
+    "llama2-7b-mha-32k": (67_753_472, "8a8b8e9f8c496a7ade5e5223bc712719084be87c21dc14de39c69056496a99b7", "k_fused"),
+    "long-scan-b4-128k": (204_997_632, "8a8b8e9f8c496a7ade5e5223bc712719084be87c21dc14de39c69056496a99b7", "k_fused"),
+    "sals-int8-b16-10k-4x": (100_298_240, "8a8b8e9f8c496a7ade5e5223bc712719084be87c21dc14de39c69056496a99b7", "k_fused"),
 }
 
 
