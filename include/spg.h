@@ -495,7 +495,11 @@ spg_status spg_latent_workspace_size(const spg_latent_params* p, int32_t total_q
  *   q            rows q_stride elements apart (a multiple of 8); q and q_lat
  *                may both be NULL, and must not overlap
  *   rope, positions  as in paged_rope_append, over the dr channels (rot_dim 0
- *                or a multiple of 16 up to dr; NULL leaves k_pe and q as they are)
+ *                or a multiple of 16 up to dr; NULL leaves k_pe and q as they are).
+ *                YARN's factor m = 0.1 ln(factor) + 1 is on k_pe and on q: the
+ *                rotary part of a logit has m^2, the rest has not.  For a model
+ *                with m^2 on the whole logit, softmax_scale takes it, and 1 / m
+ *                belongs into the projections that make k_pe and q's dr channels
  * Channels [0, r) of q_lat are left to latent_absorb. */
 spg_status paged_latent_append(const spg_latent_params* p, const spg_rope* rope, int32_t total_q,
                                const void* c, int64_t c_stride, const void* k_pe,

@@ -15,8 +15,9 @@
 // and has the 32 pairs' cos and sin in its lanes; the values are on their way
 // before the position is known (8192 tokens: 20 us, 23 the other way round).
 //
-// Measured (GB300): 8192 tokens of 32 heads, 86 MB: 20 us, 4.3 TB/s (pieces of
-// 128 bytes at a stride, of q and of q_lat); 16 tokens: 2.3 us back to back.
+// Measured (GB300): 8192 tokens of 32 heads, 86 MB: 20 us, 4.3 TB/s (a copy of
+// the same bytes, the queries' pieces of 128 bytes at a stride and the rows in
+// two launches: 12.8 + 4.4 us); 16 tokens: 2.3 us back to back.
 #include <cmath>
 
 #include "spg_chunk_common.cuh"
